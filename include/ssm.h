@@ -69,7 +69,14 @@ typedef enum {
   SSM_ERR_HIP = 9          /* a HIP call failed; see ssm_last_hip_error()     */
 } ssm_status;
 
-typedef enum { SSM_F32 = 0, SSM_BF16 = 1, SSM_F16 = 2 /* reserved */ } ssm_dtype;
+typedef enum {
+  SSM_F32 = 0,
+  SSM_BF16 = 1,
+  SSM_F16 = 2, /* reserved */
+  SSM_E4M3 = 3, /* 8-bit float, 4 exponent bits, largest 448, no infinities (norm output) */
+  SSM_I32 = 4,  /* sequence lengths (gated scan) */
+  SSM_U8 = 5    /* packed 4-bit weights and their zero points */
+} ssm_dtype;
 
 typedef struct {
   int32_t dtype; /* ssm_dtype */
@@ -91,6 +98,13 @@ typedef struct {
 #define SSM_WANT_CKPT 512u     /* scan: also write the state before every 16-step tile */
 #define SSM_HAS_CKPT 1024u     /* scan backward: read those states, do not recompute them */
 #define SSM_HAS_SSD_FWD 2048u  /* SSD backward: read the forward's A_cum, beta and chunk states */
+#define SSM_HAS_BIAS_A 4096u   /* gated scan: add bias_a[d] to gate_a                 */
+#define SSM_HAS_BIAS_X 8192u   /* gated scan: add bias_x[d] to gate_x                 */
+#define SSM_HAS_LENS 16384u    /* gated scan: lens[b] steps of row b count            */
+#define SSM_HAS_DHLAST 32768u  /* gated scan backward: gradient of h_last             */
+#define SSM_HAS_RESIDUAL 65536u /* norm: add a residual (backward: add its gradient)  */
+#define SSM_HAS_ZERO 131072u   /* 4-bit weights: zero points                          */
+#define SSM_HAS_STATE_OUT 262144u /* gated decode: write the state to state_out       */
 
 /* ------------------------------------------------------------------ scan */
 
@@ -388,6 +402,252 @@ typedef struct {
   void* y;
 } ssm_conv_ptrs;
 
+/* ---------------------------------------------- gated linear recurrence */
+
+/* Gated linear recurrence: one fp32 state per channel, a decay and an input
+ * gate computed from the token.  For every batch element b and channel d,
+ *      r_t = sigmoid(gate_a[b,t,d] + bias_a[d])
+ *      i_t = sigmoid(gate_x[b,t,d] + bias_x[d])
+ *      a_t = exp(A[d] r_t)
+ *      s_t = sqrt(max(0, 1 - a_t^2))
+ *      h_t = a_t h_{t-1} + s_t i_t x[b,t,d]          h starts at h0 or 0
+ *      y[b,t,d] = h_t * silu(z[b,t,d])               (h_t without SSM_HAS_Z)
+ * A is real, normally negative (exp(A) is the decay at an open gate); s_t
+ * keeps the state's variance at the input's.  The recurrence is evaluated in
+ * fp32; 1 - a_t^2 keeps its relative accuracy for decays near 1.
+ * Lengths: with SSM_HAS_LENS row b counts lens[b] steps, taken into
+ * [0, seqlen] by the kernel: later steps leave the state as it is (h_last is
+ * the state after step lens[b] - 1, or h0), their inputs have no influence,
+ * whatever they hold, and their y (and gradients) are zeros.
+ * Tensors (shape, dtype):
+ *   x, gate_a, gate_x : (batch, seqlen, dim)  io     innermost stride 1
+ *   z        : (batch, seqlen, dim)  io              if SSM_HAS_Z, innermost stride 1
+ *   y        : (batch, seqlen, dim)  io or F32       innermost stride 1
+ *   A        : (dim) F32                             any stride (0 = shared)
+ *   bias_a, bias_x : (dim) F32                       if SSM_HAS_BIAS_A / SSM_HAS_BIAS_X, any stride
+ *   h0       : (batch, dim) F32 contiguous           if SSM_HAS_H0
+ *   h_last   : (batch, dim) F32 contiguous           if SSM_WANT_HLAST
+ *   lens     : (batch) I32 contiguous                if SSM_HAS_LENS
+ *   ckpt     : (batch, ceil(seqlen/64), dim) F32 contiguous   if SSM_WANT_CKPT:
+ *              ckpt[b, k] = the state before step 64k, as ssm_gated_scan_bwd
+ *              takes it with SSM_HAS_CKPT
+ * io is SSM_F32 or SSM_BF16 and is the same for x, gate_a, gate_x, z.
+ * Other flags are not accepted.  Outputs may not overlap inputs or each other.
+ * Limit: 256 rows of any (batch, seqlen, dim) tensor must span less than
+ * 1 GiB (SSM_ERR_UNSUPPORTED otherwise). */
+#define SSM_GATED_CKPT_STEPS 64
+
+typedef struct {
+  int64_t batch, seqlen, dim;
+  uint32_t flags;
+  ssm_tensor_desc x, gate_a, gate_x, A, bias_a, bias_x, z, y, h0, h_last, lens, ckpt;
+} ssm_gated_desc;
+
+typedef struct {
+  const void* x;
+  const void* gate_a;
+  const void* gate_x;
+  const float* A;
+  const float* bias_a;  /* NULL unless SSM_HAS_BIAS_A */
+  const float* bias_x;  /* NULL unless SSM_HAS_BIAS_X */
+  const void* z;        /* NULL unless SSM_HAS_Z      */
+  void* y;
+  const float* h0;      /* NULL unless SSM_HAS_H0     */
+  float* h_last;        /* NULL unless SSM_WANT_HLAST */
+  const int32_t* lens;  /* NULL unless SSM_HAS_LENS   */
+  float* ckpt;          /* NULL unless SSM_WANT_CKPT  */
+} ssm_gated_ptrs;
+
+/* Backward of the gated scan: given the forward's inputs, dy = dLoss/dy and
+ * optionally dh_last = dLoss/dh_last,
+ *   g_t   = dy_t silu(z_t) (dy_t without SSM_HAS_Z), dz_t = dy_t h_t silu'(z_t)
+ *   lam_t = g_t + a_{t+1} lam_{t+1}      (past the last counted step: dh_last or 0)
+ *   du_t  = lam_t (a_t h_{t-1} - i_t x_t a_t^2 / s_t)    (u_t = A r_t; the second
+ *           term is 0 where s_t is 0)
+ *   dA    = sum du_t r_t;   dgate_a_t = du_t A r_t (1 - r_t);   dbias_a = sum dgate_a_t
+ *   dx_t  = lam_t s_t i_t;  dgate_x_t = lam_t s_t x_t i_t (1 - i_t);  dbias_x = sum dgate_x_t
+ *   dh0   = a_0 lam_0
+ * Tensors (shape, dtype): the forward's inputs as in ssm_gated_desc, and
+ *   dy, dx, dgate_a, dgate_x : (batch, seqlen, dim)   innermost stride 1
+ *   dz       : (batch, seqlen, dim)                   if SSM_HAS_Z, innermost stride 1
+ *              these five all io or all F32
+ *   dh_last  : (batch, dim) F32 contiguous            if SSM_HAS_DHLAST
+ *   dA       : (dim) F32 contiguous
+ *   dbias_a, dbias_x : (dim) F32 contiguous           if SSM_HAS_BIAS_A / SSM_HAS_BIAS_X
+ *   dh0      : (batch, dim) F32 contiguous            if SSM_HAS_H0
+ *   ckpt     : the forward's checkpoints of the same inputs, read only, if
+ *              SSM_HAS_CKPT; without the flag they are recomputed in the workspace
+ * The sums over batch and time are fp32 partial sums added in a fixed order,
+ * so the results are deterministic.  Outputs may not overlap inputs or each
+ * other.  Workspace: ssm_gated_scan_bwd_workspace_size bytes, 256-byte
+ * aligned.  Limit: the forward's span limit. */
+typedef struct {
+  int64_t batch, seqlen, dim;
+  uint32_t flags;
+  ssm_tensor_desc x, gate_a, gate_x, A, bias_a, bias_x, z, h0, lens, ckpt, dy, dh_last;
+  ssm_tensor_desc dx, dgate_a, dgate_x, dz, dA, dbias_a, dbias_x, dh0;
+} ssm_gated_bwd_desc;
+
+typedef struct {
+  const void* x;
+  const void* gate_a;
+  const void* gate_x;
+  const float* A;
+  const float* bias_a;   /* NULL unless SSM_HAS_BIAS_A  */
+  const float* bias_x;   /* NULL unless SSM_HAS_BIAS_X  */
+  const void* z;         /* NULL unless SSM_HAS_Z       */
+  const float* h0;       /* NULL unless SSM_HAS_H0      */
+  const int32_t* lens;   /* NULL unless SSM_HAS_LENS    */
+  const float* ckpt;     /* NULL unless SSM_HAS_CKPT    */
+  const void* dy;
+  const float* dh_last;  /* NULL unless SSM_HAS_DHLAST  */
+  void* dx;
+  void* dgate_a;
+  void* dgate_x;
+  void* dz;              /* NULL unless SSM_HAS_Z       */
+  float* dA;
+  float* dbias_a;        /* NULL unless SSM_HAS_BIAS_A  */
+  float* dbias_x;        /* NULL unless SSM_HAS_BIAS_X  */
+  float* dh0;            /* NULL unless SSM_HAS_H0      */
+} ssm_gated_bwd_ptrs;
+
+/* One step of the gated recurrence (autoregressive decode): equals
+ * ssm_gated_scan_fwd with seqlen 1, h0 = state.
+ *   x, gate_a, gate_x, z : (batch, dim) io   innermost stride 1 (z if SSM_HAS_Z)
+ *   y         : (batch, dim) io or F32       innermost stride 1
+ *   A, bias_a, bias_x    : as in the scan
+ *   state     : (batch, dim) F32 contiguous, read and overwritten; with
+ *               SSM_HAS_STATE_OUT only read, and
+ *   state_out : (batch, dim) F32 contiguous takes the new state
+ * Outputs may not overlap inputs (but state, in place) or each other. */
+typedef struct {
+  int64_t batch, dim;
+  uint32_t flags;
+  ssm_tensor_desc x, gate_a, gate_x, A, bias_a, bias_x, z, y, state, state_out;
+} ssm_gated_update_desc;
+
+typedef struct {
+  const void* x;
+  const void* gate_a;
+  const void* gate_x;
+  const float* A;
+  const float* bias_a;  /* NULL unless SSM_HAS_BIAS_A    */
+  const float* bias_x;  /* NULL unless SSM_HAS_BIAS_X    */
+  const void* z;        /* NULL unless SSM_HAS_Z         */
+  void* y;
+  float* state;         /* only read with SSM_HAS_STATE_OUT */
+  float* state_out;     /* NULL unless SSM_HAS_STATE_OUT */
+} ssm_gated_update_ptrs;
+
+/* ------------------------------------------------------------------ norm */
+
+/* Root-mean-square norm of every row (one token's dim values), with the
+ * residual's addition in front of it:
+ *      row = x + residual                (rounded to residual_out's type; x
+ *                                         itself without SSM_HAS_RESIDUAL)
+ *      y   = weight * row / sqrt(mean(row^2) + eps)
+ * The mean and the scaling are fp32.  The norm is taken of the row as
+ * residual_out stores it, so that the backward sees the same row.
+ * An E4M3 output is quantised by `group` consecutive columns (0: the whole
+ * row; the last group of a row may be shorter):
+ *      scale = max(amax(|y|) / 448, 2^-126),   y8 = y / scale (nearest even)
+ * The amax passes over NaN, as fmax does; a NaN is stored as NaN.
+ * Tensors (shape, dtype):
+ *   x        : (batch, seqlen, dim) io                innermost stride 1
+ *   residual : (batch, seqlen, dim) io or F32         if SSM_HAS_RESIDUAL, innermost stride 1
+ *   residual_out : (batch, seqlen, dim) io or F32     if SSM_HAS_RESIDUAL, innermost stride 1;
+ *              the same memory, type and strides as residual are allowed
+ *   weight   : (dim) F32 contiguous
+ *   y        : (batch, seqlen, dim) io, F32 or E4M3   innermost stride 1
+ *   scale    : (batch, seqlen, ceil(dim/group)) F32 contiguous ((batch, seqlen, 1) with
+ *              group 0)                               if y is E4M3
+ * io is SSM_F32 or SSM_BF16.  group: 0, 32, 64 or 128 (0 unless y is E4M3).
+ * dim <= SSM_NORM_MAX_DIM.  eps >= 0.  Outputs may not overlap inputs (but
+ * residual_out, above) or each other. */
+#define SSM_NORM_MAX_DIM 16384
+
+typedef struct {
+  int64_t batch, seqlen, dim, group;
+  float eps;
+  uint32_t flags;
+  ssm_tensor_desc x, residual, weight, y, residual_out, scale;
+} ssm_norm_desc;
+
+typedef struct {
+  const void* x;
+  const void* residual; /* NULL unless SSM_HAS_RESIDUAL */
+  const float* weight;
+  void* y;
+  void* residual_out;   /* NULL unless SSM_HAS_RESIDUAL */
+  float* scale;         /* NULL unless y is E4M3        */
+} ssm_norm_ptrs;
+
+/* Backward of the norm: row is what was normalised (residual_out, or x),
+ * dres (SSM_HAS_RESIDUAL) the gradient that reaches residual_out besides:
+ *      hat = row * rstd,  rstd = 1 / sqrt(mean(row^2) + eps)
+ *      dx  = rstd (weight dy - hat mean(weight dy hat)) + dres
+ *      dweight = sum over rows of dy hat
+ * dx is the gradient of x and of residual alike.  A quantised output's
+ * gradient is taken straight through.
+ *   dy, dx  : (batch, seqlen, dim) F32 or BF16          innermost stride 1
+ *   row     : (batch, seqlen, dim) F32 or BF16          innermost stride 1
+ *   dres    : (batch, seqlen, dim) F32 or BF16          if SSM_HAS_RESIDUAL, innermost stride 1
+ *   weight  : (dim) F32 contiguous
+ *   dweight : (dim) F32 contiguous
+ * dweight is a fixed-order sum of per-workgroup fp32 partial sums
+ * (deterministic).  Workspace: ssm_rms_norm_bwd_workspace_size bytes,
+ * 256-byte aligned.  dim and eps as in the forward; outputs may not overlap
+ * inputs or each other. */
+typedef struct {
+  int64_t batch, seqlen, dim;
+  float eps;
+  uint32_t flags;
+  ssm_tensor_desc dy, row, weight, dres, dx, dweight;
+} ssm_norm_bwd_desc;
+
+typedef struct {
+  const void* dy;
+  const void* row;
+  const float* weight;
+  const void* dres; /* NULL unless SSM_HAS_RESIDUAL */
+  void* dx;
+  float* dweight;
+} ssm_norm_bwd_ptrs;
+
+/* --------------------------------------------------------- 4-bit weights */
+
+/* Product of a few rows (decode tokens) with a matrix of 4-bit weights:
+ *      y[m,n] = sum_k x[m,k] (q[n,k] - zero[n,k/group]) scale[n,k/group] + bias[n]
+ * q[n,k] is the low (k even) or high (k odd) half of byte weight[n, k/2], 0..15;
+ * zero is 8 without SSM_HAS_ZERO.  Products are bf16 matrix-core products of
+ * x with q + 16 (exact in bf16), summed in fp32 by groups; 16 + zero times the
+ * group's sum of x is taken off before the group's scale.  A row of x that
+ * holds an infinity or a NaN has NaN in its whole row of y.
+ *   x      : (rows, ins) BF16               rows contiguous and 16-byte aligned
+ *   weight : (outs, ins/2) U8 contiguous, 16-byte aligned
+ *   scale  : (outs, ins/group) F32 or BF16  contiguous
+ *   zero   : (outs, ins/group) U8 contiguous   if SSM_HAS_ZERO (values to 255 count as they are)
+ *   bias   : (outs) F32, any stride         if SSM_HAS_BIAS
+ *   y      : (rows, outs) BF16 or F32       innermost stride 1
+ * group: 32, 64 or 128; ins a multiple of group; rows <= SSM_W4_MAX_ROWS.
+ * y may not overlap an input. */
+#define SSM_W4_MAX_ROWS 64
+
+typedef struct {
+  int64_t rows, ins, outs, group;
+  uint32_t flags;
+  ssm_tensor_desc x, weight, scale, zero, bias, y;
+} ssm_w4_desc;
+
+typedef struct {
+  const void* x;
+  const void* weight;
+  const void* scale;
+  const void* zero;  /* NULL unless SSM_HAS_ZERO */
+  const float* bias; /* NULL unless SSM_HAS_BIAS */
+  void* y;
+} ssm_w4_ptrs;
+
 /* --------------------------------------------------------------- entries */
 
 /* SSM_ABI_VERSION of the library that is loaded. */
@@ -485,6 +745,31 @@ ssm_status ssm_ssd_bwd(const ssm_ssd_bwd_desc* d, const ssm_ssd_bwd_ptrs* p, voi
 /* Causal depthwise convolution (+ bias, + SiLU) (definition above
  * ssm_conv_desc).  No workspace. */
 ssm_status ssm_causal_conv1d_fwd(const ssm_conv_desc* d, const ssm_conv_ptrs* p, void* hip_stream);
+
+/* Gated linear recurrence (definition above ssm_gated_desc).  The workspace
+ * (may be 0 bytes) is as ssm_selective_scan_fwd's. */
+ssm_status ssm_gated_scan_workspace_size(const ssm_gated_desc* d, size_t* bytes);
+ssm_status ssm_gated_scan_fwd(const ssm_gated_desc* d, const ssm_gated_ptrs* p, void* workspace,
+                              size_t workspace_bytes, void* hip_stream);
+
+/* Its backward (definition above ssm_gated_bwd_desc). */
+ssm_status ssm_gated_scan_bwd_workspace_size(const ssm_gated_bwd_desc* d, size_t* bytes);
+ssm_status ssm_gated_scan_bwd(const ssm_gated_bwd_desc* d, const ssm_gated_bwd_ptrs* p, void* workspace,
+                              size_t workspace_bytes, void* hip_stream);
+
+/* Its decode step (definition above ssm_gated_update_desc).  No workspace. */
+ssm_status ssm_gated_state_update(const ssm_gated_update_desc* d, const ssm_gated_update_ptrs* p, void* hip_stream);
+
+/* RMS norm with the residual's addition (definition above ssm_norm_desc).  No workspace. */
+ssm_status ssm_rms_norm_fwd(const ssm_norm_desc* d, const ssm_norm_ptrs* p, void* hip_stream);
+
+/* Its backward (definition above ssm_norm_bwd_desc). */
+ssm_status ssm_rms_norm_bwd_workspace_size(const ssm_norm_bwd_desc* d, size_t* bytes);
+ssm_status ssm_rms_norm_bwd(const ssm_norm_bwd_desc* d, const ssm_norm_bwd_ptrs* p, void* workspace,
+                            size_t workspace_bytes, void* hip_stream);
+
+/* Rows times 4-bit weights (definition above ssm_w4_desc).  No workspace. */
+ssm_status ssm_w4_matvec(const ssm_w4_desc* d, const ssm_w4_ptrs* p, void* hip_stream);
 
 #ifdef __cplusplus
 }

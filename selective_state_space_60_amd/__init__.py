@@ -19,10 +19,12 @@ LIB_PATH = os.path.join(_HERE, "libssm.so")
 
 SSM_OK, SSM_ERR_NULL, SSM_ERR_SHAPE, SSM_ERR_DTYPE, SSM_ERR_STRIDE, SSM_ERR_ALIGN, SSM_ERR_ALIAS, \
     SSM_ERR_UNSUPPORTED, SSM_ERR_WORKSPACE, SSM_ERR_HIP = range(10)
-SSM_F32, SSM_BF16, SSM_F16 = 0, 1, 2
+SSM_F32, SSM_BF16, SSM_F16, SSM_E4M3, SSM_I32, SSM_U8 = range(6)
 SSM_HAS_Z, SSM_HAS_D, SSM_DISC_EULER, SSM_HAS_H0, SSM_WANT_HLAST = 1, 2, 4, 8, 16
 SSM_DELTA_SOFTPLUS, SSM_HAS_DELTA_BIAS, SSM_HAS_BIAS, SSM_SILU = 32, 64, 128, 256
 SSM_WANT_CKPT, SSM_HAS_CKPT, SSM_HAS_SSD_FWD = 512, 1024, 2048
+SSM_HAS_BIAS_A, SSM_HAS_BIAS_X, SSM_HAS_LENS, SSM_HAS_DHLAST = 4096, 8192, 16384, 32768
+SSM_HAS_RESIDUAL, SSM_HAS_ZERO, SSM_HAS_STATE_OUT = 65536, 131072, 262144
 ABI_VERSION = 5
 MAX_DIMS = 5
 
@@ -31,7 +33,10 @@ EXPORTS = ("ssm_abi_version", "ssm_status_string", "ssm_last_hip_error", "ssm_se
            "ssm_selective_scan_fwd", "ssm_ssd_chunk_workspace_size", "ssm_ssd_chunk_fwd", "ssm_ssd_chunk_cumsum",
            "ssm_ssd_chunk_state", "ssm_ssd_state_passing", "ssm_ssd_chunk_scan", "ssm_selective_state_update",
            "ssm_causal_conv1d_fwd", "ssm_selective_scan_bwd_workspace_size", "ssm_selective_scan_bwd",
-           "ssm_ssd_bwd_workspace_size", "ssm_ssd_bwd", "ssm_selective_scan_fwd_noalloc")
+           "ssm_ssd_bwd_workspace_size", "ssm_ssd_bwd", "ssm_selective_scan_fwd_noalloc",
+           "ssm_gated_scan_workspace_size", "ssm_gated_scan_fwd", "ssm_gated_scan_bwd_workspace_size",
+           "ssm_gated_scan_bwd", "ssm_gated_state_update", "ssm_rms_norm_fwd", "ssm_rms_norm_bwd_workspace_size",
+           "ssm_rms_norm_bwd", "ssm_w4_matvec")
 
 
 class TensorDesc(ctypes.Structure):
@@ -48,6 +53,14 @@ _BWD_OUT = ("dx", "ddelta", "dz", "dA", "dB", "dC", "dD", "dh0", "ddelta_bias")
 _SSD_BWD_IN = ("x", "delta", "A", "B", "C", "D", "h0", "dy")
 _SSD_BWD_OUT = ("dx", "ddelta", "dA", "dB", "dC", "dD", "dh0")
 _SSD_FWD_SAVED = ("A_cum", "beta", "states")   # the forward's intermediates the backward can take
+_GATED_IN = ("x", "gate_a", "gate_x", "A", "bias_a", "bias_x", "z")
+_GATED_T = _GATED_IN + ("y", "h0", "h_last", "lens", "ckpt")
+_GATED_BWD_T = _GATED_IN + ("h0", "lens", "ckpt", "dy", "dh_last", "dx", "dgate_a", "dgate_x", "dz", "dA", "dbias_a",
+                            "dbias_x", "dh0")
+_GATED_UPD_T = _GATED_IN + ("y", "state", "state_out")
+_NORM_T = ("x", "residual", "weight", "y", "residual_out", "scale")
+_NORM_BWD_T = ("dy", "row", "weight", "dres", "dx", "dweight")
+_W4_T = ("x", "weight", "scale", "zero", "bias", "y")
 
 
 class ScanDesc(ctypes.Structure):
@@ -108,6 +121,68 @@ class SSDBwdPtrs(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in _SSD_BWD_IN + _SSD_BWD_OUT + _SSD_FWD_SAVED]
 
 
+def _sizes(names):
+    return [(n, ctypes.c_int64) for n in names]
+
+
+def _descs(names):
+    return [(n, TensorDesc) for n in names]
+
+
+def _pointers(names):
+    return [(n, ctypes.c_void_p) for n in names]
+
+
+class GatedDesc(ctypes.Structure):
+    _fields_ = _sizes(("batch", "seqlen", "dim")) + [("flags", ctypes.c_uint32)] + _descs(_GATED_T)
+
+
+class GatedPtrs(ctypes.Structure):
+    _fields_ = _pointers(_GATED_T)
+
+
+class GatedBwdDesc(ctypes.Structure):
+    _fields_ = _sizes(("batch", "seqlen", "dim")) + [("flags", ctypes.c_uint32)] + _descs(_GATED_BWD_T)
+
+
+class GatedBwdPtrs(ctypes.Structure):
+    _fields_ = _pointers(_GATED_BWD_T)
+
+
+class GatedUpdateDesc(ctypes.Structure):
+    _fields_ = _sizes(("batch", "dim")) + [("flags", ctypes.c_uint32)] + _descs(_GATED_UPD_T)
+
+
+class GatedUpdatePtrs(ctypes.Structure):
+    _fields_ = _pointers(_GATED_UPD_T)
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = _sizes(("batch", "seqlen", "dim", "group")) + [("eps", ctypes.c_float),
+                                                               ("flags", ctypes.c_uint32)] + _descs(_NORM_T)
+
+
+class NormPtrs(ctypes.Structure):
+    _fields_ = _pointers(_NORM_T)
+
+
+class NormBwdDesc(ctypes.Structure):
+    _fields_ = _sizes(("batch", "seqlen", "dim")) + [("eps", ctypes.c_float),
+                                                     ("flags", ctypes.c_uint32)] + _descs(_NORM_BWD_T)
+
+
+class NormBwdPtrs(ctypes.Structure):
+    _fields_ = _pointers(_NORM_BWD_T)
+
+
+class W4Desc(ctypes.Structure):
+    _fields_ = _sizes(("rows", "ins", "outs", "group")) + [("flags", ctypes.c_uint32)] + _descs(_W4_T)
+
+
+class W4Ptrs(ctypes.Structure):
+    _fields_ = _pointers(_W4_T)
+
+
 class SSMError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -147,6 +222,15 @@ def lib() -> ctypes.CDLL:
         L.ssm_selective_scan_bwd.argtypes = [P(ScanBwdDesc), P(ScanBwdPtrs), vp, sz, vp]
         L.ssm_ssd_bwd_workspace_size.argtypes = [P(SSDBwdDesc), P(sz)]
         L.ssm_ssd_bwd.argtypes = [P(SSDBwdDesc), P(SSDBwdPtrs), vp, sz, vp]
+        L.ssm_gated_scan_workspace_size.argtypes = [P(GatedDesc), P(sz)]
+        L.ssm_gated_scan_fwd.argtypes = [P(GatedDesc), P(GatedPtrs), vp, sz, vp]
+        L.ssm_gated_scan_bwd_workspace_size.argtypes = [P(GatedBwdDesc), P(sz)]
+        L.ssm_gated_scan_bwd.argtypes = [P(GatedBwdDesc), P(GatedBwdPtrs), vp, sz, vp]
+        L.ssm_gated_state_update.argtypes = [P(GatedUpdateDesc), P(GatedUpdatePtrs), vp]
+        L.ssm_rms_norm_fwd.argtypes = [P(NormDesc), P(NormPtrs), vp]
+        L.ssm_rms_norm_bwd_workspace_size.argtypes = [P(NormBwdDesc), P(sz)]
+        L.ssm_rms_norm_bwd.argtypes = [P(NormBwdDesc), P(NormBwdPtrs), vp, sz, vp]
+        L.ssm_w4_matvec.argtypes = [P(W4Desc), P(W4Ptrs), vp]
         for name in EXPORTS[3:]:
             getattr(L, name).restype = ctypes.c_int
         if L.ssm_abi_version() != ABI_VERSION:
@@ -168,7 +252,8 @@ def _check(status: int, where: str):
         raise SSMError(status, where)
 
 
-_DT = {torch.float32: SSM_F32, torch.bfloat16: SSM_BF16, torch.float16: SSM_F16}
+_DT = {torch.float32: SSM_F32, torch.bfloat16: SSM_BF16, torch.float16: SSM_F16,
+       torch.float8_e4m3fn: SSM_E4M3, torch.int32: SSM_I32, torch.uint8: SSM_U8}
 
 
 def tensor_desc(t) -> TensorDesc:
@@ -562,3 +647,7 @@ def ssd_bwd(dy, x, delta, A, B, C, chunk, D=None, h0=None, euler=False, dx_dtype
     ws = _workspace(n.value, dev)
     _check(lib().ssm_ssd_bwd(ctypes.byref(d), ctypes.byref(p), _p(ws), n.value, _stream(stream)), "ssm_ssd_bwd")
     return {k: v for k, v in out.items() if v is not None}
+
+
+from .layer import (GATED_CKPT_STEPS, NORM_MAX_DIM, W4_MAX_ROWS, gated_scan_bwd, gated_scan_ckpt,  # noqa: E402
+                    gated_scan_fwd, gated_state_update, rms_norm, rms_norm_bwd, w4_matvec, w4_quantize)

@@ -1,0 +1,418 @@
+// Root-mean-square norm of rows, with the residual's addition in front and an
+// optional e4m3 output with scales, and its backward, for gfx950.
+//
+//   row = x + residual (rounded to the type it is stored in)
+//   y   = weight row rstd,  rstd = rsqrt(mean(row^2) + eps)
+//
+// Bound by HBM: a row is read once, kept in registers across the reduction
+// and written once.  One wave owns a row of up to 4096 columns when there are
+// rows enough to fill the card (no barrier, 4 rows a workgroup); a workgroup
+// of four waves owns a longer row, or a short one of a few-row problem, where
+// the row's own latency is the time.  A lane holds groups of 8 consecutive
+// columns: 16-byte loads of bf16, and an e4m3 group of 32, 64 or 128 columns
+// is 4, 8 or 16 neighbouring lanes, whose largest value is found with DPP.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "ssm_internal.h"
+
+namespace ssm {
+namespace {
+
+constexpr int NT = 256;
+constexpr int V = 8;  // consecutive columns per lane
+constexpr float kE4M3Max = 448.f;
+constexpr float kMinScale = 1.17549435e-38f;  // 2^-126: a group of zeros divides by a normal number
+
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const f32x2_t v = {a, b};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
+}
+
+__device__ __forceinline__ float bf16_at(const void* p, int64_t i) {
+  return __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16);
+}
+
+// Columns [col, col + 8) of a row, of which the first n exist (n may be <= 0
+// or > 8); the others are 0.  Rows need only their element's alignment: wide
+// global accesses may be unaligned here.
+__device__ __forceinline__ void load8(const void* row, int type, int64_t col, int64_t n, float (&o)[V]) {
+  if (type == kNormBF16) {
+    if (n >= V) {
+      u32x4_t w;
+      __builtin_memcpy(&w, (const uint16_t*)row + col, 16);
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] = __uint_as_float((i & 1) ? (w[i / 2] & 0xFFFF0000u) : (w[i / 2] << 16));
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] = i < n ? bf16_at(row, col + i) : 0.f;
+    }
+  } else {
+    if (n >= V) {
+      u32x4_t w[2];
+      __builtin_memcpy(w, (const float*)row + col, 32);
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] = __uint_as_float(w[i / 4][i % 4]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] = i < n ? ((const float*)row)[col + i] : 0.f;
+    }
+  }
+}
+
+__device__ __forceinline__ void store8(void* row, int type, int64_t col, int64_t n, const float (&o)[V]) {
+  if (type == kNormBF16) {
+    if (n >= V) {
+      u32x4_t w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = pack2(o[2 * i], o[2 * i + 1]);
+      __builtin_memcpy((uint16_t*)row + col, &w, 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i < n) ((__bf16*)row)[col + i] = (__bf16)o[i];
+    }
+  } else {
+    if (n >= V) {
+      u32x4_t w[2];
+#pragma unroll
+      for (int i = 0; i < V; ++i) w[i / 4][i % 4] = __float_as_uint(o[i]);
+      __builtin_memcpy((float*)row + col, w, 32);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i < n) ((float*)row)[col + i] = o[i];
+    }
+  }
+}
+
+// Eight values, already divided by their scale, to e4m3 (nearest even).
+__device__ __forceinline__ void store8_e4m3(void* row, int64_t col, int64_t n, const float (&o)[V]) {
+  u32x2_t w = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(o[4 * i], o[4 * i + 1], 0, false);
+    w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(o[4 * i + 2], o[4 * i + 3], (int)w[i], true);
+  }
+  if (n >= V) {
+    __builtin_memcpy((uint8_t*)row + col, &w, 8);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < n) ((uint8_t*)row)[col + i] = (uint8_t)(w[i / 4] >> (8 * (i % 4)));
+  }
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+
+// The total in every lane of the wave.
+__device__ __forceinline__ float wave_sum(float v) {
+  v += dpp<0xB1>(v);   // quad_perm [1,0,3,2]
+  v += dpp<0x4E>(v);   // quad_perm [2,3,0,1]
+  v += dpp<0x141>(v);  // row_half_mirror
+  v += dpp<0x140>(v);  // row_mirror
+  v += __shfl_xor(v, 16);
+  v += __shfl_xor(v, 32);
+  return v;
+}
+
+// The largest over aligned groups of `lanes` (4, 8, 16 or 64), in every lane.
+__device__ __forceinline__ float group_max(float v, int lanes) {
+  v = fmaxf(v, dpp<0xB1>(v));
+  v = fmaxf(v, dpp<0x4E>(v));
+  if (lanes >= 8) v = fmaxf(v, dpp<0x141>(v));
+  if (lanes >= 16) v = fmaxf(v, dpp<0x140>(v));
+  if (lanes >= 64) {
+    v = fmaxf(v, __shfl_xor(v, 16));
+    v = fmaxf(v, __shfl_xor(v, 32));
+  }
+  return v;
+}
+
+// TPR threads per row (64: a wave, or the workgroup's 256), CH groups of
+// 8 columns per thread: dim <= TPR * 8 * CH.
+template <int TPR, int CH>
+__global__ __launch_bounds__(NT) void norm_fwd_kernel(NormParams p, int64_t rows) {
+  constexpr int WPR = TPR / 64;  // waves per row
+  __shared__ float lds[2][4];
+  const int lane = threadIdx.x % TPR, wave = threadIdx.x / 64;
+  const int64_t r = (int64_t)blockIdx.x * (NT / TPR) + threadIdx.x / TPR;
+  if (r >= rows) return;  // whole waves; with TPR == NT the whole workgroup
+  const int64_t b = r / p.L, t = r % p.L;
+  const int xe = p.x_type == kNormF32 ? 4 : 2, re = p.r_type == kNormF32 ? 4 : 2, oe = p.ro_type == kNormF32 ? 4 : 2;
+  const void* x = (const char*)p.x + (b * p.xs_b + t * p.xs_t) * xe;
+  float f[CH][V];
+  float ss = 0.f;
+#pragma unroll
+  for (int k = 0; k < CH; ++k) {
+    const int64_t col = (int64_t)(k * TPR + lane) * V;
+    load8(x, p.x_type, col, p.D - col, f[k]);
+  }
+  if (p.residual) {
+    const void* res = (const char*)p.residual + (b * p.rs_b + t * p.rs_t) * re;
+    void* out = (char*)p.residual_out + (b * p.ros_b + t * p.ros_t) * oe;
+    float g[CH][V];
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int64_t col = (int64_t)(k * TPR + lane) * V;
+      load8(res, p.r_type, col, p.D - col, g[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int64_t col = (int64_t)(k * TPR + lane) * V;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        f[k][i] += g[k][i];
+        if (p.ro_type == kNormBF16) f[k][i] = (float)(__bf16)f[k][i];
+      }
+      store8(out, p.ro_type, col, p.D - col, f[k]);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < CH; ++k)
+#pragma unroll
+    for (int i = 0; i < V; ++i) ss = __builtin_fmaf(f[k][i], f[k][i], ss);
+  ss = wave_sum(ss);
+  if constexpr (WPR > 1) {
+    if (threadIdx.x % 64 == 0) lds[0][wave] = ss;
+    __syncthreads();
+    ss = (lds[0][0] + lds[0][1]) + (lds[0][2] + lds[0][3]);
+  }
+  const float rstd = __builtin_amdgcn_rsqf(ss / (float)p.D + p.eps);
+  float amax = 0.f;
+#pragma unroll
+  for (int k = 0; k < CH; ++k) {
+    const int64_t col = (int64_t)(k * TPR + lane) * V;
+    float w[V];
+    load8(p.weight, kNormF32, col, p.D - col, w);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      f[k][i] = f[k][i] * rstd * w[i];
+      amax = fmaxf(amax, fabsf(f[k][i]));
+    }
+  }
+  void* y = (char*)p.y + (b * p.ys_b + t * p.ys_t) * (p.y_type == kNormF32 ? 4 : p.y_type == kNormBF16 ? 2 : 1);
+  if (p.y_type != kNormE4M3) {
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int64_t col = (int64_t)(k * TPR + lane) * V;
+      store8(y, p.y_type, col, p.D - col, f[k]);
+    }
+    return;
+  }
+  if (p.group == 0) {
+    amax = group_max(amax, 64);
+    if constexpr (WPR > 1) {
+      if (threadIdx.x % 64 == 0) lds[1][wave] = amax;
+      __syncthreads();
+      amax = fmaxf(fmaxf(lds[1][0], lds[1][1]), fmaxf(lds[1][2], lds[1][3]));
+    }
+  }
+  const int64_t ng = p.group ? (p.D + p.group - 1) / p.group : 1;
+#pragma unroll
+  for (int k = 0; k < CH; ++k) {
+    const int64_t col = (int64_t)(k * TPR + lane) * V;
+    float m = amax;
+    if (p.group) {
+      m = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) m = fmaxf(m, fabsf(f[k][i]));
+      m = group_max(m, (int)p.group / V);
+    }
+    const float scale = fmaxf(m / kE4M3Max, kMinScale);
+    const float inv = 1.f / scale;
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[k][i] *= inv;
+    store8_e4m3(y, col, p.D - col, f[k]);
+    if (p.group ? col < p.D && col % p.group == 0 : col == 0) p.scale[r * ng + (p.group ? col / p.group : 0)] = scale;
+  }
+}
+
+// ------------------------------------------------------------------ backward
+// Workgroups walk the rows with a stride and keep dweight's sums of their rows
+// in registers; the four waves' sums are added in order through LDS.
+template <int TPR, int CH>
+__global__ __launch_bounds__(NT) void norm_bwd_kernel(NormBwdParams p, int64_t rows) {
+  constexpr int RPB = NT / TPR;
+  __shared__ float lds[2][2][4];
+  const int lane = threadIdx.x % TPR, wave = threadIdx.x / 64, sub = threadIdx.x / TPR;
+  const int de = p.dy_type == kNormF32 ? 4 : 2, re = p.row_type == kNormF32 ? 4 : 2;
+  const int se = p.dres_type == kNormF32 ? 4 : 2, xe = p.dx_type == kNormF32 ? 4 : 2;
+  float acc[CH][V];
+#pragma unroll
+  for (int k = 0; k < CH; ++k)
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[k][i] = 0.f;
+  int buf = 0;
+  // with TPR == NT every thread of the workgroup runs the same number of rounds
+  for (int64_t r = (int64_t)blockIdx.x * RPB + sub; r < rows; r += (int64_t)gridDim.x * RPB, buf ^= 1) {
+    const int64_t b = r / p.L, t = r % p.L;
+    const void* dy = (const char*)p.dy + (b * p.dys_b + t * p.dys_t) * de;
+    const void* row = (const char*)p.row + (b * p.rs_b + t * p.rs_t) * re;
+    float f[CH][V], g[CH][V];
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int64_t col = (int64_t)(k * TPR + lane) * V;
+      load8(row, p.row_type, col, p.D - col, f[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int64_t col = (int64_t)(k * TPR + lane) * V;
+      load8(dy, p.dy_type, col, p.D - col, g[k]);
+    }
+    float ss = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int64_t col = (int64_t)(k * TPR + lane) * V;
+      float w[V];
+      load8(p.weight, kNormF32, col, p.D - col, w);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        ss = __builtin_fmaf(f[k][i], f[k][i], ss);
+        s1 = __builtin_fmaf(g[k][i] * w[i], f[k][i], s1);
+      }
+    }
+    ss = wave_sum(ss);
+    s1 = wave_sum(s1);
+    if constexpr (TPR > 64) {  // two buffers: a wave may be a round ahead of the others' reads
+      if (threadIdx.x % 64 == 0) {
+        lds[buf][0][wave] = ss;
+        lds[buf][1][wave] = s1;
+      }
+      __syncthreads();
+      ss = (lds[buf][0][0] + lds[buf][0][1]) + (lds[buf][0][2] + lds[buf][0][3]);
+      s1 = (lds[buf][1][0] + lds[buf][1][1]) + (lds[buf][1][2] + lds[buf][1][3]);
+    }
+    const float rstd = __builtin_amdgcn_rsqf(ss / (float)p.D + p.eps);
+    const float coef = s1 * rstd / (float)p.D * rstd;  // mean(weight dy hat) rstd
+    const void* dres = (const char*)p.dres + (b * p.drs_b + t * p.drs_t) * se;
+    void* dx = (char*)p.dx + (b * p.dxs_b + t * p.dxs_t) * xe;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int64_t col = (int64_t)(k * TPR + lane) * V;
+      float w[V], o[V];
+      load8(p.weight, kNormF32, col, p.D - col, w);
+      if (p.dres) {
+        load8(dres, p.dres_type, col, p.D - col, o);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float hat = f[k][i] * rstd;
+        acc[k][i] = __builtin_fmaf(g[k][i], hat, acc[k][i]);
+        o[i] += __builtin_fmaf(rstd, g[k][i] * w[i], -hat * coef);
+      }
+      store8(dx, p.dx_type, col, p.D - col, o);
+    }
+  }
+  float* part = p.part + (int64_t)blockIdx.x * p.D;
+  if constexpr (RPB > 1) {
+    __shared__ float sums[TPR * V * CH];
+    for (int w = 0; w < RPB; ++w) {
+      if (wave == w) {
+#pragma unroll
+        for (int k = 0; k < CH; ++k)
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            float* s = &sums[(k * TPR + lane) * V + i];
+            *s = w == 0 ? acc[k][i] : *s + acc[k][i];
+          }
+      }
+      __syncthreads();
+    }
+    for (int64_t c = threadIdx.x; c < p.D; c += NT) part[c] = sums[c];
+  } else {
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int64_t col = (int64_t)(k * TPR + lane) * V;
+      store8(part, kNormF32, col, p.D - col, acc[k]);
+    }
+  }
+}
+
+// dweight: the workgroups' sums in a fixed order, 8 interleaved runs per
+// column, then the runs.
+__global__ __launch_bounds__(NT) void norm_sums_kernel(const float* part, int64_t parts, int64_t D, float* out) {
+  __shared__ float lds[8][32];
+  const int lane = threadIdx.x % 32, run = threadIdx.x / 32;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+  float sum = 0.f;
+  if (c < D)
+    for (int64_t k = run; k < parts; k += 8) sum += part[k * D + c];
+  lds[run][lane] = sum;
+  __syncthreads();
+  if (run == 0 && c < D) {
+#pragma unroll
+    for (int k = 1; k < 8; ++k) sum += lds[k][lane];
+    out[c] = sum;
+  }
+}
+
+// A wave per row up to 4096 columns once the rows give every compute unit a
+// workgroup of four; a workgroup per row otherwise.
+bool wave_rows(int64_t rows, int64_t dim) { return dim <= 4096 && rows >= 1024; }
+
+template <int TPR, int CH>
+void launch_fwd(const NormParams& p, int64_t rows, hipStream_t stream) {
+  constexpr int RPB = NT / TPR;
+  hipLaunchKernelGGL((norm_fwd_kernel<TPR, CH>), dim3((unsigned)((rows + RPB - 1) / RPB)), dim3(NT), 0, stream, p,
+                     rows);
+}
+
+template <int TPR, int CH>
+void launch_bwd(const NormBwdParams& p, int64_t rows, hipStream_t stream) {
+  hipLaunchKernelGGL((norm_bwd_kernel<TPR, CH>), dim3((unsigned)p.parts), dim3(NT), 0, stream, p, rows);
+}
+
+}  // namespace
+
+int norm_bwd_parts(int64_t rows, int64_t dim) {
+  const int64_t blocks = wave_rows(rows, dim) ? (rows + 3) / 4 : rows;
+  return (int)std::min<int64_t>(blocks, 768);
+}
+
+#define SSM_NORM_DISPATCH(LAUNCH, P)                      \
+  if (wave_rows(rows, (P).D)) {                           \
+    const int64_t ch = ((P).D + 64 * V - 1) / (64 * V);   \
+    if (ch <= 1) LAUNCH<64, 1>(P, rows, stream);          \
+    else if (ch <= 2) LAUNCH<64, 2>(P, rows, stream);     \
+    else if (ch <= 3) LAUNCH<64, 3>(P, rows, stream);     \
+    else if (ch <= 4) LAUNCH<64, 4>(P, rows, stream);     \
+    else if (ch <= 5) LAUNCH<64, 5>(P, rows, stream);     \
+    else if (ch <= 6) LAUNCH<64, 6>(P, rows, stream);     \
+    else LAUNCH<64, 8>(P, rows, stream);                  \
+  } else {                                                \
+    const int64_t ch = ((P).D + NT * V - 1) / (NT * V);   \
+    if (ch <= 1) LAUNCH<NT, 1>(P, rows, stream);          \
+    else if (ch <= 2) LAUNCH<NT, 2>(P, rows, stream);     \
+    else if (ch <= 3) LAUNCH<NT, 3>(P, rows, stream);     \
+    else if (ch <= 4) LAUNCH<NT, 4>(P, rows, stream);     \
+    else LAUNCH<NT, 8>(P, rows, stream);                  \
+  }
+
+hipError_t launch_rms_norm(const NormParams& p, hipStream_t stream) {
+  const int64_t rows = p.batch * p.L;
+  SSM_NORM_DISPATCH(launch_fwd, p)
+  return hipGetLastError();
+}
+
+hipError_t launch_rms_norm_bwd(const NormBwdParams& p, hipStream_t stream) {
+  const int64_t rows = p.batch * p.L;
+  SSM_NORM_DISPATCH(launch_bwd, p)
+  hipLaunchKernelGGL(norm_sums_kernel, dim3((unsigned)((p.D + 31) / 32)), dim3(NT), 0, stream, p.part,
+                     (int64_t)p.parts, p.D, p.dweight);
+  return hipGetLastError();
+}
+
+}  // namespace ssm

@@ -8,11 +8,12 @@
 #include <cstring>
 
 #include "../../include/ssm.h"
+#include "abi_checks.h"
 #include "ssm_internal.h"
 
-namespace {
+using namespace ssm::abi;
 
-thread_local int g_last_hip_error = 0;
+namespace {
 
 constexpr uint32_t kScanFlags = SSM_HAS_Z | SSM_HAS_D | SSM_DISC_EULER | SSM_HAS_H0 | SSM_WANT_HLAST |
                                 SSM_DELTA_SOFTPLUS | SSM_HAS_DELTA_BIAS | SSM_WANT_CKPT;
@@ -30,76 +31,6 @@ void ckpt_shape(int64_t batch, int64_t seqlen, int64_t dim, int64_t dstate, int6
   sh[3] = dstate;
 }
 constexpr int kSimds = 256 * 4;  // MI355X: 256 compute units x 4 SIMDs
-
-int64_t esize(int32_t dt) { return dt == SSM_BF16 || dt == SSM_F16 ? 2 : 4; }
-
-struct Span {
-  uintptr_t lo = 0, hi = 0;  // [lo, hi)
-  bool valid = false;
-};
-
-Span span_of(const ssm_tensor_desc& t, const void* ptr) {
-  Span s;
-  if (!ptr) return s;
-  int64_t last = 0;
-  for (int i = 0; i < t.ndim; ++i) last += (t.shape[i] - 1) * t.stride[i];
-  s.lo = (uintptr_t)ptr;
-  s.hi = s.lo + (uintptr_t)((last + 1) * esize(t.dtype));
-  s.valid = true;
-  return s;
-}
-
-// The bytes [ptr, ptr + bytes) of a plain contiguous buffer.
-Span span_bytes(const void* ptr, int64_t bytes) {
-  Span s;
-  if (!ptr) return s;
-  s.lo = (uintptr_t)ptr;
-  s.hi = s.lo + (uintptr_t)bytes;
-  s.valid = true;
-  return s;
-}
-
-bool overlap(const Span& a, const Span& b) { return a.valid && b.valid && a.lo < b.hi && b.lo < a.hi; }
-
-// Shape, dtype and stride checks of one tensor.
-ssm_status check_tensor(const ssm_tensor_desc& t, int ndim, const int64_t* shape, bool dtype_ok, bool inner_unit,
-                        bool contiguous) {
-  if (!dtype_ok) return SSM_ERR_DTYPE;
-  if (t.ndim != ndim) return SSM_ERR_SHAPE;
-  for (int i = 0; i < ndim; ++i)
-    if (t.shape[i] != shape[i]) return SSM_ERR_SHAPE;
-  for (int i = 0; i < ndim; ++i)
-    if (t.stride[i] < 0) return SSM_ERR_STRIDE;
-  if (inner_unit && t.stride[ndim - 1] != 1 && t.shape[ndim - 1] > 1) return SSM_ERR_STRIDE;
-  if (contiguous) {
-    int64_t expect = 1;
-    for (int i = ndim - 1; i >= 0; --i) {
-      if (t.shape[i] > 1 && t.stride[i] != expect) return SSM_ERR_STRIDE;
-      expect *= t.shape[i];
-    }
-  }
-  return SSM_OK;
-}
-
-// An output must not write one element twice: with dimensions sorted by
-// stride, each stride must be at least the extent of the smaller ones.
-bool non_overlapping(const ssm_tensor_desc& t) {
-  int idx[SSM_MAX_DIMS];
-  int n = 0;
-  for (int i = 0; i < t.ndim; ++i)
-    if (t.shape[i] > 1) idx[n++] = i;
-  std::sort(idx, idx + n, [&](int a, int b) { return t.stride[a] < t.stride[b]; });
-  int64_t extent = 1;
-  for (int k = 0; k < n; ++k) {
-    if (t.stride[idx[k]] < extent) return false;
-    extent = t.stride[idx[k]] * (t.shape[idx[k]] - 1) + extent;
-  }
-  return true;
-}
-
-bool aligned(const void* p, int64_t bytes) { return ((uintptr_t)p % (uintptr_t)bytes) == 0; }
-
-int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
 
 // ------------------------------------------------------------------ scan
 
@@ -741,12 +672,6 @@ ssm_status validate_conv(const ssm_conv_desc* d, const ssm_conv_ptrs* p) {
   return SSM_OK;
 }
 
-ssm_status hip_status(hipError_t e) {
-  if (e == hipSuccess) return SSM_OK;
-  g_last_hip_error = (int)e;
-  return SSM_ERR_HIP;
-}
-
 // Fills the kernel parameters of a validated scan and launches it; the
 // workspace (pl.ws_total bytes, 256-byte aligned) is the caller's or the
 // static scratch.
@@ -808,7 +733,7 @@ const char* ssm_status_string(ssm_status s) {
   return "unknown ssm_status";
 }
 
-int ssm_last_hip_error(void) { return g_last_hip_error; }
+int ssm_last_hip_error(void) { return last_hip_error(); }
 
 ssm_status ssm_selective_scan_workspace_size(const ssm_scan_desc* d, size_t* bytes) {
   if (!bytes) return SSM_ERR_NULL;

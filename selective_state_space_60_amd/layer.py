@@ -1,0 +1,283 @@
+"""Binding of the operators of a pre-norm gated recurrent layer: the gated
+linear recurrence (``gated_scan_fwd``, ``gated_scan_bwd``,
+``gated_state_update``), the RMS norm (``rms_norm``, ``rms_norm_bwd``) and the
+product with 4-bit weights (``w4_matvec``).  Argument marshalling only, as in
+the package; definitions stand in include/ssm.h.
+
+The descriptor of a call (shapes, strides, types, flags) and the workspace
+size it asks for are kept by exactly these values, so that a call that repeats
+a shape costs a lookup; pointers and values are never kept.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import (_GATED_BWD_T, _GATED_T, _GATED_UPD_T, _NORM_BWD_T, _NORM_T, _W4_T, SSM_HAS_BIAS, SSM_HAS_BIAS_A,
+               SSM_HAS_BIAS_X, SSM_HAS_CKPT, SSM_HAS_DHLAST, SSM_HAS_H0, SSM_HAS_LENS, SSM_HAS_RESIDUAL,
+               SSM_HAS_STATE_OUT, SSM_HAS_Z, SSM_HAS_ZERO, SSM_WANT_CKPT, SSM_WANT_HLAST, GatedBwdDesc, GatedBwdPtrs,
+               GatedDesc, GatedPtrs, GatedUpdateDesc, GatedUpdatePtrs, NormBwdDesc, NormBwdPtrs, NormDesc, NormPtrs,
+               W4Desc, W4Ptrs, _check, lib, tensor_desc)
+
+GATED_CKPT_STEPS = 64  # SSM_GATED_CKPT_STEPS
+NORM_MAX_DIM = 16384   # SSM_NORM_MAX_DIM
+W4_MAX_ROWS = 64       # SSM_W4_MAX_ROWS
+
+_MAX_PLANS = 1024
+_plans: dict = {}
+
+
+class _Plan:
+    """One entry point's descriptor and workspace size."""
+    __slots__ = ("desc", "ref", "nbytes")
+
+    def __init__(self, desc, size_entry):
+        self.desc = desc
+        self.ref = ctypes.byref(desc)
+        self.nbytes = 0
+        if size_entry is not None:
+            n = ctypes.c_size_t()
+            _check(getattr(lib(), size_entry)(self.ref, ctypes.byref(n)), size_entry)
+            self.nbytes = n.value
+
+
+def _call(entry, Desc, Ptrs, names, sizes, flags, tensors, stream, size_entry=None, eps=None):
+    """Look up or build the descriptor of `tensors` (in the order of `names`,
+    None: left out) and launch on `stream` (default: the current stream of the
+    tensors' device)."""
+    key = (entry, sizes, flags, eps) + tuple([None if t is None else (t.dtype, t.shape, t.stride()) for t in tensors])
+    plan = _plans.get(key)
+    if plan is None:
+        d = Desc()
+        for name, v in sizes:
+            setattr(d, name, v)
+        d.flags = flags
+        if eps is not None:
+            d.eps = eps
+        for name, t in zip(names, tensors):
+            setattr(d, name, tensor_desc(t))
+        plan = _Plan(d, size_entry)
+        if len(_plans) >= _MAX_PLANS:
+            _plans.clear()
+        _plans[key] = plan
+    device = tensors[0].device
+    ptrs = Ptrs(*[None if t is None else t.data_ptr() for t in tensors])
+    index = device.index
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _launch(entry, plan, ptrs, stream, device)
+    return _launch(entry, plan, ptrs, stream, device)
+
+
+def _launch(entry, plan, ptrs, stream, device):
+    fn = getattr(lib(), entry)
+    if stream is None:
+        handle = torch.cuda.current_stream(device).cuda_stream
+    else:
+        handle = stream.cuda_stream
+    if plan.nbytes == 0 and len(fn.argtypes) == 3:
+        _check(fn(plan.ref, ctypes.byref(ptrs), handle), entry)
+        return
+    ws = _empty(stream, (plan.nbytes,), torch.uint8, device) if plan.nbytes else None
+    _check(fn(plan.ref, ctypes.byref(ptrs), None if ws is None else ws.data_ptr(), plan.nbytes, handle), entry)
+
+
+def _empty(stream, shape, dtype, device):
+    """Memory for a call on `stream`: it belongs to that stream's pool, so that
+    freeing it early is safe there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _one_gpu(where, *tensors):
+    device = tensors[0].device
+    if device.type != "cuda":
+        raise ValueError("%s: tensors must be on a GPU" % where)
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError("%s: all tensors must be on %s" % (where, device))
+    return device
+
+
+# -------------------------------------------------- gated linear recurrence
+
+def gated_scan_ckpt(batch: int, seqlen: int, dim: int, device="cuda"):
+    """An uninitialised checkpoint buffer for gated_scan_fwd(ckpt=...) and
+    gated_scan_bwd(ckpt=...): the state before every 64th step."""
+    return torch.empty((batch, (seqlen + GATED_CKPT_STEPS - 1) // GATED_CKPT_STEPS, dim), dtype=torch.float32,
+                       device=device)
+
+
+def _gated_flags(bias_a, bias_x, z):
+    return ((SSM_HAS_BIAS_A if bias_a is not None else 0) | (SSM_HAS_BIAS_X if bias_x is not None else 0) |
+            (SSM_HAS_Z if z is not None else 0))
+
+
+def gated_scan_fwd(x, gate_a, gate_x, A, bias_a=None, bias_x=None, z=None, h0=None, lens=None, want_hlast=False,
+                   y_dtype=None, y=None, ckpt=None, stream=None):
+    """y = gated linear recurrence of x (see include/ssm.h).  Returns (y,
+    h_last or None).
+
+    x, gate_a, gate_x, z: (batch, L, dim), all fp32 or all bf16, unit innermost
+    stride; A, bias_a, bias_x: (dim,) fp32; h0: (batch, dim) fp32; lens:
+    (batch,) int32 on the GPU, the steps of each row that count (later y are
+    zeros, h_last is the state after the last that counts).  ckpt: optional
+    gated_scan_ckpt(...) buffer, filled for gated_scan_bwd(ckpt=...)."""
+    dev = _one_gpu("gated_scan_fwd", x, gate_a, gate_x, A, bias_a, bias_x, z, h0, lens, y, ckpt)
+    batch, L, dim = x.shape
+    if y is None:
+        y = _empty(stream, x.shape, y_dtype or x.dtype, dev)
+    h_last = _empty(stream, (batch, dim), torch.float32, dev) if want_hlast else None
+    flags = (_gated_flags(bias_a, bias_x, z) | (SSM_HAS_H0 if h0 is not None else 0) |
+             (SSM_WANT_HLAST if want_hlast else 0) | (SSM_HAS_LENS if lens is not None else 0) |
+             (SSM_WANT_CKPT if ckpt is not None else 0))
+    _call("ssm_gated_scan_fwd", GatedDesc, GatedPtrs, _GATED_T, (("batch", batch), ("seqlen", L), ("dim", dim)),
+          flags, (x, gate_a, gate_x, A, bias_a, bias_x, z, y, h0, h_last, lens, ckpt), stream,
+          size_entry="ssm_gated_scan_workspace_size")
+    return y, h_last
+
+
+def gated_scan_bwd(dy, x, gate_a, gate_x, A, bias_a=None, bias_x=None, z=None, h0=None, lens=None, dh_last=None,
+                   ckpt=None, stream=None) -> dict:
+    """Gradients of sum(dy * y) + sum(dh_last * h_last) for y, h_last =
+    gated_scan_fwd(x, gate_a, gate_x, A, bias_a, bias_x, z, h0, lens) (see
+    include/ssm.h).  ckpt: the forward's checkpoints of the same inputs;
+    without them they are recomputed.
+
+    Returns a dict: dx, dgate_a, dgate_x, dz (if z), all of dy's dtype (x's or
+    fp32), and fp32 dA, dbias_a, dbias_x (dim,; if given) and dh0 (if h0)."""
+    dev = _one_gpu("gated_scan_bwd", x, dy, gate_a, gate_x, A, bias_a, bias_x, z, h0, lens, dh_last, ckpt)
+    batch, L, dim = x.shape
+    # one buffer each: the gradients of the streams and of the channels
+    n = 3 if z is None else 4
+    g = _empty(stream, (n,) + tuple(x.shape), dy.dtype, dev)
+    s = _empty(stream, (3, dim), torch.float32, dev)
+    out = {"dx": g[0], "dgate_a": g[1], "dgate_x": g[2], "dz": g[3] if z is not None else None, "dA": s[0],
+           "dbias_a": s[1] if bias_a is not None else None, "dbias_x": s[2] if bias_x is not None else None,
+           "dh0": _empty(stream, (batch, dim), torch.float32, dev) if h0 is not None else None}
+    flags = (_gated_flags(bias_a, bias_x, z) | (SSM_HAS_H0 if h0 is not None else 0) |
+             (SSM_HAS_LENS if lens is not None else 0) | (SSM_HAS_CKPT if ckpt is not None else 0) |
+             (SSM_HAS_DHLAST if dh_last is not None else 0))
+    _call("ssm_gated_scan_bwd", GatedBwdDesc, GatedBwdPtrs, _GATED_BWD_T,
+          (("batch", batch), ("seqlen", L), ("dim", dim)), flags,
+          (x, gate_a, gate_x, A, bias_a, bias_x, z, h0, lens, ckpt, dy, dh_last) + tuple(out.values()), stream,
+          size_entry="ssm_gated_scan_bwd_workspace_size")
+    return {k: v for k, v in out.items() if v is not None}
+
+
+def gated_state_update(state, x, gate_a, gate_x, A, bias_a=None, bias_x=None, z=None, state_out=None, y_dtype=None,
+                       y=None, stream=None):
+    """One decode step of the gated recurrence (see include/ssm.h): advances
+    ``state`` (batch, dim) fp32 in place, or into ``state_out`` if given, and
+    returns y (batch, dim).  x, gate_a, gate_x, z: (batch, dim)."""
+    dev = _one_gpu("gated_state_update", x, state, gate_a, gate_x, A, bias_a, bias_x, z, state_out, y)
+    if y is None:
+        y = _empty(stream, x.shape, y_dtype or x.dtype, dev)
+    batch, dim = x.shape
+    flags = _gated_flags(bias_a, bias_x, z) | (SSM_HAS_STATE_OUT if state_out is not None else 0)
+    _call("ssm_gated_state_update", GatedUpdateDesc, GatedUpdatePtrs, _GATED_UPD_T, (("batch", batch), ("dim", dim)),
+          flags, (x, gate_a, gate_x, A, bias_a, bias_x, z, y, state, state_out), stream)
+    return y
+
+
+# ---------------------------------------------------------------------- norm
+
+def _rows(t):
+    """(batch, L, dim) view of a (..., dim) tensor of two or three dimensions."""
+    return t if t is None or t.dim() == 3 else t.unsqueeze(0)
+
+
+def rms_norm(x, weight, eps=1e-5, residual=None, residual_dtype=None, residual_out=None, y_dtype=None, group=0,
+             y=None, stream=None):
+    """RMS norm of the rows of x (+ residual) (see include/ssm.h).  Returns
+    (y, residual_out or None, scale or None).
+
+    x, residual: (batch, L, dim) or (rows, dim), unit innermost stride; weight
+    (dim,) fp32.  residual_out (the sum) has residual_dtype, default
+    residual's; it may be residual itself.  y_dtype: x's dtype (default),
+    torch.float32, or torch.float8_e4m3fn, which comes with fp32 scales, one
+    for each `group` columns (32, 64 or 128; 0: one a row): scale has x's
+    leading shape and ceil(dim / group) columns."""
+    dev = _one_gpu("rms_norm", x, weight, residual, residual_out, y)
+    if x.dim() not in (2, 3) or (residual is not None and residual.shape != x.shape):
+        raise ValueError("rms_norm: x and residual are (rows, dim) or (batch, L, dim), of one shape")
+    if residual is None and residual_out is not None:
+        raise ValueError("rms_norm: residual_out without residual")
+    if y is None:
+        y = _empty(stream, x.shape, y_dtype or x.dtype, dev)
+    if residual is not None and residual_out is None:
+        residual_out = _empty(stream, x.shape, residual_dtype or residual.dtype, dev)
+    dim = x.shape[-1]
+    scale = None
+    if y.dtype == torch.float8_e4m3fn:
+        scale = _empty(stream, tuple(x.shape[:-1]) + ((dim + group - 1) // group if group > 0 else 1,),
+                       torch.float32, dev)
+    x3 = _rows(x)
+    _call("ssm_rms_norm_fwd", NormDesc, NormPtrs, _NORM_T,
+          (("batch", x3.shape[0]), ("seqlen", x3.shape[1]), ("dim", dim), ("group", group)),
+          SSM_HAS_RESIDUAL if residual is not None else 0,
+          (x3, _rows(residual), weight, _rows(y), _rows(residual_out), _rows(scale)), stream, eps=float(eps))
+    return y, residual_out, scale
+
+
+def rms_norm_bwd(dy, row, weight, eps=1e-5, dres=None, grad_dtype=None, stream=None) -> dict:
+    """Gradients of sum(dy * y) + sum(dres * residual_out) for y, residual_out
+    = rms_norm(...) (see include/ssm.h).  row: what was normalised
+    (residual_out, or x without a residual); dres: the gradient that reaches
+    residual_out besides.
+
+    Returns {"dx": grad_dtype, default dy's -- the gradient of x and of
+    residual alike, "dweight": (dim,) fp32}."""
+    dev = _one_gpu("rms_norm_bwd", dy, row, weight, dres)
+    if row.dim() not in (2, 3) or dy.shape != row.shape or (dres is not None and dres.shape != row.shape):
+        raise ValueError("rms_norm_bwd: dy, row and dres are (rows, dim) or (batch, L, dim), of one shape")
+    dx = _empty(stream, row.shape, grad_dtype or dy.dtype, dev)
+    dweight = _empty(stream, (row.shape[-1],), torch.float32, dev)
+    r3 = _rows(row)
+    _call("ssm_rms_norm_bwd", NormBwdDesc, NormBwdPtrs, _NORM_BWD_T,
+          (("batch", r3.shape[0]), ("seqlen", r3.shape[1]), ("dim", r3.shape[2])),
+          SSM_HAS_RESIDUAL if dres is not None else 0, (_rows(dy), r3, weight, _rows(dres), _rows(dx), dweight),
+          stream, size_entry="ssm_rms_norm_bwd_workspace_size", eps=float(eps))
+    return {"dx": dx, "dweight": dweight}
+
+
+# ------------------------------------------------------------ 4-bit weights
+
+def w4_quantize(weight, group=128, scale_dtype=torch.bfloat16):
+    """(packed, scale) of a weight matrix (outs, ins) for w4_matvec, symmetric
+    about 8: scale = amax(|w|) / 7 of every group of a row (rounded to
+    scale_dtype), q = round(w / scale) + 8 in 1..15; the even column of a pair
+    is the low half of its byte.  Done once when weights are loaded, on the
+    weight's own device."""
+    outs, ins = weight.shape
+    if group not in (32, 64, 128) or ins % group:
+        raise ValueError("w4_quantize: group is 32, 64 or 128 and divides the columns")
+    w = weight.detach().float().reshape(outs, ins // group, group)
+    scale = (w.abs().amax(-1) / 7.0).to(scale_dtype)
+    s = scale.float().unsqueeze(-1)
+    q = torch.where(s > 0, torch.round(w / s), torch.zeros_like(w)).clamp(-7, 7).to(torch.int32) + 8
+    q = q.reshape(outs, ins // 2, 2)
+    return (q[..., 0] | (q[..., 1] << 4)).to(torch.uint8), scale
+
+
+def w4_matvec(x, weight, scale, zero=None, bias=None, y_dtype=None, y=None, stream=None):
+    """y = x W^T + bias with 4-bit weights (see include/ssm.h).  x: (rows,
+    ins) bf16, rows <= 64; weight: (outs, ins / 2) uint8, two weights a byte;
+    scale: (outs, ins / group) bf16 or fp32, group 32, 64 or 128; zero: (outs,
+    ins / group) uint8 (default 8); bias: (outs,) fp32.  Returns y (rows,
+    outs), bf16 by default."""
+    dev = _one_gpu("w4_matvec", x, weight, scale, zero, bias, y)
+    rows, ins = x.shape
+    outs = weight.shape[0]
+    if scale.dim() != 2 or scale.shape[1] == 0 or ins % scale.shape[1]:
+        raise ValueError("w4_matvec: scale is (outs, ins / group)")
+    if y is None:
+        y = _empty(stream, (rows, outs), y_dtype or x.dtype, dev)
+    _call("ssm_w4_matvec", W4Desc, W4Ptrs, _W4_T,
+          (("rows", rows), ("ins", ins), ("outs", outs), ("group", ins // scale.shape[1])),
+          (SSM_HAS_ZERO if zero is not None else 0) | (SSM_HAS_BIAS if bias is not None else 0),
+          (x, weight, scale, zero, bias, y), stream)
+    return y

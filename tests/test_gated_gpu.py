@@ -1,0 +1,272 @@
+"""GPU parity of the gated linear recurrence (ssm_gated_scan_fwd / _bwd,
+ssm_gated_state_update) against its fp64 definition, step by step, at sizes
+where a chunk (8 and 16 steps), a round (128 and 256), a checkpoint (64) or a
+channel tile (32 and 64) ends inside, starts or is missed by one."""
+import pytest
+
+import _layer_ref as ref
+from _gpu import banner
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():  # pragma: no cover
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+import selective_state_space_60_amd as ssm  # noqa: E402
+
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def make(b, L, D, io, z=True, h0=True, lens=None, bias=True, seed=0, pack=True, A=None):
+    """Inputs on the CPU: x, gate_a, gate_x (, z) as slices of one projection
+    (or apart); decays from 0.37 to 0.992 at an open gate."""
+    g = torch.Generator().manual_seed(seed)
+    n = 4 if z else 3
+    rnd = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    t = {}
+    if pack:
+        p = rnd(b, L, n * D).clamp(-4, 4).to(TYPES[io])
+        parts = [p[..., k * D:(k + 1) * D] for k in range(n)]
+    else:
+        parts = [rnd(b, L, D).clamp(-4, 4).to(TYPES[io]) for _ in range(n)]
+    t["x"], t["ga"], t["gx"] = parts[:3]
+    t["z"] = parts[3] if z else None
+    t["A"] = -torch.exp(-4.8 * torch.rand(D, generator=g)) if A is None else A
+    t["ba"] = rnd(D).clamp(-2, 2) if bias else None
+    t["bx"] = rnd(D).clamp(-2, 2) if bias else None
+    t["h0"] = rnd(b, D) if h0 else None
+    t["lens"] = None if lens is None else torch.tensor(lens, dtype=torch.int32)
+    t["dy"] = rnd(b, L, D).to(TYPES[io])
+    t["dh_last"] = rnd(b, D)
+    return t
+
+
+def up(t):
+    """The same tensors on the GPU with the same strides."""
+    out = {}
+    for k, v in t.items():
+        if v is None:
+            out[k] = None
+        elif k in ("x", "ga", "gx", "z") and v.storage_offset() + v.numel() != v.untyped_storage().nbytes() // v.element_size():
+            base = torch.as_strided(v, (v.untyped_storage().nbytes() // v.element_size(),), (1,), 0).cuda()
+            out[k] = torch.as_strided(base, v.shape, v.stride(), v.storage_offset())
+        else:
+            out[k] = v.cuda()
+    return out
+
+
+def forward(c, **kw):
+    return ssm.gated_scan_fwd(c["x"], c["ga"], c["gx"], c["A"], c["ba"], c["bx"], z=c["z"], h0=c["h0"],
+                              lens=c["lens"], **kw)
+
+
+def backward(c, **kw):
+    return ssm.gated_scan_bwd(c["dy"], c["x"], c["ga"], c["gx"], c["A"], c["ba"], c["bx"], z=c["z"], h0=c["h0"],
+                              lens=c["lens"], dh_last=c["dh_last"], **kw)
+
+
+def check_all(t, c, y, h_last, grads, what):
+    L, b = t["x"].shape[1], t["x"].shape[0]
+    want = ref.gated(t["x"], t["ga"], t["gx"], t["A"], t["ba"], t["bx"], t["z"], t["h0"], t["lens"], t["dy"],
+                     t["dh_last"])
+    rs, rg, ra = ref.rel_state(L, t["A"]), ref.rel_grad(L, t["A"]), ref.rel_sum(L, b)
+    ref.check(y, want["y"], want["mag_y"], rs, what + " y")
+    if h_last is not None:
+        ref.check(h_last, want["h_last"], want["mag_h_last"], rs, what + " h_last")
+    if grads is None:
+        return
+    names = ["dx", "dgate_a", "dgate_x", "dA"] + (["dz"] if t["z"] is not None else []) + \
+        (["dbias_a", "dbias_x"] if t["ba"] is not None else []) + (["dh0"] if t["h0"] is not None else [])
+    assert sorted(grads) == sorted(names)
+    for k in names:
+        ref.check(grads[k], want[k], want["mag_" + k], rg + (ra if k in ("dA", "dbias_a", "dbias_x") else 0),
+                  what + " " + k)
+
+
+SIZES = [
+    # (batch, L, D)
+    (1, 1, 1), (2, 1, 64), (1, 2, 33), (3, 8, 66), (2, 15, 32), (1, 16, 65), (2, 17, 31), (1, 63, 128), (2, 64, 62),
+    (1, 65, 2), (1, 127, 64), (2, 128, 3), (1, 129, 130), (1, 255, 64), (2, 256, 34), (1, 257, 64), (1, 1023, 5),
+    (2, 1025, 64),
+]
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("size", SIZES, ids=lambda s: "x".join(map(str, s)))
+def test_forward_backward(size, io):
+    banner("gated %s %s" % (size, io))
+    t = make(*size, io, z=size[1] % 2 == 1, h0=size[0] == 2, bias=size[2] != 3, seed=sum(size))
+    c = up(t)
+    ckpt = ssm.gated_scan_ckpt(*size)
+    y, h = forward(c, want_hlast=True, ckpt=ckpt)
+    check_all(t, c, y, h, backward(c, ckpt=ckpt), "from checkpoints")
+    y2, none = forward(c)
+    assert none is None and torch.equal(y, y2)
+    check_all(t, c, y, h, backward(c), "recomputed")
+
+
+def test_sequence_split():
+    """Few channels and many steps: the sequence is cut into segments, forward
+    and backward, with a ragged end and a length inside an early segment."""
+    b, L, D = 2, 5000, 40
+    t = make(b, L, D, "f32", lens=[5000, 1300], seed=3)
+    c = up(t)
+    d = ssm.GatedDesc()
+    for k, v in zip(("batch", "seqlen", "dim"), (b, L, D)):
+        setattr(d, k, v)
+    ckpt = ssm.gated_scan_ckpt(b, L, D)
+    y, h = forward(c, want_hlast=True, ckpt=ckpt)
+    check_all(t, c, y, h, backward(c, ckpt=ckpt), "split")
+    check_all(t, c, y, h, backward(c), "split, recomputed")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("lens", [[0, 1, 2], [16, 300, 17], [300, 300, 300], [-5, 1000, 128], [0, 0, 0]],
+                         ids=lambda v: "_".join(map(str, v)))
+def test_lengths(io, lens):
+    """Rows of every length, with infinities and NaN behind their end: those
+    change nothing, y and the gradients there are zeros, and h_last and dh0
+    pass through (lengths out of range are taken into [0, L])."""
+    banner("gated lens %s %s" % (lens, io))
+    b, L, D = 3, 300, 70
+    t = make(b, L, D, io, lens=lens, seed=5)
+    for k in ("x", "ga", "gx", "z", "dy"):
+        t[k] = t[k].clone()
+        for r, n in enumerate(lens):
+            n = min(max(n, 0), L)
+            t[k][r, n:] = float("nan")
+            t[k][r, n::3] = float("inf")
+    c = up(t)
+    y, h = forward(c, want_hlast=True)
+    grads = backward(c)
+    check_all(t, c, y, h, grads, "lens")
+    for r, n in enumerate(lens):
+        n = min(max(n, 0), L)
+        for k in (y, grads["dx"], grads["dgate_a"], grads["dgate_x"], grads["dz"]):
+            assert not k[r, n:].any()
+        if n == 0:
+            assert torch.equal(h[r], c["h0"][r]) and torch.equal(grads["dh0"][r], c["dh_last"][r])
+
+
+def test_fp32_outputs_from_bf16():
+    """bf16 inputs with fp32 y and fp32 gradients."""
+    t = make(2, 200, 96, "bf16", seed=7)
+    c = up(t)
+    c["dy"] = c["dy"].float()
+    y, h = forward(c, want_hlast=True, y_dtype=torch.float32)
+    g = backward(c)
+    assert y.dtype == g["dx"].dtype == g["dz"].dtype == torch.float32
+    check_all(t, c, y, h, g, "fp32")
+
+
+def test_strides_and_neighbours():
+    """Batch-strided, time-strided and broadcast inputs, A shared by stride 0;
+    y inside a sentinel-filled buffer leaves its neighbours alone."""
+    b, L, D = 2, 70, 36
+    t = make(b, L, D, "f32", seed=9, z=False, pack=False, A=torch.tensor([-0.3]).expand(D))
+    wide = torch.randn(b, 2 * L, D + 6)
+    t["x"] = wide[:, ::2, 3:3 + D]            # every other step, rows on no pair
+    t["ga"] = t["ga"][:1].expand(b, L, D)     # one row for the whole batch
+    c = {k: (v.cuda() if v is not None else None) for k, v in t.items()}
+    wd = wide.cuda()
+    c["x"] = wd[:, ::2, 3:3 + D]
+    c["ga"] = t["ga"][:1].contiguous().cuda().expand(b, L, D)
+    c["A"] = torch.tensor([-0.3], device="cuda").expand(D)
+    buf = torch.full((b, L + 2, D + 10), 777.0, device="cuda")
+    y, h = forward(c, want_hlast=True, y=buf[:, 1:L + 1, 5:5 + D])
+    check_all(t, c, y, h, backward(c), "strided")
+    inside = torch.zeros_like(buf, dtype=torch.bool)
+    inside[:, 1:L + 1, 5:5 + D] = True
+    assert bool((buf[~inside] == 777.0).all())
+
+
+def test_decay_limits():
+    """A = 0 keeps the state (nothing enters it) and has a finite gradient; a
+    decay of exp(-60) forgets; A > 0 takes in nothing; gates at +-100."""
+    b, L, D = 1, 40, 4
+    t = make(b, L, D, "f32", z=False, bias=False, seed=11, A=torch.tensor([0.0, -60.0, -1e-6, 0.01]))
+    t["ga"] = torch.full((b, L, D), 100.0)
+    t["ga"][:, ::2] = -100.0
+    t["gx"] = torch.full((b, L, D), 100.0)
+    c = up(t)
+    y, h = forward(c, want_hlast=True)
+    g = backward(c)
+    want = ref.gated(t["x"], t["ga"], t["gx"], t["A"], h0=t["h0"])
+    assert torch.equal(y[..., 0], c["h0"][:, :1].expand(b, L))
+    ref.check(y, want["y"], want["mag_y"], (64 + 4 * L) * 2.0 ** -23, "limits y", floor=1e-30)
+    for k, v in g.items():
+        assert bool(torch.isfinite(v).all()), k
+
+
+def test_nan_propagates():
+    """A NaN of a live step reaches that channel's later outputs and no other channel."""
+    t = make(1, 40, 8, "f32", seed=12, z=False, pack=False)
+    t["x"][0, 10, 3] = float("nan")
+    y, h = forward(up(t), want_hlast=True)
+    bad = torch.isnan(y).cpu()
+    want = torch.zeros_like(bad)
+    want[0, 10:, 3] = True
+    assert torch.equal(bad, want) and torch.equal(torch.isnan(h).cpu()[0], want[0, -1])
+
+
+def test_gradients_against_differences():
+    """Central differences of the fp64 definition along random directions."""
+    b, L, D = 2, 37, 6
+    t = make(b, L, D, "f32", seed=13, lens=[37, 20])
+    c = up(t)
+    grads = backward(c)
+    names = {"x": "dx", "ga": "dgate_a", "gx": "dgate_x", "z": "dz", "A": "dA", "ba": "dbias_a", "bx": "dbias_x",
+             "h0": "dh0"}
+
+    def loss(v):
+        o = ref.gated(v["x"], v["ga"], v["gx"], v["A"], v["ba"], v["bx"], v["z"], v["h0"], v["lens"])
+        return float((o["y"] * t["dy"].double()).sum() + (o["h_last"] * t["dh_last"].double()).sum())
+
+    gen = torch.Generator().manual_seed(1)
+    for k, name in names.items():
+        d = torch.randn(t[k].shape, generator=gen, dtype=torch.float64)
+        e = 1e-5
+        hi, lo = dict(t), dict(t)
+        hi[k], lo[k] = t[k].double() + e * d, t[k].double() - e * d
+        diff = (loss(hi) - loss(lo)) / (2 * e)
+        got = float((grads[name].double().cpu() * d).sum())
+        scale = float((grads[name].double().cpu() * d).abs().sum())
+        # truncation e^2 f''' / 6 is below 1e-8 of the scale, rounding 1e-16 / e below 1e-10; fp32 gradients 1e-5
+        assert abs(diff - got) <= 2e-5 * scale, (k, diff, got, scale)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [(1, 1), (3, 7), (2, 64), (5, 513), (64, 1000)], ids=lambda s: "%dx%d" % s)
+def test_update(size, io):
+    """One step equals the scan of one step; in place and into another state."""
+    b, D = size
+    t = make(b, 1, D, io, seed=b + D)
+    want = ref.gated(t["x"], t["ga"], t["gx"], t["A"], t["ba"], t["bx"], t["z"], t["h0"])
+    c = up(t)
+    s = {k: c[k][:, 0] for k in ("x", "ga", "gx", "z")}
+    state, out = c["h0"].clone(), torch.full_like(c["h0"], 5.0)
+    y = ssm.gated_state_update(state, s["x"], s["ga"], s["gx"], c["A"], c["ba"], c["bx"], z=s["z"], state_out=out)
+    assert torch.equal(state, c["h0"])
+    rel = ref.rel_state(1, t["A"])
+    ref.check(y, want["y"][:, 0], want["mag_y"][:, 0], rel, "step y")
+    ref.check(out, want["h_last"], want["mag_h_last"], rel, "step state")
+    y2 = ssm.gated_state_update(state, s["x"], s["ga"], s["gx"], c["A"], c["ba"], c["bx"], z=s["z"])
+    assert torch.equal(y, y2) and torch.equal(state, out)
+    y32 = ssm.gated_state_update(out, s["x"], s["ga"], s["gx"], c["A"], y_dtype=torch.float32)
+    assert y32.dtype == torch.float32 and torch.equal(y32, out)
+
+
+def test_scan_then_steps():
+    """A scan's final state continued by single steps equals one longer scan."""
+    t = make(2, 40, 66, "f32", seed=21)
+    c = up(t)
+    y, h = forward(c, want_hlast=True)
+    cut = {k: (v[:, :33] if k in ("x", "ga", "gx", "z") else v) for k, v in c.items()}
+    y0, state = forward(cut, want_hlast=True)
+    ys = [y0] + [ssm.gated_state_update(state, c["x"][:, j], c["ga"][:, j], c["gx"][:, j], c["A"], c["ba"], c["bx"],
+                                        z=c["z"][:, j])[:, None] for j in range(33, 40)]
+    want = ref.gated(t["x"], t["ga"], t["gx"], t["A"], t["ba"], t["bx"], t["z"], t["h0"])
+    rel = ref.rel_state(40, t["A"])
+    ref.check(torch.cat(ys, 1), want["y"], want["mag_y"], rel, "steps y")
+    ref.check(state, want["h_last"], want["mag_h_last"], rel, "steps state")
