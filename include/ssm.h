@@ -105,6 +105,7 @@ typedef struct {
 #define SSM_HAS_RESIDUAL 65536u /* norm: add a residual (backward: add its gradient)  */
 #define SSM_HAS_ZERO 131072u   /* 4-bit weights: zero points                          */
 #define SSM_HAS_STATE_OUT 262144u /* gated decode: write the state to state_out       */
+#define SSM_NO_WAIT 524288u    /* gated scan: no workgroup waits for another          */
 
 /* ------------------------------------------------------------------ scan */
 
@@ -433,6 +434,13 @@ typedef struct {
  *              takes it with SSM_HAS_CKPT
  * io is SSM_F32 or SSM_BF16 and is the same for x, gate_a, gate_x, z.
  * Other flags are not accepted.  Outputs may not overlap inputs or each other.
+ * Segments of a sequence run side by side and pass the state on through the
+ * workspace, so two calls that may overlap in time need workspaces of their
+ * own.  A workgroup's wait for its predecessor is bounded; when it runs out
+ * (never in a call that has its workspace to itself) the workgroup computes
+ * the state that enters its segment from the start of the sequence, by the
+ * same operations.  SSM_NO_WAIT makes every workgroup do so: the same bits,
+ * at a cost that grows with the square of the length.
  * Limit: 256 rows of any (batch, seqlen, dim) tensor must span less than
  * 1 GiB (SSM_ERR_UNSUPPORTED otherwise). */
 #define SSM_GATED_CKPT_STEPS 64
@@ -478,8 +486,8 @@ typedef struct {
  *   ckpt     : the forward's checkpoints of the same inputs, read only, if
  *              SSM_HAS_CKPT; without the flag they are recomputed in the workspace
  * The sums over batch and time are fp32 partial sums added in a fixed order,
- * so the results are deterministic.  Outputs may not overlap inputs or each
- * other.  Workspace: ssm_gated_scan_bwd_workspace_size bytes, 256-byte
+ * so the results are deterministic.  SSM_NO_WAIT as in the forward.  Outputs
+ * may not overlap inputs or each other.  Workspace: ssm_gated_scan_bwd_workspace_size bytes, 256-byte
  * aligned.  Limit: the forward's span limit. */
 typedef struct {
   int64_t batch, seqlen, dim;

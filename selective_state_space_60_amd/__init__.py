@@ -24,7 +24,7 @@ SSM_HAS_Z, SSM_HAS_D, SSM_DISC_EULER, SSM_HAS_H0, SSM_WANT_HLAST = 1, 2, 4, 8, 1
 SSM_DELTA_SOFTPLUS, SSM_HAS_DELTA_BIAS, SSM_HAS_BIAS, SSM_SILU = 32, 64, 128, 256
 SSM_WANT_CKPT, SSM_HAS_CKPT, SSM_HAS_SSD_FWD = 512, 1024, 2048
 SSM_HAS_BIAS_A, SSM_HAS_BIAS_X, SSM_HAS_LENS, SSM_HAS_DHLAST = 4096, 8192, 16384, 32768
-SSM_HAS_RESIDUAL, SSM_HAS_ZERO, SSM_HAS_STATE_OUT = 65536, 131072, 262144
+SSM_HAS_RESIDUAL, SSM_HAS_ZERO, SSM_HAS_STATE_OUT, SSM_NO_WAIT = 65536, 131072, 262144, 524288
 ABI_VERSION = 5
 MAX_DIMS = 5
 
@@ -222,15 +222,13 @@ def lib() -> ctypes.CDLL:
         L.ssm_selective_scan_bwd.argtypes = [P(ScanBwdDesc), P(ScanBwdPtrs), vp, sz, vp]
         L.ssm_ssd_bwd_workspace_size.argtypes = [P(SSDBwdDesc), P(sz)]
         L.ssm_ssd_bwd.argtypes = [P(SSDBwdDesc), P(SSDBwdPtrs), vp, sz, vp]
-        L.ssm_gated_scan_workspace_size.argtypes = [P(GatedDesc), P(sz)]
-        L.ssm_gated_scan_fwd.argtypes = [P(GatedDesc), P(GatedPtrs), vp, sz, vp]
-        L.ssm_gated_scan_bwd_workspace_size.argtypes = [P(GatedBwdDesc), P(sz)]
-        L.ssm_gated_scan_bwd.argtypes = [P(GatedBwdDesc), P(GatedBwdPtrs), vp, sz, vp]
-        L.ssm_gated_state_update.argtypes = [P(GatedUpdateDesc), P(GatedUpdatePtrs), vp]
-        L.ssm_rms_norm_fwd.argtypes = [P(NormDesc), P(NormPtrs), vp]
-        L.ssm_rms_norm_bwd_workspace_size.argtypes = [P(NormBwdDesc), P(sz)]
-        L.ssm_rms_norm_bwd.argtypes = [P(NormBwdDesc), P(NormBwdPtrs), vp, sz, vp]
-        L.ssm_w4_matvec.argtypes = [P(W4Desc), P(W4Ptrs), vp]
+        # descriptors and pointer structs of these go by address (or as packed bytes)
+        for name in ("ssm_gated_scan", "ssm_gated_scan_bwd", "ssm_rms_norm_bwd"):
+            getattr(L, name + "_workspace_size").argtypes = [vp, P(sz)]
+        for name in ("ssm_gated_scan_fwd", "ssm_gated_scan_bwd", "ssm_rms_norm_bwd"):
+            getattr(L, name).argtypes = [vp, vp, vp, sz, vp]
+        for name in ("ssm_gated_state_update", "ssm_rms_norm_fwd", "ssm_w4_matvec"):
+            getattr(L, name).argtypes = [vp, vp, vp]
         for name in EXPORTS[3:]:
             getattr(L, name).restype = ctypes.c_int
         if L.ssm_abi_version() != ABI_VERSION:

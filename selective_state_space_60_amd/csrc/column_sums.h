@@ -1,0 +1,41 @@
+// Sums of per-workgroup partial rows, in a fixed order (deterministic).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace ssm {
+
+// out_y[c] = sum over k < parts of part[k * stride + y * D + c], for the up to
+// three outputs y that are not null.  A workgroup takes 32 columns; 32 threads
+// share a column's parts, so a thread adds parts / 32 loads that do not wait
+// for each other, and the 32 runs are added in order.
+static __global__ __launch_bounds__(1024) void column_sums_kernel(const float* part, int64_t parts, int64_t stride,
+                                                                  int64_t D, float* out0, float* out1, float* out2) {
+  __shared__ float lds[32][33];
+  const int lane = threadIdx.x % 32, run = threadIdx.x / 32;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+  float* const out = blockIdx.y == 0 ? out0 : blockIdx.y == 1 ? out1 : out2;
+  if (!out) return;  // block-uniform
+  float sum = 0.f;
+  if (c < D) {
+    const float* src = part + blockIdx.y * D + c;
+#pragma unroll 8
+    for (int64_t k = run; k < parts; k += 32) sum += src[k * stride];
+  }
+  lds[run][lane] = sum;
+  __syncthreads();
+  if (run == 0 && c < D) {
+#pragma unroll
+    for (int k = 1; k < 32; ++k) sum += lds[k][lane];
+    out[c] = sum;
+  }
+}
+
+static inline void launch_column_sums(const float* part, int64_t parts, int64_t stride, int64_t D, float* out0,
+                                      float* out1, float* out2, hipStream_t stream) {
+  hipLaunchKernelGGL(column_sums_kernel, dim3((unsigned)((D + 31) / 32), out1 || out2 ? 3 : 1), dim3(1024), 0, stream,
+                     part, parts, stride, D, out0, out1, out2);
+}
+
+}  // namespace ssm

@@ -5,42 +5,59 @@
 //
 // One fp32 state per channel and 6-8 transcendentals per element, so memory
 // and VALU issue are close: every stream is read once and written once, and
-// nothing is recomputed across workgroups unless the sequence is split.
+// nothing is computed twice.
 //
-// Time is parallel inside a workgroup.  A workgroup owns 64 channels (32
-// lanes of two) and walks the sequence in rounds of 16 chunks; each half-wave
-// holds one chunk of T consecutive steps in registers.  It scans its chunk
-// from zero to the pair (P, H) = (product of decays, end state), the pairs of
-// the 16 chunks are exchanged through LDS, every lane folds them in order
+// A workgroup owns 64 channels (32 lanes of two) over one segment of 16
+// chunks.  Each half-wave holds one chunk of T consecutive steps in registers
+// and scans it from zero to the pair (P, H) = (product of decays, end state).
+// The first wave, a channel a lane, folds the 16 pairs through LDS
 //   h <- P h + H
-// to the state that enters its chunk (and the state after the round), and the
-// chunk is walked again from registers with the true state.  One barrier a
-// round: the exchange buffer alternates.
+// to the segment's own pair, finds the state that enters the segment, and
+// hands every chunk the state that enters it; the chunks are then walked again
+// from registers with the true state.
 //
-// The backward runs the rounds from the end.  Forward states come from the
+// The segments of one sequence run side by side.  A workgroup publishes its
+// pair as soon as it has it and its end state once it knows the state that
+// enters it, each in a word that says by itself whether it has been written.
+// To find the entering state a workgroup goes back over its predecessors,
+// eight at a time, to the nearest published end state and folds the pairs
+// since then forward from it: the same operations in the same order whichever
+// state it finds, so the result does not depend on timing.  Workgroups are
+// dispatched in order (a layer of all tiles after another, a tile always on
+// the same XCD), so those waited for are running or done.  The wait is bounded
+// all the same: a workgroup that runs out of polls computes the entering state
+// itself, from the start of the sequence, by the same operations.
+//
+// The backward takes the segments from the end.  Forward states come from the
 // checkpoints (every 64th step) and the same fold; the adjoint
 //   lam_t = g_t + m_t,  m_{t-1} = a_t lam_t
-// is affine in the carry m as well, with the same product P, and is folded
-// from the other end in the same exchange.
+// is affine in the carry m as well, with the same product P, and its carry is
+// found among the later segments in the same way.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
 
+#include "column_sums.h"
 #include "ssm_internal.h"
+
+// A segment's pair comes out the same from every variant of a kernel: products
+// and sums are contracted where an fma is written, nowhere else.
+#pragma clang fp contract(off)
 
 namespace ssm {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int LC = kGatedLanes;
+constexpr int LC = 32;  // lanes per chunk
 constexpr int NCH = kGatedChunks;
 constexpr int NT = LC * NCH;
 constexpr int kFwdT = kGatedFwdSteps;
 constexpr int kBwdT = kGatedBwdSteps;
-constexpr int kBwdRound = NCH * kBwdT;
-static_assert(kGatedCkptSteps % kFwdT == 0 && (NCH * kFwdT) % kGatedCkptSteps == 0, "checkpoints fall on chunks");
-static_assert(kBwdRound % kGatedCkptSteps == 0, "every backward round starts at a checkpoint");
-static_assert(kGatedRound % kBwdRound == 0, "segments hold whole rounds of both passes");
+constexpr int kFwdSeg = NCH * kFwdT;
+constexpr int kBwdSeg = NCH * kBwdT;
+static_assert(kGatedCkptSteps % kFwdT == 0 && kFwdSeg % kGatedCkptSteps == 0, "checkpoints fall on chunks");
+static_assert(kBwdSeg % kGatedCkptSteps == 0, "every backward segment starts at a checkpoint");
+static_assert(kFwdSeg <= kGatedSpanSteps && kBwdSeg <= kGatedSpanSteps, "a segment's rows fit the offsets");
 
 constexpr uint32_t kRsrcWord3 = 0x00020000u;  // raw (unformatted) buffer access
 constexpr uint32_t kMaxRange = 0x40000000u;   // the host keeps a round's rows below this
@@ -124,8 +141,10 @@ __device__ __forceinline__ float one_minus_sq(float t, float a) {
   q = __builtin_fmaf(q, t, -0.44392627f);
   q = __builtin_fmaf(q, t, -0.96090275f);
   q = __builtin_fmaf(q, t, -1.38629436f);
-  const float d = __builtin_fmaf(-a, a, 1.f);
-  return fmaxf(fabsf(t) < 0.25f ? t * q : d, 0.f);
+  // the clamps to [0, 1] are modifiers of the product and of the fma
+  const float n = __builtin_amdgcn_fmed3f(t * q, 0.f, 1.f);
+  const float d = __builtin_amdgcn_fmed3f(__builtin_fmaf(-a, a, 1.f), 0.f, 1.f);
+  return fabsf(t) < 0.25f ? n : d;
 }
 
 // The per-channel constants of a lane.
@@ -164,6 +183,8 @@ struct Stream {
                                       int64_t L, int64_t D, int e, int T, int chunk, int lane_elem, bool ok) {
     r = rows_from(p, sb, st, b, t0, c0, L, D, e);
     row = (uint32_t)(st * e);
+    // keep j * row inside the round: hoisted, the offsets of five streams spill the scalar registers
+    asm volatile("" : "+s"(row));
     off = ok ? (uint32_t)(chunk * T) * row + (uint32_t)(lane_elem * e) : kFar;
   }
 };
@@ -181,49 +202,163 @@ __device__ __forceinline__ void store_row(const Stream& s, int j, int n, const f
   else store<F32, V>(s.r, s.off, (uint32_t)j * s.row, o);
 }
 
-// ------------------------------------------------------------------- forward
-// kOut writes y (and h_last, checkpoints); kCkpt only the checkpoints; kAgg
-// only the pair (P, H) of segments 0 .. n_seg-2 of a split sequence.
-enum Mode { kOut, kCkpt, kAgg };
+// ------------------------------------------------------------------ segments
+// Words of the segments of one sequence: agg holds (P, H) of a segment, inc
+// its end state.  All bits set means not yet written (the launch fills them);
+// a NaN that is published has other bits.
+struct Chain {
+  unsigned long long* agg;
+  uint32_t* inc;
+  int64_t step;  // words from one segment to the next
+  int polls;     // bound of the wait
+};
 
-template <bool BF16, bool YF32, bool Z, int V, Mode M>
-struct Fwd {
+constexpr int kBack = 8;    // predecessors read at once
+constexpr int kStack = 32;  // pairs kept while going back; a multiple of kBack
+
+__device__ __forceinline__ uint32_t bits_of(float v) { return v != v ? 0x7FC00000u : __float_as_uint(v); }
+
+__device__ __forceinline__ void publish_pair(const Chain& q, int64_t at, float P, float H) {
+  const unsigned long long w = (unsigned long long)bits_of(H) << 32 | bits_of(P);
+  __hip_atomic_store(q.agg + at, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+__device__ __forceinline__ void publish_state(const Chain& q, int64_t at, float h) {
+  __hip_atomic_store(q.inc + at, bits_of(h), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// One wave, a channel per lane (`ok`: the lane has one): the state that enters
+// segment k >= 1, whose word index is `at`.  False when the polls ran out.
+template <int CW>
+__device__ __forceinline__ bool entering(const Chain& q, int64_t k, int64_t at, bool ok, float2 (&stack)[kStack][CW],
+                                         int lane, float& h) {
+  int depth = 0, polls = q.polls;
+  int64_t j = k - 1;
+  at -= q.step;
+  while (true) {
+    uint32_t s[kBack];
+    unsigned long long w[kBack];
+#pragma unroll
+    for (int i = 0; i < kBack; ++i) {
+      const bool in = ok && j - i >= 0;
+      s[i] = in ? __hip_atomic_load(q.inc + at - i * q.step, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0u;
+      w[i] = in ? __hip_atomic_load(q.agg + at - i * q.step, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0ull;
+    }
+    int used = 0;
+    bool found = false, stop = false;
+#pragma unroll
+    for (int i = 0; i < kBack; ++i)
+      if (!found && !stop) {  // wave-uniform
+        if (__all(s[i] != 0xFFFFFFFFu)) {
+          found = true;
+          h = __uint_as_float(s[i]);
+        } else if (depth + used < kStack && __all((uint32_t)w[i] != 0xFFFFFFFFu)) {
+          if (lane < CW)
+            stack[depth + used][lane] = make_float2(__uint_as_float((uint32_t)w[i]),
+                                                    __uint_as_float((uint32_t)(w[i] >> 32)));
+          ++used;
+        } else {
+          stop = true;
+        }
+      }
+    depth += used;
+    j -= used;
+    at -= used * q.step;
+    if (found) break;
+    if (used == 0) {
+      if (--polls <= 0) return false;
+      __builtin_amdgcn_s_sleep(2);
+    }
+  }
+  // own writes of this lane: no barrier between them and these reads
+  for (int d = depth - 1; d >= 0; --d)
+    if (lane < CW) h = __builtin_fmaf(stack[d][lane].x, h, stack[d][lane].y);
+  return true;
+}
+
+// Fills the words: 16 bytes a thread.
+__global__ __launch_bounds__(256) void gated_fill_kernel(uint4* words, int64_t n) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < n) words[i] = uint4{0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
+}
+
+// Where a workgroup is: tile, batch row, segment, and the lane's place in it.
+// grid.x holds all tiles of all rows (padded to a multiple of 8, so that a
+// tile keeps its XCD from segment to segment), grid.y and z the segments.
+template <int V>
+struct Place {
+  static constexpr int CW = LC * V;  // channels of the tile
+  int64_t b, c0, c, len;             // c: the lane's first channel
+  int64_t k;                         // the segment's place in the order of work
+  int lane, chunk;
+  bool ok;
+
+  __device__ __forceinline__ bool set(const GatedParams& p, unsigned tiles, int64_t nseg) {
+    const unsigned tile = blockIdx.x % tiles;
+    b = blockIdx.x / tiles;
+    k = (int64_t)blockIdx.z * gridDim.y + blockIdx.y;
+    if (b >= p.batch || k >= nseg) return false;  // block-uniform
+    lane = threadIdx.x % LC;
+    chunk = threadIdx.x / LC;
+    c0 = (int64_t)tile * CW;
+    c = c0 + lane * V;
+    ok = c < p.D;  // with V == 2 the channels are even: a lane is all in or all out
+    len = row_len(p, b);
+    return true;
+  }
+};
+
+// ------------------------------------------------------------------- forward
+template <bool BF16, bool YF32, bool Z, int V, bool Y>
+struct Fwd : Place<V> {
+  using Place<V>::CW;
+  using Place<V>::b;
+  using Place<V>::c0;
+  using Place<V>::c;
+  using Place<V>::len;
+  using Place<V>::k;
+  using Place<V>::lane;
+  using Place<V>::chunk;
+  using Place<V>::ok;
   static constexpr int E = BF16 ? 2 : 4;
   static constexpr int YE = (YF32 || !BF16) ? 4 : 2;
   static constexpr int T = kFwdT;
-  typedef float2 Pairs[NCH][LC * V];
+  static constexpr bool kZ = Z && Y;
+  struct Shared {
+    float2 pair[NCH][CW];
+    float2 stack[kStack][CW];
+    float in[NCH][CW];
+    int found;
+  };
 
   const GatedParams& p;
-  int64_t b, c0, c, len;
-  int lane, chunk;
-  bool ok;
   Chan<V> ch;
-  float h[V], P[V];  // state at the start of the round; product of the decays so far (kAgg)
+  Raw<BF16, V> zr[kZ ? T : 1];
+  float a[T][V], u[T][V];
 
   __device__ __forceinline__ Fwd(const GatedParams& q) : p(q) {}
 
-  template <bool MASK>
-  __device__ __forceinline__ void round(int64_t t0, Pairs& lds) {
-    Stream sx, sa, sg, sz, sy;
-    sx.set(p.x, p.xs_b, p.xs_t, b, t0, c0, p.L, p.D, E, T, chunk, lane * V, ok);
+  // Decays and inputs of the chunk of the segment at t0 into a, u, and its pair into LDS.
+  template <bool MASK, bool WITH_Z>
+  __device__ __forceinline__ void scan_chunk(int64_t t0, Shared& sh) {
+    Stream sx, sa, sg, sz;
+    const int live = MASK ? clamp_steps(len - t0 - chunk * T, T) : T;  // steps that count
     sa.set(p.gate_a, p.gas_b, p.gas_t, b, t0, c0, p.L, p.D, E, T, chunk, lane * V, ok);
     sg.set(p.gate_x, p.gxs_b, p.gxs_t, b, t0, c0, p.L, p.D, E, T, chunk, lane * V, ok);
-    const int64_t t = t0 + chunk * T;
-    const int rows = MASK ? clamp_steps(p.L - t, T) : T;   // rows of the chunk inside the sequence
-    const int live = MASK ? clamp_steps(len - t, T) : T;   // steps that count
-    Raw<BF16, V> xr[T], ar[T], gr[T], zr[Z && M == kOut ? T : 1];
+    sx.set(p.x, p.xs_b, p.xs_t, b, t0, c0, p.L, p.D, E, T, chunk, lane * V, ok);
+    Raw<BF16, V> xr[T], ar[T], gr[T];
 #pragma unroll
     for (int j = 0; j < T; ++j) {
       ar[j] = load_row<MASK, BF16, V>(sa, j, live);
       gr[j] = load_row<MASK, BF16, V>(sg, j, live);
       xr[j] = load_row<MASK, BF16, V>(sx, j, live);
     }
-    if constexpr (Z && M == kOut) {
+    if constexpr (kZ && WITH_Z) {
       sz.set(p.z, p.zs_b, p.zs_t, b, t0, c0, p.L, p.D, E, T, chunk, lane * V, ok);
 #pragma unroll
       for (int j = 0; j < T; ++j) zr[j] = load_row<MASK, BF16, V>(sz, j, live);
     }
-    float a[T][V], u[T][V], cp[V], cH[V];
+    float cp[V], cH[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       cp[v] = 1.f;
@@ -246,26 +381,66 @@ struct Fwd {
         cH[v] = __builtin_fmaf(a[j][v], cH[v], u[j][v]);
       }
 #pragma unroll
-    for (int v = 0; v < V; ++v) lds[chunk][lane * V + v] = make_float2(cp[v], cH[v]);
+    for (int v = 0; v < V; ++v) sh.pair[chunk][lane * V + v] = make_float2(cp[v], cH[v]);
+  }
+
+  // The segment's pair, by the first wave.
+  __device__ __forceinline__ float2 fold(const Shared& sh, int ch_lane) const {
+    float2 f = make_float2(1.f, 0.f);
+#pragma unroll
+    for (int q = 0; q < NCH; ++q) {
+      const float2 w = sh.pair[q][ch_lane];
+      f.x *= w.x;
+      f.y = __builtin_fmaf(w.x, f.y, w.y);
+    }
+    return f;
+  }
+
+  // The whole segment.  `known`: h is the entering state (in the first wave's
+  // lanes); otherwise it is looked for, and false returned if it is not found.
+  template <bool MASK>
+  __device__ __forceinline__ bool segment(const Chain& q, Shared& sh, bool known, float h) {
+    const int64_t t0 = k * kFwdSeg, t = t0 + chunk * T;
+    const int rows = MASK ? clamp_steps(p.L - t, T) : T;  // rows of the chunk inside the sequence
+    const int live = MASK ? clamp_steps(len - t, T) : T;
+    scan_chunk<MASK, true>(t0, sh);
     __syncthreads();
+    if (threadIdx.x < 64) {
+      const int l = threadIdx.x;
+      const bool mine = l < CW && c0 + l < p.D;
+      const int64_t at = (k * p.batch + b) * p.D + c0 + l;
+      const float2 f = fold(sh, l < CW ? l : 0);
+      const bool more = (k + 1) * kFwdSeg < p.L;
+      if (more && k > 0 && mine) publish_pair(q, at, f.x, f.y);
+      bool found = known || k == 0;
+      if (!found) found = entering<CW>(q, k, at, mine, sh.stack, l, h);
+      if (found) {
+        if (mine) {
+          const float end = __builtin_fmaf(f.x, h, f.y);
+          if (more) publish_state(q, at, end);
+          else if (Y && p.h_last) p.h_last[b * p.D + c0 + l] = end;
+        }
+        if (l < CW)
+#pragma unroll
+          for (int i = 0; i < NCH; ++i) {
+            sh.in[i][l] = h;
+            h = __builtin_fmaf(sh.pair[i][l].x, h, sh.pair[i][l].y);
+          }
+      }
+      if (l == 0) sh.found = found;
+    }
+    __syncthreads();
+    if (!sh.found) return false;
     float in[V];
 #pragma unroll
-    for (int k = 0; k < NCH; ++k)
+    for (int v = 0; v < V; ++v) in[v] = sh.in[chunk][lane * V + v];
+    if (p.ckpt && (chunk * T) % kGatedCkptSteps == 0 && ok && rows > 0) {
+      const int64_t nk = (p.L + kGatedCkptSteps - 1) / kGatedCkptSteps;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float2 w = lds[k][lane * V + v];
-        if (k == chunk) in[v] = h[v];
-        h[v] = __builtin_fmaf(w.x, h[v], w.y);
-        if constexpr (M == kAgg) P[v] *= w.x;
-      }
-    if constexpr (M != kAgg) {
-      if (p.ckpt && (chunk * T) % kGatedCkptSteps == 0 && ok && rows > 0) {
-        const int64_t nk = (p.L + kGatedCkptSteps - 1) / kGatedCkptSteps;
-#pragma unroll
-        for (int v = 0; v < V; ++v) p.ckpt[(b * nk + t / kGatedCkptSteps) * p.D + c + v] = in[v];
-      }
+      for (int v = 0; v < V; ++v) p.ckpt[(b * nk + t / kGatedCkptSteps) * p.D + c + v] = in[v];
     }
-    if constexpr (M == kOut) {
+    if constexpr (Y) {
+      Stream sy;
       sy.set(p.y, p.ys_b, p.ys_t, b, t0, c0, p.L, p.D, YE, T, chunk, lane * V, ok);
 #pragma unroll
       for (int j = 0; j < T; ++j) {
@@ -283,98 +458,80 @@ struct Fwd {
         store_row<MASK, YF32 || !BF16, V>(sy, j, rows, o);
       }
     }
+    return true;
   }
 };
 
-template <bool BF16, bool YF32, bool Z, int V, Mode M>
-__global__ __launch_bounds__(NT) void gated_fwd_kernel(GatedParams p, unsigned tiles) {
-  typedef Fwd<BF16, YF32, Z, V, M> F;
-  constexpr int R = NCH * kFwdT;
-  __shared__ typename F::Pairs lds[2];
-  const int nseg = M == kAgg ? p.n_seg - 1 : p.n_seg;
-  const unsigned tile = blockIdx.x % tiles;
-  const int64_t rest = blockIdx.x / tiles;
-  const int seg = (int)(rest % nseg);
+template <bool BF16, bool YF32, bool Z, int V, bool Y>
+__global__ __launch_bounds__(NT) void gated_fwd_kernel(GatedParams p, Chain q, unsigned tiles, int64_t nseg) {
+  typedef Fwd<BF16, YF32, Z, V, Y> F;
+  __shared__ typename F::Shared sh;
   F f(p);
-  f.b = rest / nseg;
-  f.lane = threadIdx.x % LC;
-  f.chunk = threadIdx.x / LC;
-  f.c0 = (int64_t)tile * LC * V;
-  f.c = f.c0 + f.lane * V;
-  f.ok = f.c < p.D;  // with V == 2 the channels are even: a lane is all in or all out
-  f.len = row_len(p, f.b);
+  if (!f.set(p, tiles, nseg)) return;
   f.ch.load(p, f.c, f.ok);
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    f.P[v] = 1.f;
-    f.h[v] = M != kAgg && p.h0 && f.ok ? p.h0[f.b * p.D + f.c + v] : 0.f;
+  const int l = threadIdx.x;  // the first wave's channels
+  const float h0 = p.h0 && l < F::CW && f.c0 + l < p.D ? p.h0[f.b * p.D + f.c0 + l] : 0.f;
+  if (q.polls > 0 || f.k == 0) {
+    if ((f.k + 1) * kFwdSeg <= f.len ? f.template segment<false>(q, sh, false, h0)
+                                     : f.template segment<true>(q, sh, false, h0))
+      return;
   }
-  if constexpr (M != kAgg) {
-    for (int s = 0; s < seg; ++s)  // the state that enters the segment
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (f.ok) {
-          const float2 w = p.agg[(f.b * (p.n_seg - 1) + s) * p.D + f.c + v];
-          f.h[v] = __builtin_fmaf(w.x, f.h[v], w.y);
-        }
-  }
-  const int64_t ts = (int64_t)seg * p.seg_len;
-  const int64_t te = min(p.L, ts + p.seg_len);
-  int buf = 0;
-  for (int64_t t0 = ts; t0 < te; t0 += R, buf ^= 1) {
-    if (t0 + R <= f.len) f.template round<false>(t0, lds[buf]);
-    else f.template round<true>(t0, lds[buf]);
-  }
-  if (f.chunk == 0 && f.ok) {
-    if constexpr (M == kAgg) {
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        p.agg[(f.b * (p.n_seg - 1) + seg) * p.D + f.c + v] = make_float2(f.P[v], f.h[v]);
-    } else if (p.h_last && seg == p.n_seg - 1) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) p.h_last[f.b * p.D + f.c + v] = f.h[v];
+  // Not found in time: the segments before this one, from the start.
+  float h = h0;
+  for (int64_t k = 0; k < f.k; ++k) {
+    __syncthreads();  // the last fold has read the pairs
+    f.template scan_chunk<true, false>(k * kFwdSeg, sh);
+    __syncthreads();
+    if (l < 64) {
+      const float2 w = f.fold(sh, l < F::CW ? l : 0);
+      h = __builtin_fmaf(w.x, h, w.y);
     }
   }
+  __syncthreads();
+  f.template segment<true>(q, sh, true, h);
 }
 
 // ------------------------------------------------------------------ backward
-// kGrads writes the gradients; kCarry only (P, O) of segments 1 .. n_seg-1 of
-// a split sequence: the carry out of a segment is P carry_in + O.
-enum BwdMode { kGrads, kCarry };
-
-template <bool BF16, bool GF32, bool Z, int V, BwdMode M>
-struct Bwd {
+template <bool BF16, bool GF32, bool Z, int V>
+struct Bwd : Place<V> {
+  using Place<V>::CW;
+  using Place<V>::b;
+  using Place<V>::c0;
+  using Place<V>::c;
+  using Place<V>::len;
+  using Place<V>::k;
+  using Place<V>::lane;
+  using Place<V>::chunk;
+  using Place<V>::ok;
   static constexpr int E = BF16 ? 2 : 4;
   static constexpr bool G32 = GF32 || !BF16;
   static constexpr int GE = G32 ? 4 : 2;
   static constexpr int T = kBwdT;
-  // decay product, end state from zero, carry out from a zero carry in
-  struct Agg {
-    float P[NCH][LC * V], H[NCH][LC * V], O[NCH][LC * V];
+  struct Shared {
+    float P[NCH][CW], H[NCH][CW], O[NCH][CW];  // decay product, end state from zero, carry out from a zero carry
+    float2 stack[kStack][CW];
+    float h[NCH][CW], m[NCH][CW];              // state and carry that enter each chunk
+    int found;
   };
 
   const GatedBwdParams& q;
   const GatedParams& p;
-  int64_t b, c0, c, len;
-  int lane, chunk;
-  bool ok;
   Chan<V> ch;
-  float A[V];
-  float m[V], P[V];                 // carry into the round's last step; decay product so far (kCarry)
-  float sA[V], sba[V], sbx[V];      // sums of dA, dgate_a, dgate_x over the lane's steps
+  // a, the input s i x (later the state before the step), g, r, i, 1 / s, 1 - a^2 and x of every step
+  float a[T][V], u[T][V], g[T][V], r[T][V], i[T][V], is[T][V], om[T][V], zf[Z ? T : 1][V];
+  Raw<BF16, V> xr[T];
 
   __device__ __forceinline__ Bwd(const GatedBwdParams& w) : q(w), p(w.f) {}
 
-  template <bool MASK>
-  __device__ __forceinline__ void round(int64_t t0, Agg& lds) {
+  // GRADS: everything of the chunk of the segment at t0; else only what the carry needs (a, g).
+  template <bool MASK, bool GRADS>
+  __device__ __forceinline__ void scan_chunk(int64_t t0, Shared& sh) {
     Stream sx, sa, sg, sz, sd;
-    const int64_t t = t0 + chunk * T;
-    const int rows = MASK ? clamp_steps(p.L - t, T) : T;
-    const int live = MASK ? clamp_steps(len - t, T) : T;
+    const int live = MASK ? clamp_steps(len - t0 - chunk * T, T) : T;
     sa.set(p.gate_a, p.gas_b, p.gas_t, b, t0, c0, p.L, p.D, E, T, chunk, lane * V, ok);
     sd.set(q.dy, q.dys_b, q.dys_t, b, t0, c0, p.L, p.D, GE, T, chunk, lane * V, ok);
     if constexpr (Z) sz.set(p.z, p.zs_b, p.zs_t, b, t0, c0, p.L, p.D, E, T, chunk, lane * V, ok);
-    Raw<BF16, V> xr[T], ar[T], gr[T], zr[Z ? T : 1];
+    Raw<BF16, V> ar[T], gr[T], zr[Z ? T : 1];
     Raw<!G32, V> dr[T];
 #pragma unroll
     for (int j = 0; j < T; ++j) {
@@ -382,8 +539,7 @@ struct Bwd {
       dr[j] = load_row<MASK, !G32, V>(sd, j, live);
       if constexpr (Z) zr[j] = load_row<MASK, BF16, V>(sz, j, live);
     }
-    float c_in[V];  // state that enters the round
-    if constexpr (M == kGrads) {
+    if constexpr (GRADS) {
       sx.set(p.x, p.xs_b, p.xs_t, b, t0, c0, p.L, p.D, E, T, chunk, lane * V, ok);
       sg.set(p.gate_x, p.gxs_b, p.gxs_t, b, t0, c0, p.L, p.D, E, T, chunk, lane * V, ok);
 #pragma unroll
@@ -391,12 +547,7 @@ struct Bwd {
         gr[j] = load_row<MASK, BF16, V>(sg, j, live);
         xr[j] = load_row<MASK, BF16, V>(sx, j, live);
       }
-      const int64_t nk = (p.L + kGatedCkptSteps - 1) / kGatedCkptSteps;
-#pragma unroll
-      for (int v = 0; v < V; ++v) c_in[v] = ok ? p.ckpt[(b * nk + t0 / kGatedCkptSteps) * p.D + c + v] : 0.f;
     }
-    // a, the input s i x (later the state before the step), g, r, i, 1 / s and 1 - a^2 of every step
-    float a[T][V], u[T][V], g[T][V], r[T][V], i[T][V], is[T][V], om[T][V], zf[Z && M == kGrads ? T : 1][V];
     float cp[V], cH[V], cM[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -407,30 +558,29 @@ struct Bwd {
     for (int j = 0; j < T; ++j)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const bool dead = MASK && j >= live;
         r[j][v] = gate(elem(ar[j], v), ch.nba[v]);
         const float e = r[j][v] * ch.al2[v];
         a[j][v] = __builtin_amdgcn_exp2f(e);
         const float dy = elem(dr[j], v);
         g[j][v] = dy;
         if constexpr (Z) {
-          const float z = elem(zr[j], v), sz_ = gate(z, 0.f);
-          g[j][v] = dy * (z * sz_);
-          if constexpr (M == kGrads) zf[j][v] = dy * (sz_ * __builtin_fmaf(z, 1.f - sz_, 1.f));
+          const float z = elem(zr[j], v), s = gate(z, 0.f);
+          g[j][v] = dy * (z * s);
+          if constexpr (GRADS) zf[j][v] = dy * (s * __builtin_fmaf(z, 1.f - s, 1.f));
         }
-        if constexpr (M == kGrads) {
+        if constexpr (GRADS) {
           i[j][v] = gate(elem(gr[j], v), ch.nbx[v]);
           om[j][v] = one_minus_sq(e, a[j][v]);
           is[j][v] = om[j][v] > 0.f ? __builtin_amdgcn_rsqf(om[j][v]) : 0.f;
           u[j][v] = om[j][v] * is[j][v] * (i[j][v] * elem(xr[j], v));
         }
-        if (dead) {
+        if (MASK && j >= live) {
           a[j][v] = 1.f;
           g[j][v] = 0.f;
-          if constexpr (M == kGrads) u[j][v] = 0.f;
+          if constexpr (GRADS) u[j][v] = 0.f;
         }
         cp[v] *= a[j][v];
-        if constexpr (M == kGrads) cH[v] = __builtin_fmaf(a[j][v], cH[v], u[j][v]);
+        if constexpr (GRADS) cH[v] = __builtin_fmaf(a[j][v], cH[v], u[j][v]);
       }
 #pragma unroll
     for (int j = T - 1; j >= 0; --j)
@@ -438,170 +588,165 @@ struct Bwd {
       for (int v = 0; v < V; ++v) cM[v] = a[j][v] * (g[j][v] + cM[v]);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      lds.P[chunk][lane * V + v] = cp[v];
-      lds.O[chunk][lane * V + v] = cM[v];
-      if constexpr (M == kGrads) lds.H[chunk][lane * V + v] = cH[v];
-    }
-    __syncthreads();
-    float mi[V];  // carry into the chunk's last step
-#pragma unroll
-    for (int k = NCH - 1; k >= 0; --k)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if (k == chunk) mi[v] = m[v];
-        const float w = lds.P[k][lane * V + v];
-        m[v] = __builtin_fmaf(w, m[v], lds.O[k][lane * V + v]);
-        if constexpr (M == kCarry) P[v] *= w;
-      }
-    if constexpr (M == kGrads) {
-      float h[V];
-#pragma unroll
-      for (int k = 0; k < NCH; ++k)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          if (k == chunk) h[v] = c_in[v];
-          c_in[v] = __builtin_fmaf(lds.P[k][lane * V + v], c_in[v], lds.H[k][lane * V + v]);
-        }
-      Stream so;
-      if constexpr (Z) so.set(q.dz, q.dzs_b, q.dzs_t, b, t0, c0, p.L, p.D, GE, T, chunk, lane * V, ok);
-#pragma unroll
-      for (int j = 0; j < T; ++j) {
-        float o[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float hn = __builtin_fmaf(a[j][v], h[v], u[j][v]);
-          u[j][v] = h[v];
-          h[v] = hn;
-          if constexpr (Z) o[v] = MASK && j >= live ? 0.f : hn * zf[j][v];
-        }
-        if constexpr (Z) store_row<MASK, G32, V>(so, j, rows, o);
-      }
-      Stream dx, da, dg;
-      dx.set(q.dx, q.dxs_b, q.dxs_t, b, t0, c0, p.L, p.D, GE, T, chunk, lane * V, ok);
-      da.set(q.dgate_a, q.dgas_b, q.dgas_t, b, t0, c0, p.L, p.D, GE, T, chunk, lane * V, ok);
-      dg.set(q.dgate_x, q.dgxs_b, q.dgxs_t, b, t0, c0, p.L, p.D, GE, T, chunk, lane * V, ok);
-#pragma unroll
-      for (int j = T - 1; j >= 0; --j) {
-        float ox[V], oa[V], og[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float x = elem(xr[j], v);
-          const float lam = g[j][v] + mi[v];
-          mi[v] = a[j][v] * lam;
-          // du = lam (a h_{t-1} - i x a^2 / s)
-          const float du = mi[v] * (u[j][v] - i[j][v] * x * a[j][v] * is[j][v]);
-          const float dv = lam * (om[j][v] * is[j][v]);
-          ox[v] = dv * i[j][v];
-          oa[v] = du * A[v] * __builtin_fmaf(-r[j][v], r[j][v], r[j][v]);
-          og[v] = dv * x * __builtin_fmaf(-i[j][v], i[j][v], i[j][v]);
-          float dA = du * r[j][v];
-          if (MASK && j >= live) ox[v] = oa[v] = og[v] = dA = 0.f;
-          sA[v] += dA;
-          sba[v] += oa[v];
-          sbx[v] += og[v];
-        }
-        store_row<MASK, G32, V>(dx, j, rows, ox);
-        store_row<MASK, G32, V>(da, j, rows, oa);
-        store_row<MASK, G32, V>(dg, j, rows, og);
-      }
+      sh.P[chunk][lane * V + v] = cp[v];
+      sh.O[chunk][lane * V + v] = cM[v];
+      if constexpr (GRADS) sh.H[chunk][lane * V + v] = cH[v];
     }
   }
-};
 
-template <bool BF16, bool GF32, bool Z, int V, BwdMode M>
-__global__ __launch_bounds__(NT) void gated_bwd_kernel(GatedBwdParams q, unsigned tiles) {
-  typedef Bwd<BF16, GF32, Z, V, M> F;
-  constexpr int R = kBwdRound;
-  __shared__ typename F::Agg lds[2];
-  const GatedParams& p = q.f;
-  const int nseg = M == kCarry ? p.n_seg - 1 : p.n_seg;
-  const unsigned tile = blockIdx.x % tiles;
-  const int64_t rest = blockIdx.x / tiles;
-  const int part = (int)(rest % nseg);
-  const int seg = M == kCarry ? part + 1 : part;
-  F f(q);
-  f.b = rest / nseg;
-  f.lane = threadIdx.x % LC;
-  f.chunk = threadIdx.x / LC;
-  f.c0 = (int64_t)tile * LC * V;
-  f.c = f.c0 + f.lane * V;
-  f.ok = f.c < p.D;
-  f.len = row_len(p, f.b);
-  f.ch.load(p, f.c, f.ok);
+  // The segment's pair for the carry, by the first wave.
+  __device__ __forceinline__ float2 fold(const Shared& sh, int l) const {
+    float2 f = make_float2(1.f, 0.f);
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    f.A[v] = f.ok ? p.A[(f.c + v) * p.As_d] : 0.f;
-    f.P[v] = 1.f;
-    f.m[v] = M == kGrads && q.dh_last && f.ok ? q.dh_last[f.b * p.D + f.c + v] : 0.f;
-    f.sA[v] = f.sba[v] = f.sbx[v] = 0.f;
+    for (int w = NCH - 1; w >= 0; --w) {
+      f.x *= sh.P[w][l];
+      f.y = __builtin_fmaf(sh.P[w][l], f.y, sh.O[w][l]);
+    }
+    return f;
   }
-  if constexpr (M == kGrads) {
-    for (int s = p.n_seg - 1; s > seg; --s)  // the carry that comes in from the later segments
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (f.ok) {
-          const float2 w = q.agg[(f.b * (p.n_seg - 1) + s - 1) * p.D + f.c + v];
-          f.m[v] = __builtin_fmaf(w.x, f.m[v], w.y);
-        }
-  }
-  const int64_t ts = (int64_t)seg * p.seg_len;
-  const int64_t te = min(p.L, ts + p.seg_len);
-  int buf = 0;
-  for (int64_t t0 = ts + (te - 1 - ts) / R * R; t0 >= ts; t0 -= R, buf ^= 1) {
-    if (t0 + R <= f.len) f.template round<false>(t0, lds[buf]);
-    else f.template round<true>(t0, lds[buf]);
-  }
-  if constexpr (M == kCarry) {
-    if (f.chunk == 0 && f.ok)
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        q.agg[(f.b * (p.n_seg - 1) + part) * p.D + f.c + v] = make_float2(f.P[v], f.m[v]);
-  } else {
-    if (q.dh0 && seg == 0 && f.chunk == 0 && f.ok)
-#pragma unroll
-      for (int v = 0; v < V; ++v) q.dh0[f.b * p.D + f.c + v] = f.m[v];
-    // the 16 chunks' sums, added in order by the first chunk's lanes
+
+  // Segment seg = nseg - 1 - k.  `known`: m is the carry into its last step.
+  template <bool MASK>
+  __device__ __forceinline__ bool segment(const Chain& cn, Shared& sh, int64_t seg, bool known, float m) {
+    const int64_t t0 = seg * kBwdSeg, t = t0 + chunk * T;
+    const int rows = MASK ? clamp_steps(p.L - t, T) : T;
+    const int live = MASK ? clamp_steps(len - t, T) : T;
+    scan_chunk<MASK, true>(t0, sh);
     __syncthreads();
-    typename F::Agg& w = lds[0];
+    if (threadIdx.x < 64) {
+      const int l = threadIdx.x;
+      const bool mine = l < CW && c0 + l < p.D;
+      const int64_t nk = (p.L + kGatedCkptSteps - 1) / kGatedCkptSteps;
+      float h = mine ? p.ckpt[(b * nk + t0 / kGatedCkptSteps) * p.D + c0 + l] : 0.f;
+      const int64_t at = (k * p.batch + b) * p.D + c0 + l;
+      const float2 f = fold(sh, l < CW ? l : 0);
+      if (seg > 0 && k > 0 && mine) publish_pair(cn, at, f.x, f.y);
+      bool found = known || k == 0;
+      if (!found) found = entering<CW>(cn, k, at, mine, sh.stack, l, m);
+      if (found) {
+        if (mine) {
+          const float end = __builtin_fmaf(f.x, m, f.y);
+          if (seg > 0) publish_state(cn, at, end);
+          else if (q.dh0) q.dh0[b * p.D + c0 + l] = end;
+        }
+        if (l < CW) {
+#pragma unroll
+          for (int w = 0; w < NCH; ++w) {
+            sh.h[w][l] = h;
+            h = __builtin_fmaf(sh.P[w][l], h, sh.H[w][l]);
+          }
+#pragma unroll
+          for (int w = NCH - 1; w >= 0; --w) {
+            sh.m[w][l] = m;
+            m = __builtin_fmaf(sh.P[w][l], m, sh.O[w][l]);
+          }
+        }
+      }
+      if (l == 0) sh.found = found;
+    }
+    __syncthreads();
+    if (!sh.found) return false;
+    float h[V], mi[V], A[V], sA[V], sba[V], sbx[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      w.P[f.chunk][f.lane * V + v] = f.sA[v];
-      w.H[f.chunk][f.lane * V + v] = f.sba[v];
-      w.O[f.chunk][f.lane * V + v] = f.sbx[v];
+      h[v] = sh.h[chunk][lane * V + v];
+      mi[v] = sh.m[chunk][lane * V + v];
+      A[v] = ok ? p.A[(c + v) * p.As_d] : 0.f;
+      sA[v] = sba[v] = sbx[v] = 0.f;
+    }
+    Stream so, dx, da, dg;
+    if constexpr (Z) so.set(q.dz, q.dzs_b, q.dzs_t, b, t0, c0, p.L, p.D, GE, T, chunk, lane * V, ok);
+#pragma unroll
+    for (int j = 0; j < T; ++j) {
+      float o[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float hn = __builtin_fmaf(a[j][v], h[v], u[j][v]);
+        u[j][v] = h[v];
+        h[v] = hn;
+        if constexpr (Z) o[v] = MASK && j >= live ? 0.f : hn * zf[j][v];
+      }
+      if constexpr (Z) store_row<MASK, G32, V>(so, j, rows, o);
+    }
+    dx.set(q.dx, q.dxs_b, q.dxs_t, b, t0, c0, p.L, p.D, GE, T, chunk, lane * V, ok);
+    da.set(q.dgate_a, q.dgas_b, q.dgas_t, b, t0, c0, p.L, p.D, GE, T, chunk, lane * V, ok);
+    dg.set(q.dgate_x, q.dgxs_b, q.dgxs_t, b, t0, c0, p.L, p.D, GE, T, chunk, lane * V, ok);
+#pragma unroll
+    for (int j = T - 1; j >= 0; --j) {
+      float ox[V], oa[V], og[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float x = elem(xr[j], v);
+        const float lam = g[j][v] + mi[v];
+        mi[v] = a[j][v] * lam;
+        // du = lam (a h_{t-1} - i x a^2 / s)
+        const float du = mi[v] * __builtin_fmaf(-(i[j][v] * x) * a[j][v], is[j][v], u[j][v]);
+        const float dv = lam * (om[j][v] * is[j][v]);
+        ox[v] = dv * i[j][v];
+        oa[v] = du * A[v] * __builtin_fmaf(-r[j][v], r[j][v], r[j][v]);
+        og[v] = dv * x * __builtin_fmaf(-i[j][v], i[j][v], i[j][v]);
+        float dA = du * r[j][v];
+        if (MASK && j >= live) ox[v] = oa[v] = og[v] = dA = 0.f;
+        sA[v] += dA;
+        sba[v] += oa[v];
+        sbx[v] += og[v];
+      }
+      store_row<MASK, G32, V>(dx, j, rows, ox);
+      store_row<MASK, G32, V>(da, j, rows, oa);
+      store_row<MASK, G32, V>(dg, j, rows, og);
+    }
+    // The 16 chunks' sums, added in order.  P, H and O were last read before
+    // the barrier.
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      sh.P[chunk][lane * V + v] = sA[v];
+      sh.H[chunk][lane * V + v] = sba[v];
+      sh.O[chunk][lane * V + v] = sbx[v];
     }
     __syncthreads();
-    if (f.chunk < 3 && f.ok) {
-      const auto& from = f.chunk == 0 ? w.P : f.chunk == 1 ? w.H : w.O;
+    if (chunk < 3 && ok) {
+      const auto& from = chunk == 0 ? sh.P : chunk == 1 ? sh.H : sh.O;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         float sum = 0.f;
 #pragma unroll
-        for (int k = 0; k < NCH; ++k) sum += from[k][f.lane * V + v];
-        q.part[((f.b * p.n_seg + seg) * 3 + f.chunk) * p.D + f.c + v] = sum;
+        for (int w = 0; w < NCH; ++w) sum += from[w][lane * V + v];
+        q.part[((k * p.batch + b) * 3 + chunk) * p.D + c + v] = sum;
       }
     }
+    return true;
   }
-}
+};
 
-// dA, dbias_a, dbias_x: the partial sums of every (row, segment) in a fixed
-// order: 8 interleaved runs per channel, then the runs.
-__global__ __launch_bounds__(256) void gated_sums_kernel(const float* part, int64_t parts, int64_t D, float* dA,
-                                                         float* dba, float* dbx) {
-  __shared__ float lds[8][32];
-  const int lane = threadIdx.x % 32, run = threadIdx.x / 32;
-  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
-  float* const out = blockIdx.y == 0 ? dA : blockIdx.y == 1 ? dba : dbx;
-  if (!out) return;  // block-uniform
-  float sum = 0.f;
-  if (c < D)
-    for (int64_t k = run; k < parts; k += 8) sum += part[(k * 3 + blockIdx.y) * D + c];
-  lds[run][lane] = sum;
-  __syncthreads();
-  if (run == 0 && c < D) {
-#pragma unroll
-    for (int k = 1; k < 8; ++k) sum += lds[k][lane];
-    out[c] = sum;
+template <bool BF16, bool GF32, bool Z, int V>
+__global__ __launch_bounds__(NT) void gated_bwd_kernel(GatedBwdParams q, Chain cn, unsigned tiles, int64_t nseg) {
+  typedef Bwd<BF16, GF32, Z, V> F;
+  __shared__ typename F::Shared sh;
+  const GatedParams& p = q.f;
+  F f(q);
+  if (!f.set(p, tiles, nseg)) return;
+  f.ch.load(p, f.c, f.ok);
+  const int l = threadIdx.x;
+  const int64_t seg = nseg - 1 - f.k;
+  const float m0 = q.dh_last && l < F::CW && f.c0 + l < p.D ? q.dh_last[f.b * p.D + f.c0 + l] : 0.f;
+  if (cn.polls > 0 || f.k == 0) {
+    if ((seg + 1) * kBwdSeg <= f.len ? f.template segment<false>(cn, sh, seg, false, m0)
+                                     : f.template segment<true>(cn, sh, seg, false, m0))
+      return;
   }
+  // Not found in time: the segments behind this one, from the end.
+  float m = m0;
+  for (int64_t s = nseg - 1; s > seg; --s) {
+    __syncthreads();
+    f.template scan_chunk<true, false>(s * kBwdSeg, sh);
+    __syncthreads();
+    if (l < 64) {
+      const float2 w = f.fold(sh, l < F::CW ? l : 0);
+      m = __builtin_fmaf(w.x, m, w.y);
+    }
+  }
+  __syncthreads();
+  f.template segment<true>(cn, sh, seg, true, m);
 }
 
 // ---------------------------------------------------------------- one token
@@ -652,19 +797,36 @@ bool pair_rows(const void* ptr, int e, int64_t sb, int64_t st) {
   return (uintptr_t)ptr % (2 * e) == 0 && sb % 2 == 0 && st % 2 == 0;
 }
 
+// The grid of all tiles and segments, and the chain's words in `ws`, filled.
+template <int V>
+dim3 seg_grid(const GatedParams& p, int64_t nseg, unsigned& tiles) {
+  tiles = (unsigned)((p.D + LC * V - 1) / (LC * V));
+  const int64_t y = std::min<int64_t>(nseg, 32768);
+  return dim3((unsigned)((tiles * p.batch + 7) / 8 * 8), (unsigned)y, (unsigned)((nseg + y - 1) / y));
+}
+
+Chain make_chain(const GatedParams& p, void* ws, int64_t nseg, hipStream_t stream) {
+  Chain q = {nullptr, nullptr, p.batch * p.D, p.polls};
+  if (nseg > 1) {
+    const int64_t words = nseg * q.step;
+    q.agg = (unsigned long long*)ws;
+    q.inc = (uint32_t*)(q.agg + words);
+    const int64_t n = gated_chain_bytes(p.batch, p.D, nseg) / 16;
+    hipLaunchKernelGGL(gated_fill_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream, (uint4*)ws, n);
+  }
+  return q;
+}
+
 template <bool BF16, bool YF32, bool Z, int V>
 void launch_fwd(const GatedParams& p, hipStream_t stream) {
-  const unsigned tiles = (unsigned)((p.D + LC * V - 1) / (LC * V));
-  const unsigned rows = (unsigned)(tiles * p.batch);
-  if (p.n_seg > 1)
-    hipLaunchKernelGGL((gated_fwd_kernel<BF16, false, false, V, kAgg>), dim3(rows * (p.n_seg - 1)), dim3(NT), 0,
-                       stream, p, tiles);
+  const int64_t nseg = (p.L + kFwdSeg - 1) / kFwdSeg;
+  unsigned tiles;
+  const dim3 grid = seg_grid<V>(p, nseg, tiles);
+  const Chain q = make_chain(p, p.chain, nseg, stream);
   if (p.y)
-    hipLaunchKernelGGL((gated_fwd_kernel<BF16, YF32, Z, V, kOut>), dim3(rows * p.n_seg), dim3(NT), 0, stream, p,
-                       tiles);
+    hipLaunchKernelGGL((gated_fwd_kernel<BF16, YF32, Z, V, true>), grid, dim3(NT), 0, stream, p, q, tiles, nseg);
   else
-    hipLaunchKernelGGL((gated_fwd_kernel<BF16, false, false, V, kCkpt>), dim3(rows * p.n_seg), dim3(NT), 0, stream,
-                       p, tiles);
+    hipLaunchKernelGGL((gated_fwd_kernel<BF16, false, false, V, false>), grid, dim3(NT), 0, stream, p, q, tiles, nseg);
 }
 
 template <bool BF16, bool YF32, int V>
@@ -683,15 +845,12 @@ void launch_fwd_io(const GatedParams& p, hipStream_t stream) {
 template <bool BF16, bool GF32, bool Z, int V>
 void launch_bwd(const GatedBwdParams& q, hipStream_t stream) {
   const GatedParams& p = q.f;
-  const unsigned tiles = (unsigned)((p.D + LC * V - 1) / (LC * V));
-  const unsigned rows = (unsigned)(tiles * p.batch);
-  if (p.n_seg > 1)
-    hipLaunchKernelGGL((gated_bwd_kernel<BF16, GF32, Z, V, kCarry>), dim3(rows * (p.n_seg - 1)), dim3(NT), 0, stream,
-                       q, tiles);
-  hipLaunchKernelGGL((gated_bwd_kernel<BF16, GF32, Z, V, kGrads>), dim3(rows * p.n_seg), dim3(NT), 0, stream, q,
-                     tiles);
-  hipLaunchKernelGGL(gated_sums_kernel, dim3((unsigned)((p.D + 31) / 32), 3), dim3(256), 0, stream, q.part,
-                     p.batch * p.n_seg, p.D, q.dA, q.dbias_a, q.dbias_x);
+  const int64_t nseg = (p.L + kBwdSeg - 1) / kBwdSeg;
+  unsigned tiles;
+  const dim3 grid = seg_grid<V>(p, nseg, tiles);
+  const Chain cn = make_chain(p, p.chain, nseg, stream);
+  hipLaunchKernelGGL((gated_bwd_kernel<BF16, GF32, Z, V>), grid, dim3(NT), 0, stream, q, cn, tiles, nseg);
+  launch_column_sums(q.part, p.batch * nseg, 3 * p.D, p.D, q.dA, q.dbias_a, q.dbias_x, stream);
 }
 
 template <bool BF16, bool GF32, int V>
@@ -716,14 +875,15 @@ void launch_update(const GatedUpdateParams& p, hipStream_t stream) {
   else hipLaunchKernelGGL((gated_update_kernel<true, false, V>), grid, dim3(256), 0, stream, p, tiles);
 }
 
-}  // namespace
-
+// Two channels per lane when every row starts on a whole pair.
 bool gated_pairs(const GatedParams& p) {
   const int e = p.io_bf16 ? 2 : 4, ye = p.y_f32 || !p.io_bf16 ? 4 : 2;
   return p.D % 2 == 0 && pair_rows(p.x, e, p.xs_b, p.xs_t) && pair_rows(p.gate_a, e, p.gas_b, p.gas_t) &&
          pair_rows(p.gate_x, e, p.gxs_b, p.gxs_t) && pair_rows(p.z, e, p.zs_b, p.zs_t) &&
          pair_rows(p.y, ye, p.ys_b, p.ys_t);
 }
+
+}  // namespace
 
 hipError_t launch_gated_scan(const GatedParams& p, hipStream_t stream) {
   if (gated_pairs(p)) launch_fwd_io<2>(p, stream);

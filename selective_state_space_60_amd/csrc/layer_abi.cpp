@@ -97,37 +97,35 @@ class Ptrs {
 
 // -------------------------------------------------------------- gated scan
 
-constexpr uint32_t kGatedInFlags = SSM_HAS_Z | SSM_HAS_H0 | SSM_HAS_BIAS_A | SSM_HAS_BIAS_X | SSM_HAS_LENS;
+constexpr uint32_t kGatedInFlags = SSM_HAS_Z | SSM_HAS_H0 | SSM_HAS_BIAS_A | SSM_HAS_BIAS_X | SSM_HAS_LENS |
+                                   SSM_NO_WAIT;
 constexpr uint32_t kGatedFlags = kGatedInFlags | SSM_WANT_HLAST | SSM_WANT_CKPT;
 constexpr uint32_t kGatedBwdFlags = kGatedInFlags | SSM_HAS_CKPT | SSM_HAS_DHLAST;
 
-// Split of the sequence over workgroups: only when batch x channels leave
-// compute units without one (a split reads the inputs twice), into segments
-// of whole rounds, at least four rounds long.
+// The sequence is cut into segments of 16 chunks, one workgroup each for a
+// tile of channels; with more than one, words pass the state on.
 struct GatedPlan {
-  int64_t nk = 0, seg_len = 0;
-  int n_seg = 1;
-  int64_t blocks = 0;
+  int64_t nk = 0, fwd_seg = 0, bwd_seg = 0;
+  int64_t blocks = 0;  // of one segment
 };
 
 GatedPlan plan_gated(int64_t batch, int64_t seqlen, int64_t dim) {
   GatedPlan pl;
-  pl.nk = (seqlen + ssm::kGatedCkptSteps - 1) / ssm::kGatedCkptSteps;
-  const int64_t tile = 2 * ssm::kGatedLanes;
-  const int64_t blocks = batch * ((dim + tile - 1) / tile);
-  const int64_t rounds = (seqlen + ssm::kGatedRound - 1) / ssm::kGatedRound;
-  int64_t n = 1;
-  if (blocks < 256) n = std::max<int64_t>(1, std::min<int64_t>(512 / blocks, rounds / 4));
-  pl.seg_len = (rounds + n - 1) / n * ssm::kGatedRound;
-  pl.n_seg = (int)((seqlen + pl.seg_len - 1) / pl.seg_len);
-  // one channel per lane (unaligned rows) takes twice the workgroups
-  pl.blocks = batch * ((dim + ssm::kGatedLanes - 1) / ssm::kGatedLanes) * pl.n_seg;
+  auto parts = [&](int64_t n) { return (seqlen + n - 1) / n; };
+  pl.nk = parts(ssm::kGatedCkptSteps);
+  pl.fwd_seg = parts(ssm::kGatedChunks * ssm::kGatedFwdSteps);
+  pl.bwd_seg = parts(ssm::kGatedChunks * ssm::kGatedBwdSteps);
+  pl.blocks = batch * ((dim + 31) / 32) + 7;  // at one channel per lane, rounded up to eight
   return pl;
 }
 
-// A round's rows must fit the 32-bit offsets of the kernel.
+bool gated_grid_ok(const GatedPlan& pl) {
+  return pl.blocks < kMaxBlocks512 && pl.bwd_seg < ((int64_t)1 << 30);
+}
+
+// A segment's rows must fit the 32-bit offsets of the kernel.
 bool gated_fits(const ssm_tensor_desc& t) {
-  return (ssm::kGatedRound * (__int128)t.stride[1] + 2 * ssm::kGatedLanes) * esize(t.dtype) < kMaxSpan;
+  return (ssm::kGatedSpanSteps * (__int128)t.stride[1] + 64) * esize(t.dtype) < kMaxSpan;
 }
 
 struct GatedShapes {
@@ -186,17 +184,13 @@ ssm_status validate_gated(const ssm_gated_desc* d) {
   SSM_TRY(check_out(d->flags & SSM_WANT_HLAST, d->h_last, 2, sh.bd, d->h_last.dtype == SSM_F32, false, true));
   SSM_TRY(check_out(d->flags & SSM_WANT_CKPT, d->ckpt, 3, sh.ck, d->ckpt.dtype == SSM_F32, false, true));
   if (!gated_fits(d->y)) return SSM_ERR_UNSUPPORTED;
-  if (plan_gated(d->batch, d->seqlen, d->dim).blocks >= kMaxBlocks512) return SSM_ERR_UNSUPPORTED;
+  if (!gated_grid_ok(plan_gated(d->batch, d->seqlen, d->dim))) return SSM_ERR_UNSUPPORTED;
   return SSM_OK;
-}
-
-int64_t gated_agg_bytes(const GatedPlan& pl, int64_t batch, int64_t dim) {
-  return round256(batch * (pl.n_seg - 1) * dim * 8);
 }
 
 // The kernel parameters of the inputs; what is left out stays null.
 template <class D, class P>
-ssm::GatedParams gated_params(const D& d, const P& p, const GatedPlan& pl) {
+ssm::GatedParams gated_params(const D& d, const P& p) {
   ssm::GatedParams q;
   std::memset(&q, 0, sizeof(q));
   const uint32_t f = d.flags;
@@ -215,26 +209,24 @@ ssm::GatedParams gated_params(const D& d, const P& p, const GatedPlan& pl) {
   if (q.bias_a) q.bas_d = d.bias_a.stride[0];
   if (q.bias_x) q.bxs_d = d.bias_x.stride[0];
   q.io_bf16 = d.x.dtype == SSM_BF16;
-  q.n_seg = pl.n_seg;
-  q.seg_len = pl.seg_len;
+  q.polls = (f & SSM_NO_WAIT) ? 0 : ssm::kGatedPolls;
   return q;
 }
 
 // Gated backward workspace, in this order: checkpoints (unless given), the
-// sums' partials, the split's aggregates (the checkpoint forward's first, then
+// sums' partials, the segments' words (the checkpoint forward's first, then
 // the carries': the forward is done with them by then).
 struct GatedBwdPlan {
-  GatedPlan g;
-  int64_t ws_ckpt = 0, ws_part = 0, ws_agg = 0, ws_total = 0;
+  int64_t ws_ckpt = 0, ws_part = 0, ws_chain = 0, ws_total = 0;
 };
 
 GatedBwdPlan plan_gated_bwd(const ssm_gated_bwd_desc& d) {
   GatedBwdPlan pl;
-  pl.g = plan_gated(d.batch, d.seqlen, d.dim);
-  pl.ws_ckpt = (d.flags & SSM_HAS_CKPT) ? 0 : round256(d.batch * pl.g.nk * d.dim * 4);
-  pl.ws_part = round256(d.batch * pl.g.n_seg * 3 * d.dim * 4);
-  pl.ws_agg = gated_agg_bytes(pl.g, d.batch, d.dim);
-  pl.ws_total = pl.ws_ckpt + pl.ws_part + pl.ws_agg;
+  const GatedPlan g = plan_gated(d.batch, d.seqlen, d.dim);
+  pl.ws_ckpt = (d.flags & SSM_HAS_CKPT) ? 0 : round256(d.batch * g.nk * d.dim * 4);
+  pl.ws_part = round256(d.batch * g.bwd_seg * 3 * d.dim * 4);
+  pl.ws_chain = ssm::gated_chain_bytes(d.batch, d.dim, std::max(g.fwd_seg, g.bwd_seg));
+  pl.ws_total = pl.ws_ckpt + pl.ws_part + pl.ws_chain;
   return pl;
 }
 
@@ -262,7 +254,7 @@ ssm_status validate_gated_bwd(const ssm_gated_bwd_desc* d) {
   if (!gated_fits(d->dy) || !gated_fits(d->dx) || !gated_fits(d->dgate_a) || !gated_fits(d->dgate_x) ||
       ((f & SSM_HAS_Z) && !gated_fits(d->dz)))
     return SSM_ERR_UNSUPPORTED;
-  if (plan_gated(d->batch, d->seqlen, d->dim).blocks >= kMaxBlocks512) return SSM_ERR_UNSUPPORTED;
+  if (!gated_grid_ok(plan_gated(d->batch, d->seqlen, d->dim))) return SSM_ERR_UNSUPPORTED;
   return SSM_OK;
 }
 
@@ -436,7 +428,7 @@ extern "C" {
 ssm_status ssm_gated_scan_workspace_size(const ssm_gated_desc* d, size_t* bytes) {
   if (!bytes) return SSM_ERR_NULL;
   SSM_TRY(validate_gated(d));
-  *bytes = (size_t)gated_agg_bytes(plan_gated(d->batch, d->seqlen, d->dim), d->batch, d->dim);
+  *bytes = (size_t)ssm::gated_chain_bytes(d->batch, d->dim, plan_gated(d->batch, d->seqlen, d->dim).fwd_seg);
   return SSM_OK;
 }
 
@@ -444,8 +436,7 @@ ssm_status ssm_gated_scan_fwd(const ssm_gated_desc* d, const ssm_gated_ptrs* p, 
                               size_t workspace_bytes, void* hip_stream) {
   SSM_TRY(validate_gated(d));
   if (!p) return SSM_ERR_NULL;
-  const GatedPlan pl = plan_gated(d->batch, d->seqlen, d->dim);
-  const int64_t need = gated_agg_bytes(pl, d->batch, d->dim);
+  const int64_t need = ssm::gated_chain_bytes(d->batch, d->dim, plan_gated(d->batch, d->seqlen, d->dim).fwd_seg);
   Ptrs a;
   SSM_TRY(take_gated_inputs(*d, *p, a));
   SSM_TRY(a.out(true, d->y, p->y));
@@ -454,13 +445,13 @@ ssm_status ssm_gated_scan_fwd(const ssm_gated_desc* d, const ssm_gated_ptrs* p, 
   SSM_TRY(a.check(need ? span_bytes(workspace, need) : Span()));
   if (need && (!workspace || workspace_bytes < (size_t)need)) return SSM_ERR_WORKSPACE;
   if (need && !aligned(workspace, 256)) return SSM_ERR_ALIGN;
-  ssm::GatedParams q = gated_params(*d, *p, pl);
+  ssm::GatedParams q = gated_params(*d, *p);
   q.y = p->y;
   q.ys_b = d->y.stride[0]; q.ys_t = d->y.stride[1];
   q.y_f32 = d->y.dtype == SSM_F32;
   q.h_last = (d->flags & SSM_WANT_HLAST) ? p->h_last : nullptr;
   q.ckpt = (d->flags & SSM_WANT_CKPT) ? p->ckpt : nullptr;
-  q.agg = (float2*)workspace;
+  q.chain = workspace;
   return hip_status(ssm::launch_gated_scan(q, (hipStream_t)hip_stream));
 }
 
@@ -483,11 +474,10 @@ ssm_status ssm_gated_scan_bwd(const ssm_gated_bwd_desc* d, const ssm_gated_bwd_p
   char* w = (char*)workspace;
   ssm::GatedBwdParams q;
   std::memset(&q, 0, sizeof(q));
-  q.f = gated_params(*d, *p, pl.g);
+  q.f = gated_params(*d, *p);
   q.f.ckpt = (f & SSM_HAS_CKPT) ? const_cast<float*>(p->ckpt) : (float*)w;  // given checkpoints are only read
   q.part = (float*)(w + pl.ws_ckpt);
-  q.agg = (float2*)(w + pl.ws_ckpt + pl.ws_part);
-  q.f.agg = q.agg;
+  q.f.chain = w + pl.ws_ckpt + pl.ws_part;
   q.dy = p->dy;
   q.dh_last = (f & SSM_HAS_DHLAST) ? p->dh_last : nullptr;
   q.dx = p->dx; q.dgate_a = p->dgate_a; q.dgate_x = p->dgate_x;

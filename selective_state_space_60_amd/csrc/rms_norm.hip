@@ -15,6 +15,7 @@
 
 #include <algorithm>
 
+#include "column_sums.h"
 #include "ssm_internal.h"
 
 namespace ssm {
@@ -341,24 +342,6 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormBwdParams p, int64_t r
   }
 }
 
-// dweight: the workgroups' sums in a fixed order, 8 interleaved runs per
-// column, then the runs.
-__global__ __launch_bounds__(NT) void norm_sums_kernel(const float* part, int64_t parts, int64_t D, float* out) {
-  __shared__ float lds[8][32];
-  const int lane = threadIdx.x % 32, run = threadIdx.x / 32;
-  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
-  float sum = 0.f;
-  if (c < D)
-    for (int64_t k = run; k < parts; k += 8) sum += part[k * D + c];
-  lds[run][lane] = sum;
-  __syncthreads();
-  if (run == 0 && c < D) {
-#pragma unroll
-    for (int k = 1; k < 8; ++k) sum += lds[k][lane];
-    out[c] = sum;
-  }
-}
-
 // A wave per row up to 4096 columns once the rows give every compute unit a
 // workgroup of four; a workgroup per row otherwise.
 bool wave_rows(int64_t rows, int64_t dim) { return dim <= 4096 && rows >= 1024; }
@@ -410,8 +393,7 @@ hipError_t launch_rms_norm(const NormParams& p, hipStream_t stream) {
 hipError_t launch_rms_norm_bwd(const NormBwdParams& p, hipStream_t stream) {
   const int64_t rows = p.batch * p.L;
   SSM_NORM_DISPATCH(launch_bwd, p)
-  hipLaunchKernelGGL(norm_sums_kernel, dim3((unsigned)((p.D + 31) / 32)), dim3(NT), 0, stream, p.part,
-                     (int64_t)p.parts, p.D, p.dweight);
+  launch_column_sums(p.part, p.parts, p.D, p.D, p.dweight, nullptr, nullptr, stream);
   return hipGetLastError();
 }
 

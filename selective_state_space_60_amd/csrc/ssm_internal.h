@@ -167,28 +167,28 @@ struct GatedParams {
   int64_t As_d, bas_d, bxs_d;
   int io_bf16;  // x, gate_a, gate_x, z are bf16 (1) or fp32 (0)
   int y_f32;    // y stored as fp32 (1) or in the io type (0)
-  // Sequence split: segment s covers [s*seg_len, min(L, (s+1)*seg_len)).
-  int n_seg;
-  int64_t seg_len;
-  float2* agg;  // (batch, n_seg-1, D): product of the decays of segment s, and its end state from zero
+  void* chain;  // words of the segments (gated_chain_bytes), 256-byte aligned; unused for one segment
+  int polls;    // bound of a workgroup's wait for its predecessor; 0: none waits
 };
 
-// Tiling (also used by the host planner): a workgroup owns 32 lanes x
-// (1 or 2) channels and walks the time in rounds of 16 chunks.
-constexpr int kGatedLanes = 32;
+// Tiling (also used by the host planner): a workgroup owns 32 lanes x (1 or 2)
+// channels over a segment of 16 chunks.
 constexpr int kGatedChunks = 16;
 constexpr int kGatedFwdSteps = 16;  // steps per chunk, forward
 constexpr int kGatedBwdSteps = 8;   // steps per chunk, backward
 constexpr int kGatedCkptSteps = 64;
-constexpr int kGatedRound = kGatedChunks * kGatedFwdSteps;
+constexpr int kGatedSpanSteps = 256;  // rows a kernel addresses from one base, at most
+constexpr int kGatedPolls = 1 << 16;  // tens of milliseconds; a wait is microseconds
 
-// Two channels per lane when every row starts on a whole pair.
-bool gated_pairs(const GatedParams& p);
+// Bytes of the words of nseg segments: a pair and a state per channel.
+inline int64_t gated_chain_bytes(int64_t batch, int64_t dim, int64_t nseg) {
+  return nseg > 1 ? (nseg * batch * dim * 12 + 255) / 256 * 256 : 0;
+}
 
 hipError_t launch_gated_scan(const GatedParams& p, hipStream_t stream);
 
 struct GatedBwdParams {
-  GatedParams f;       // the forward's inputs; f.ckpt: the checkpoints; f.n_seg, f.seg_len: the backward's split
+  GatedParams f;       // the forward's inputs; f.ckpt: the checkpoints
   const void* dy;
   const float* dh_last;  // (batch, D) or null
   void* dx;
@@ -201,8 +201,7 @@ struct GatedBwdParams {
   float* dh0;          // (batch, D) or null
   int64_t dys_b, dys_t, dxs_b, dxs_t, dgas_b, dgas_t, dgxs_b, dgxs_t, dzs_b, dzs_t;
   int g_f32;           // dy, dx, dgate_a, dgate_x, dz are fp32 (1) or in the io type (0)
-  float* part;         // (batch * n_seg, 3, D): sums of dA, dbias_a, dbias_x over one segment of one row
-  float2* agg;         // (batch, n_seg-1, D): decay product and carry out of segment s + 1 from a zero carry in
+  float* part;         // (segments * batch, 3, D): sums of dA, dbias_a, dbias_x over one segment of one row
 };
 
 hipError_t launch_gated_scan_bwd(const GatedBwdParams& p, hipStream_t stream);

@@ -11,14 +11,14 @@ a shape costs a lookup; pointers and values are never kept.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
 from . import (_GATED_BWD_T, _GATED_T, _GATED_UPD_T, _NORM_BWD_T, _NORM_T, _W4_T, SSM_HAS_BIAS, SSM_HAS_BIAS_A,
                SSM_HAS_BIAS_X, SSM_HAS_CKPT, SSM_HAS_DHLAST, SSM_HAS_H0, SSM_HAS_LENS, SSM_HAS_RESIDUAL,
-               SSM_HAS_STATE_OUT, SSM_HAS_Z, SSM_HAS_ZERO, SSM_WANT_CKPT, SSM_WANT_HLAST, GatedBwdDesc, GatedBwdPtrs,
-               GatedDesc, GatedPtrs, GatedUpdateDesc, GatedUpdatePtrs, NormBwdDesc, NormBwdPtrs, NormDesc, NormPtrs,
-               W4Desc, W4Ptrs, _check, lib, tensor_desc)
+               SSM_HAS_STATE_OUT, SSM_HAS_Z, SSM_HAS_ZERO, SSM_WANT_CKPT, SSM_WANT_HLAST, GatedBwdDesc, GatedDesc,
+               GatedUpdateDesc, NormBwdDesc, NormDesc, W4Desc, _check, lib, tensor_desc)
 
 GATED_CKPT_STEPS = 64  # SSM_GATED_CKPT_STEPS
 NORM_MAX_DIM = 16384   # SSM_NORM_MAX_DIM
@@ -27,60 +27,66 @@ W4_MAX_ROWS = 64       # SSM_W4_MAX_ROWS
 _MAX_PLANS = 1024
 _plans: dict = {}
 
+# The current stream's handle without building a Stream object (a microsecond of a decode step's call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _sig(tensors):
+    """What a descriptor depends on: type, shape, strides and device of each tensor."""
+    return tuple([None if t is None else (t.dtype, t.shape, t.stride(), t.get_device()) for t in tensors])
+
 
 class _Plan:
-    """One entry point's descriptor and workspace size."""
-    __slots__ = ("desc", "ref", "nbytes")
+    """An entry point with a descriptor of fixed shapes, and the workspace size it asks for."""
+    __slots__ = ("entry", "fn", "desc", "address", "pack", "index", "nbytes")
 
-    def __init__(self, desc, size_entry):
-        self.desc = desc
-        self.ref = ctypes.byref(desc)
-        self.nbytes = 0
-        if size_entry is not None:
-            n = ctypes.c_size_t()
-            _check(getattr(lib(), size_entry)(self.ref, ctypes.byref(n)), size_entry)
-            self.nbytes = n.value
-
-
-def _call(entry, Desc, Ptrs, names, sizes, flags, tensors, stream, size_entry=None, eps=None):
-    """Look up or build the descriptor of `tensors` (in the order of `names`,
-    None: left out) and launch on `stream` (default: the current stream of the
-    tensors' device)."""
-    key = (entry, sizes, flags, eps) + tuple([None if t is None else (t.dtype, t.shape, t.stride()) for t in tensors])
-    plan = _plans.get(key)
-    if plan is None:
+    def __init__(self, entry, Desc, names, sizes, flags, tensors, size_entry=None):
+        index = tensors[0].get_device()
+        if index < 0:
+            raise ValueError("%s: tensors must be on a GPU" % entry)
+        for t in tensors:
+            if t is not None and t.get_device() != index:
+                raise ValueError("%s: all tensors must be on one GPU" % entry)
         d = Desc()
         for name, v in sizes:
             setattr(d, name, v)
         d.flags = flags
-        if eps is not None:
-            d.eps = eps
         for name, t in zip(names, tensors):
             setattr(d, name, tensor_desc(t))
-        plan = _Plan(d, size_entry)
-        if len(_plans) >= _MAX_PLANS:
-            _plans.clear()
-        _plans[key] = plan
-    device = tensors[0].device
-    ptrs = Ptrs(*[None if t is None else t.data_ptr() for t in tensors])
-    index = device.index
-    if index != torch.cuda.current_device():
-        with torch.cuda.device(index):
-            return _launch(entry, plan, ptrs, stream, device)
-    return _launch(entry, plan, ptrs, stream, device)
+        self.entry, self.fn, self.index, self.desc = entry, getattr(lib(), entry), index, d
+        self.address = ctypes.addressof(d)
+        self.pack = struct.Struct("%dP" % len(names)).pack  # the pointer structs hold one pointer per name
+        self.nbytes = None
+        if size_entry is not None:
+            n = ctypes.c_size_t()
+            _check(getattr(lib(), size_entry)(self.address, ctypes.byref(n)), size_entry)
+            self.nbytes = n.value
 
 
-def _launch(entry, plan, ptrs, stream, device):
-    fn = getattr(lib(), entry)
-    if stream is None:
-        handle = torch.cuda.current_stream(device).cuda_stream
+def _keep(key, plan):
+    if len(_plans) >= _MAX_PLANS:
+        _plans.clear()
+    _plans[key] = plan
+    return plan
+
+
+def _launch(plan, tensors, stream):
+    """Run the plan on these tensors, on `stream` (default: the current stream of their device)."""
+    if plan.index != torch.cuda.current_device():
+        with torch.cuda.device(plan.index):
+            return _launch(plan, tensors, stream)
+    handle = _raw_stream(plan.index) if stream is None else stream.cuda_stream
+    ptrs = plan.pack(*[0 if t is None else t.data_ptr() for t in tensors])
+    if plan.nbytes is None:
+        status = plan.fn(plan.address, ptrs, handle)
+    elif plan.nbytes == 0:
+        status = plan.fn(plan.address, ptrs, None, 0, handle)
     else:
-        handle = stream.cuda_stream
-    if plan.nbytes == 0 and len(fn.argtypes) == 3:
-        _check(fn(plan.ref, ctypes.byref(ptrs), handle), entry)
-        return
-    ws = _empty(stream, (plan.nbytes,), torch.uint8, device) if plan.nbytes else None
-    _check(fn(plan.ref, ctypes.byref(ptrs), None if ws is None else ws.data_ptr(), plan.nbytes, handle), entry)
+        ws = _empty(stream, (plan.nbytes,), torch.uint8, tensors[0].device)
+        status = plan.fn(plan.address, ptrs, ws.data_ptr(), plan.nbytes, handle)
+    if status:
+        _check(status, plan.entry)
 
 
 def _empty(stream, shape, dtype, device):
@@ -92,14 +98,11 @@ def _empty(stream, shape, dtype, device):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _one_gpu(where, *tensors):
-    device = tensors[0].device
-    if device.type != "cuda":
-        raise ValueError("%s: tensors must be on a GPU" % where)
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError("%s: all tensors must be on %s" % (where, device))
-    return device
+def _like(stream, t, dtype=None):
+    """Contiguous memory of t's shape."""
+    if stream is None:
+        return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
+    return _empty(stream, t.shape, dtype or t.dtype, t.device)
 
 
 # -------------------------------------------------- gated linear recurrence
@@ -126,17 +129,23 @@ def gated_scan_fwd(x, gate_a, gate_x, A, bias_a=None, bias_x=None, z=None, h0=No
     (batch,) int32 on the GPU, the steps of each row that count (later y are
     zeros, h_last is the state after the last that counts).  ckpt: optional
     gated_scan_ckpt(...) buffer, filled for gated_scan_bwd(ckpt=...)."""
-    dev = _one_gpu("gated_scan_fwd", x, gate_a, gate_x, A, bias_a, bias_x, z, h0, lens, y, ckpt)
-    batch, L, dim = x.shape
+    key = ("gated_scan_fwd", want_hlast, y_dtype, _sig((x, gate_a, gate_x, A, bias_a, bias_x, z, h0, lens, y, ckpt)))
+    plan = _plans.get(key)
     if y is None:
-        y = _empty(stream, x.shape, y_dtype or x.dtype, dev)
-    h_last = _empty(stream, (batch, dim), torch.float32, dev) if want_hlast else None
-    flags = (_gated_flags(bias_a, bias_x, z) | (SSM_HAS_H0 if h0 is not None else 0) |
-             (SSM_WANT_HLAST if want_hlast else 0) | (SSM_HAS_LENS if lens is not None else 0) |
-             (SSM_WANT_CKPT if ckpt is not None else 0))
-    _call("ssm_gated_scan_fwd", GatedDesc, GatedPtrs, _GATED_T, (("batch", batch), ("seqlen", L), ("dim", dim)),
-          flags, (x, gate_a, gate_x, A, bias_a, bias_x, z, y, h0, h_last, lens, ckpt), stream,
-          size_entry="ssm_gated_scan_workspace_size")
+        y = _like(stream, x, y_dtype)
+    h_last = None
+    if want_hlast:
+        h_last = _empty(stream, (x.shape[0], x.shape[2]), torch.float32, x.device)
+    tensors = (x, gate_a, gate_x, A, bias_a, bias_x, z, y, h0, h_last, lens, ckpt)
+    if plan is None:
+        batch, L, dim = x.shape
+        flags = (_gated_flags(bias_a, bias_x, z) | (SSM_HAS_H0 if h0 is not None else 0) |
+                 (SSM_WANT_HLAST if want_hlast else 0) | (SSM_HAS_LENS if lens is not None else 0) |
+                 (SSM_WANT_CKPT if ckpt is not None else 0))
+        plan = _keep(key, _Plan("ssm_gated_scan_fwd", GatedDesc, _GATED_T,
+                                (("batch", batch), ("seqlen", L), ("dim", dim)), flags, tensors,
+                                "ssm_gated_scan_workspace_size"))
+    _launch(plan, tensors, stream)
     return y, h_last
 
 
@@ -149,22 +158,24 @@ def gated_scan_bwd(dy, x, gate_a, gate_x, A, bias_a=None, bias_x=None, z=None, h
 
     Returns a dict: dx, dgate_a, dgate_x, dz (if z), all of dy's dtype (x's or
     fp32), and fp32 dA, dbias_a, dbias_x (dim,; if given) and dh0 (if h0)."""
-    dev = _one_gpu("gated_scan_bwd", x, dy, gate_a, gate_x, A, bias_a, bias_x, z, h0, lens, dh_last, ckpt)
-    batch, L, dim = x.shape
-    # one buffer each: the gradients of the streams and of the channels
-    n = 3 if z is None else 4
-    g = _empty(stream, (n,) + tuple(x.shape), dy.dtype, dev)
-    s = _empty(stream, (3, dim), torch.float32, dev)
-    out = {"dx": g[0], "dgate_a": g[1], "dgate_x": g[2], "dz": g[3] if z is not None else None, "dA": s[0],
-           "dbias_a": s[1] if bias_a is not None else None, "dbias_x": s[2] if bias_x is not None else None,
-           "dh0": _empty(stream, (batch, dim), torch.float32, dev) if h0 is not None else None}
-    flags = (_gated_flags(bias_a, bias_x, z) | (SSM_HAS_H0 if h0 is not None else 0) |
-             (SSM_HAS_LENS if lens is not None else 0) | (SSM_HAS_CKPT if ckpt is not None else 0) |
-             (SSM_HAS_DHLAST if dh_last is not None else 0))
-    _call("ssm_gated_scan_bwd", GatedBwdDesc, GatedBwdPtrs, _GATED_BWD_T,
-          (("batch", batch), ("seqlen", L), ("dim", dim)), flags,
-          (x, gate_a, gate_x, A, bias_a, bias_x, z, h0, lens, ckpt, dy, dh_last) + tuple(out.values()), stream,
-          size_entry="ssm_gated_scan_bwd_workspace_size")
+    ins = (x, gate_a, gate_x, A, bias_a, bias_x, z, h0, lens, ckpt, dy, dh_last)
+    key = ("gated_scan_bwd", _sig(ins))
+    plan = _plans.get(key)
+    out = {"dx": _like(stream, dy), "dgate_a": _like(stream, dy), "dgate_x": _like(stream, dy),
+           "dz": None if z is None else _like(stream, dy), "dA": _like(stream, A),
+           "dbias_a": None if bias_a is None else _like(stream, bias_a),
+           "dbias_x": None if bias_x is None else _like(stream, bias_x),
+           "dh0": None if h0 is None else _like(stream, h0)}
+    tensors = ins + tuple(out.values())
+    if plan is None:
+        batch, L, dim = x.shape
+        flags = (_gated_flags(bias_a, bias_x, z) | (SSM_HAS_H0 if h0 is not None else 0) |
+                 (SSM_HAS_LENS if lens is not None else 0) | (SSM_HAS_CKPT if ckpt is not None else 0) |
+                 (SSM_HAS_DHLAST if dh_last is not None else 0))
+        plan = _keep(key, _Plan("ssm_gated_scan_bwd", GatedBwdDesc, _GATED_BWD_T,
+                                (("batch", batch), ("seqlen", L), ("dim", dim)), flags, tensors,
+                                "ssm_gated_scan_bwd_workspace_size"))
+    _launch(plan, tensors, stream)
     return {k: v for k, v in out.items() if v is not None}
 
 
@@ -173,20 +184,25 @@ def gated_state_update(state, x, gate_a, gate_x, A, bias_a=None, bias_x=None, z=
     """One decode step of the gated recurrence (see include/ssm.h): advances
     ``state`` (batch, dim) fp32 in place, or into ``state_out`` if given, and
     returns y (batch, dim).  x, gate_a, gate_x, z: (batch, dim)."""
-    dev = _one_gpu("gated_state_update", x, state, gate_a, gate_x, A, bias_a, bias_x, z, state_out, y)
+    ins = (x, gate_a, gate_x, A, bias_a, bias_x, z)
+    key = ("gated_state_update", y_dtype, _sig(ins + (y, state, state_out)))
+    plan = _plans.get(key)
     if y is None:
-        y = _empty(stream, x.shape, y_dtype or x.dtype, dev)
-    batch, dim = x.shape
-    flags = _gated_flags(bias_a, bias_x, z) | (SSM_HAS_STATE_OUT if state_out is not None else 0)
-    _call("ssm_gated_state_update", GatedUpdateDesc, GatedUpdatePtrs, _GATED_UPD_T, (("batch", batch), ("dim", dim)),
-          flags, (x, gate_a, gate_x, A, bias_a, bias_x, z, y, state, state_out), stream)
+        y = _like(stream, x, y_dtype)
+    tensors = ins + (y, state, state_out)
+    if plan is None:
+        batch, dim = x.shape
+        flags = _gated_flags(bias_a, bias_x, z) | (SSM_HAS_STATE_OUT if state_out is not None else 0)
+        plan = _keep(key, _Plan("ssm_gated_state_update", GatedUpdateDesc, _GATED_UPD_T,
+                                (("batch", batch), ("dim", dim)), flags, tensors))
+    _launch(plan, tensors, stream)
     return y
 
 
 # ---------------------------------------------------------------------- norm
 
 def _rows(t):
-    """(batch, L, dim) view of a (..., dim) tensor of two or three dimensions."""
+    """(batch, L, dim) view of a tensor of two or three dimensions."""
     return t if t is None or t.dim() == 3 else t.unsqueeze(0)
 
 
@@ -201,25 +217,30 @@ def rms_norm(x, weight, eps=1e-5, residual=None, residual_dtype=None, residual_o
     torch.float32, or torch.float8_e4m3fn, which comes with fp32 scales, one
     for each `group` columns (32, 64 or 128; 0: one a row): scale has x's
     leading shape and ceil(dim / group) columns."""
-    dev = _one_gpu("rms_norm", x, weight, residual, residual_out, y)
-    if x.dim() not in (2, 3) or (residual is not None and residual.shape != x.shape):
-        raise ValueError("rms_norm: x and residual are (rows, dim) or (batch, L, dim), of one shape")
-    if residual is None and residual_out is not None:
-        raise ValueError("rms_norm: residual_out without residual")
+    key = ("rms_norm", eps, residual_dtype, y_dtype, group, _sig((x, weight, residual, residual_out, y)))
+    plan = _plans.get(key)
+    if plan is None:
+        if x.dim() not in (2, 3) or (residual is not None and residual.shape != x.shape):
+            raise ValueError("rms_norm: x and residual are (rows, dim) or (batch, L, dim), of one shape")
+        if residual is None and residual_out is not None:
+            raise ValueError("rms_norm: residual_out without residual")
     if y is None:
-        y = _empty(stream, x.shape, y_dtype or x.dtype, dev)
+        y = _like(stream, x, y_dtype)
     if residual is not None and residual_out is None:
-        residual_out = _empty(stream, x.shape, residual_dtype or residual.dtype, dev)
-    dim = x.shape[-1]
+        residual_out = _like(stream, x, residual_dtype or residual.dtype)
     scale = None
     if y.dtype == torch.float8_e4m3fn:
-        scale = _empty(stream, tuple(x.shape[:-1]) + ((dim + group - 1) // group if group > 0 else 1,),
-                       torch.float32, dev)
-    x3 = _rows(x)
-    _call("ssm_rms_norm_fwd", NormDesc, NormPtrs, _NORM_T,
-          (("batch", x3.shape[0]), ("seqlen", x3.shape[1]), ("dim", dim), ("group", group)),
-          SSM_HAS_RESIDUAL if residual is not None else 0,
-          (x3, _rows(residual), weight, _rows(y), _rows(residual_out), _rows(scale)), stream, eps=float(eps))
+        scale = _empty(stream, x.shape[:-1] + ((x.shape[-1] + group - 1) // group if group > 0 else 1,),
+                       torch.float32, x.device)
+    tensors = (x, residual, weight, y, residual_out, scale)
+    if plan is None:
+        x3 = _rows(x)
+        plan = _keep(key, _Plan("ssm_rms_norm_fwd", NormDesc, _NORM_T,
+                                (("batch", x3.shape[0]), ("seqlen", x3.shape[1]), ("dim", x3.shape[2]),
+                                 ("group", group), ("eps", float(eps))),
+                                SSM_HAS_RESIDUAL if residual is not None else 0,
+                                (x3, _rows(residual), weight, _rows(y), _rows(residual_out), _rows(scale))))
+    _launch(plan, tensors, stream)
     return y, residual_out, scale
 
 
@@ -231,16 +252,22 @@ def rms_norm_bwd(dy, row, weight, eps=1e-5, dres=None, grad_dtype=None, stream=N
 
     Returns {"dx": grad_dtype, default dy's -- the gradient of x and of
     residual alike, "dweight": (dim,) fp32}."""
-    dev = _one_gpu("rms_norm_bwd", dy, row, weight, dres)
-    if row.dim() not in (2, 3) or dy.shape != row.shape or (dres is not None and dres.shape != row.shape):
+    key = ("rms_norm_bwd", eps, grad_dtype, _sig((dy, row, weight, dres)))
+    plan = _plans.get(key)
+    if plan is None and (row.dim() not in (2, 3) or dy.shape != row.shape or
+                         (dres is not None and dres.shape != row.shape)):
         raise ValueError("rms_norm_bwd: dy, row and dres are (rows, dim) or (batch, L, dim), of one shape")
-    dx = _empty(stream, row.shape, grad_dtype or dy.dtype, dev)
-    dweight = _empty(stream, (row.shape[-1],), torch.float32, dev)
-    r3 = _rows(row)
-    _call("ssm_rms_norm_bwd", NormBwdDesc, NormBwdPtrs, _NORM_BWD_T,
-          (("batch", r3.shape[0]), ("seqlen", r3.shape[1]), ("dim", r3.shape[2])),
-          SSM_HAS_RESIDUAL if dres is not None else 0, (_rows(dy), r3, weight, _rows(dres), _rows(dx), dweight),
-          stream, size_entry="ssm_rms_norm_bwd_workspace_size", eps=float(eps))
+    dx = _like(stream, dy, grad_dtype)
+    dweight = _like(stream, weight)
+    tensors = (dy, row, weight, dres, dx, dweight)
+    if plan is None:
+        r3 = _rows(row)
+        plan = _keep(key, _Plan("ssm_rms_norm_bwd", NormBwdDesc, _NORM_BWD_T,
+                                (("batch", r3.shape[0]), ("seqlen", r3.shape[1]), ("dim", r3.shape[2]),
+                                 ("eps", float(eps))), SSM_HAS_RESIDUAL if dres is not None else 0,
+                                (_rows(dy), r3, weight, _rows(dres), _rows(dx), dweight),
+                                "ssm_rms_norm_bwd_workspace_size"))
+    _launch(plan, tensors, stream)
     return {"dx": dx, "dweight": dweight}
 
 
@@ -269,15 +296,19 @@ def w4_matvec(x, weight, scale, zero=None, bias=None, y_dtype=None, y=None, stre
     scale: (outs, ins / group) bf16 or fp32, group 32, 64 or 128; zero: (outs,
     ins / group) uint8 (default 8); bias: (outs,) fp32.  Returns y (rows,
     outs), bf16 by default."""
-    dev = _one_gpu("w4_matvec", x, weight, scale, zero, bias, y)
-    rows, ins = x.shape
-    outs = weight.shape[0]
-    if scale.dim() != 2 or scale.shape[1] == 0 or ins % scale.shape[1]:
-        raise ValueError("w4_matvec: scale is (outs, ins / group)")
+    key = ("w4_matvec", y_dtype, _sig((x, weight, scale, zero, bias, y)))
+    plan = _plans.get(key)
     if y is None:
-        y = _empty(stream, (rows, outs), y_dtype or x.dtype, dev)
-    _call("ssm_w4_matvec", W4Desc, W4Ptrs, _W4_T,
-          (("rows", rows), ("ins", ins), ("outs", outs), ("group", ins // scale.shape[1])),
-          (SSM_HAS_ZERO if zero is not None else 0) | (SSM_HAS_BIAS if bias is not None else 0),
-          (x, weight, scale, zero, bias, y), stream)
+        y = _empty(stream, (x.shape[0], weight.shape[0]), y_dtype or x.dtype, x.device)
+    tensors = (x, weight, scale, zero, bias, y)
+    if plan is None:
+        rows, ins = x.shape
+        if scale.dim() != 2 or scale.shape[1] == 0 or ins % scale.shape[1]:
+            raise ValueError("w4_matvec: scale is (outs, ins / group)")
+        plan = _keep(key, _Plan("ssm_w4_matvec", W4Desc, _W4_T,
+                                (("rows", rows), ("ins", ins), ("outs", weight.shape[0]),
+                                 ("group", ins // scale.shape[1])),
+                                (SSM_HAS_ZERO if zero is not None else 0) |
+                                (SSM_HAS_BIAS if bias is not None else 0), tensors))
+    _launch(plan, tensors, stream)
     return y

@@ -106,19 +106,75 @@ def test_forward_backward(size, io):
     check_all(t, c, y, h, backward(c), "recomputed")
 
 
-def test_sequence_split():
-    """Few channels and many steps: the sequence is cut into segments, forward
-    and backward, with a ragged end and a length inside an early segment."""
+def test_many_segments():
+    """Few channels and many steps: many segments in flight pass the state on,
+    forward and backward, with a ragged end and a length inside an early one."""
     b, L, D = 2, 5000, 40
     t = make(b, L, D, "f32", lens=[5000, 1300], seed=3)
     c = up(t)
-    d = ssm.GatedDesc()
-    for k, v in zip(("batch", "seqlen", "dim"), (b, L, D)):
-        setattr(d, k, v)
     ckpt = ssm.gated_scan_ckpt(b, L, D)
     y, h = forward(c, want_hlast=True, ckpt=ckpt)
     check_all(t, c, y, h, backward(c, ckpt=ckpt), "split")
     check_all(t, c, y, h, backward(c), "split, recomputed")
+
+
+def by_abi(entry, Desc, Ptrs, flags, sizes, tensors):
+    """A call through the C ABI with a workspace of exactly the size asked for."""
+    import ctypes
+    d, p = Desc(), Ptrs()
+    for k, v in sizes.items():
+        setattr(d, k, v)
+    d.flags = flags
+    for k, v in tensors.items():
+        setattr(d, k, ssm.tensor_desc(v))
+        setattr(p, k, None if v is None else v.data_ptr())
+    n = ctypes.c_size_t()
+    size = entry.replace("_fwd", "") + "_workspace_size"
+    assert getattr(ssm.lib(), size)(ctypes.byref(d), ctypes.byref(n)) == ssm.SSM_OK
+    ws = torch.randint(0, 256, (max(n.value, 1),), dtype=torch.uint8, device="cuda")
+    status = getattr(ssm.lib(), entry)(ctypes.byref(d), ctypes.byref(p), ws.data_ptr(), n.value,
+                                       torch.cuda.current_stream().cuda_stream)
+    assert status == ssm.SSM_OK
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("io,size", [("f32", (2, 1100, 40)), ("bf16", (1, 2000, 66)), ("f32", (1, 700, 33))])
+def test_no_wait_gives_the_same_bits(io, size):
+    """With SSM_NO_WAIT every workgroup computes the state that enters its
+    segment itself: what a wait that runs out comes to.  Same operations, same
+    bits; the workspace's contents before the call do not matter."""
+    banner("gated no wait %s %s" % (size, io))
+    t = make(*size, io, lens=[size[1], 333][:size[0]], seed=31)
+    c = up(t)
+    ckpt = ssm.gated_scan_ckpt(*size)
+    y, h = forward(c, want_hlast=True, ckpt=ckpt)
+    grads = backward(c, ckpt=ckpt)
+    sizes = dict(zip(("batch", "seqlen", "dim"), size))
+    ins = {"x": c["x"], "gate_a": c["ga"], "gate_x": c["gx"], "A": c["A"], "bias_a": c["ba"], "bias_x": c["bx"],
+           "z": c["z"], "h0": c["h0"], "lens": c["lens"]}
+    common = (ssm.SSM_HAS_Z | ssm.SSM_HAS_H0 | ssm.SSM_HAS_BIAS_A | ssm.SSM_HAS_BIAS_X | ssm.SSM_HAS_LENS)
+    for extra in (0, ssm.SSM_NO_WAIT):
+        y2, h2, ck2 = torch.full_like(y, 3.0), torch.full_like(h, 3.0), torch.full_like(ckpt, 3.0)
+        by_abi("ssm_gated_scan_fwd", ssm.GatedDesc, ssm.GatedPtrs,
+               common | ssm.SSM_WANT_HLAST | ssm.SSM_WANT_CKPT | extra, sizes,
+               dict(ins, y=y2, h_last=h2, ckpt=ck2))
+        assert torch.equal(y2, y) and torch.equal(h2, h) and torch.equal(ck2, ckpt)
+        out = {k: torch.full_like(v, 3.0) for k, v in grads.items()}
+        by_abi("ssm_gated_scan_bwd", ssm.GatedBwdDesc, ssm.GatedBwdPtrs, common | ssm.SSM_HAS_DHLAST | extra, sizes,
+               dict(ins, dy=c["dy"], dh_last=c["dh_last"], **out))
+        for k, v in grads.items():
+            assert torch.equal(out[k], v), k
+
+
+def test_repeated_calls_give_the_same_bits():
+    """The chain of segments does not make the result depend on timing."""
+    c = up(make(1, 20000, 64, "f32", seed=33))
+    y, h = forward(c, want_hlast=True)
+    g = backward(c)
+    for _ in range(5):
+        y2, h2 = forward(c, want_hlast=True)
+        g2 = backward(c)
+        assert torch.equal(y, y2) and torch.equal(h, h2) and all(torch.equal(g[k], g2[k]) for k in g)
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
