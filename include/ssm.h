@@ -441,7 +441,7 @@ typedef struct {
  * the state that enters its segment from the start of the sequence, by the
  * same operations.  SSM_NO_WAIT makes every workgroup do so: the same bits,
  * at a cost that grows with the square of the length.
- * Limit: 256 rows of any (batch, seqlen, dim) tensor must span less than
+ * Limit: 128 rows of any (batch, seqlen, dim) tensor must span less than
  * 1 GiB (SSM_ERR_UNSUPPORTED otherwise). */
 #define SSM_GATED_CKPT_STEPS 64
 

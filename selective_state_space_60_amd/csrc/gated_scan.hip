@@ -7,10 +7,10 @@
 // and VALU issue are close: every stream is read once and written once, and
 // nothing is computed twice.
 //
-// A workgroup owns 64 channels (32 lanes of two) over one segment of 16
+// A workgroup owns 64 channels (32 lanes of two) over one segment of 8
 // chunks.  Each half-wave holds one chunk of T consecutive steps in registers
 // and scans it from zero to the pair (P, H) = (product of decays, end state).
-// The first wave, a channel a lane, folds the 16 pairs through LDS
+// The first wave, a channel a lane, folds the 8 pairs through LDS
 //   h <- P h + H
 // to the segment's own pair, finds the state that enters the segment, and
 // hands every chunk the state that enters it; the chunks are then walked again
@@ -20,7 +20,7 @@
 // pair as soon as it has it and its end state once it knows the state that
 // enters it, each in a word that says by itself whether it has been written.
 // To find the entering state a workgroup goes back over its predecessors,
-// eight at a time, to the nearest published end state and folds the pairs
+// four at a time, to the nearest published end state and folds the pairs
 // since then forward from it: the same operations in the same order whichever
 // state it finds, so the result does not depend on timing.  Workgroups are
 // dispatched in order (a layer of all tiles after another, a tile always on
@@ -49,12 +49,14 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int LC = 32;  // lanes per chunk
-constexpr int NCH = kGatedChunks;
-constexpr int NT = LC * NCH;
 constexpr int kFwdT = kGatedFwdSteps;
 constexpr int kBwdT = kGatedBwdSteps;
-constexpr int kFwdSeg = NCH * kFwdT;
-constexpr int kBwdSeg = NCH * kBwdT;
+constexpr int kFwdNT = LC * kGatedFwdChunks, kFwdSeg = kGatedFwdChunks * kFwdT;
+constexpr int kBwdNT = LC * kGatedBwdChunks, kBwdSeg = kGatedBwdChunks * kBwdT;
+// Waves per SIMD that the registers are cut to: 128 and 168 hold a chunk of
+// two channels without a spill (4 x 4096 x 5120 forward at 3 waves: 247 us
+// against 197).
+constexpr int kFwdWaves = 4, kBwdWaves = 3;
 static_assert(kGatedCkptSteps % kFwdT == 0 && kFwdSeg % kGatedCkptSteps == 0, "checkpoints fall on chunks");
 static_assert(kBwdSeg % kGatedCkptSteps == 0, "every backward segment starts at a checkpoint");
 static_assert(kFwdSeg <= kGatedSpanSteps && kBwdSeg <= kGatedSpanSteps, "a segment's rows fit the offsets");
@@ -175,7 +177,7 @@ __device__ __forceinline__ int64_t row_len(const GatedParams& p, int64_t b) {
 // row of its chunk and the row stride, in bytes.
 struct Stream {
   __amdgpu_buffer_rsrc_t r;
-  uint32_t off, row;
+  uint32_t off, row, at;
 
   // T: steps per chunk, e: bytes per element; `ok` is false for the lanes
   // behind the last channel
@@ -183,23 +185,38 @@ struct Stream {
                                       int64_t L, int64_t D, int e, int T, int chunk, int lane_elem, bool ok) {
     r = rows_from(p, sb, st, b, t0, c0, L, D, e);
     row = (uint32_t)(st * e);
-    // keep j * row inside the round: hoisted, the offsets of five streams spill the scalar registers
-    asm volatile("" : "+s"(row));
     off = ok ? (uint32_t)(chunk * T) * row + (uint32_t)(lane_elem * e) : kFar;
+    at = 0;
+  }
+  // The rows are walked one after another: `at` is the current one's offset.
+  // Opaque to the compiler, which would otherwise compute the offsets of all
+  // rows of all streams at once and spill the scalar registers.
+  __device__ __forceinline__ void next() {
+    at += row;
+    asm volatile("" : "+s"(at));
+  }
+  __device__ __forceinline__ void last(int T) {
+    at = (uint32_t)(T - 1) * row;
+    asm volatile("" : "+s"(at));
+  }
+  __device__ __forceinline__ void prev() {
+    at -= row;
+    asm volatile("" : "+s"(at));
   }
 };
 
-// Row j of the chunk; with MASK rows from `n` on are sent out of range.
+// The current row, number j of the chunk, and on to the next; with MASK rows
+// from `n` on are sent out of range.
 template <bool MASK, bool BF16, int V>
-__device__ __forceinline__ Raw<BF16, V> load_row(const Stream& s, int j, int n) {
-  if constexpr (MASK) return load<BF16, V>(s.r, j < n ? s.off + (uint32_t)j * s.row : kFar, 0);
-  else return load<BF16, V>(s.r, s.off, (uint32_t)j * s.row);
+__device__ __forceinline__ Raw<BF16, V> load_row(Stream& s, int j, int n) {
+  const Raw<BF16, V> o = load<BF16, V>(s.r, !MASK || j < n ? s.off : kFar, s.at);
+  s.next();
+  return o;
 }
 
 template <bool MASK, bool F32, int V>
 __device__ __forceinline__ void store_row(const Stream& s, int j, int n, const float (&o)[V]) {
-  if constexpr (MASK) store<F32, V>(s.r, j < n && s.off != kFar ? s.off + (uint32_t)j * s.row : kFar, 0, o);
-  else store<F32, V>(s.r, s.off, (uint32_t)j * s.row, o);
+  store<F32, V>(s.r, !MASK || j < n ? s.off : kFar, s.at, o);
 }
 
 // ------------------------------------------------------------------ segments
@@ -213,7 +230,7 @@ struct Chain {
   int polls;     // bound of the wait
 };
 
-constexpr int kBack = 8;    // predecessors read at once
+constexpr int kBack = 4;    // predecessors read at once
 constexpr int kStack = 32;  // pairs kept while going back; a multiple of kBack
 
 __device__ __forceinline__ uint32_t bits_of(float v) { return v != v ? 0x7FC00000u : __float_as_uint(v); }
@@ -322,7 +339,7 @@ struct Fwd : Place<V> {
   using Place<V>::ok;
   static constexpr int E = BF16 ? 2 : 4;
   static constexpr int YE = (YF32 || !BF16) ? 4 : 2;
-  static constexpr int T = kFwdT;
+  static constexpr int T = kFwdT, NCH = kGatedFwdChunks;
   static constexpr bool kZ = Z && Y;
   struct Shared {
     float2 pair[NCH][CW];
@@ -387,7 +404,7 @@ struct Fwd : Place<V> {
   // The segment's pair, by the first wave.
   __device__ __forceinline__ float2 fold(const Shared& sh, int ch_lane) const {
     float2 f = make_float2(1.f, 0.f);
-#pragma unroll
+#pragma unroll 4
     for (int q = 0; q < NCH; ++q) {
       const float2 w = sh.pair[q][ch_lane];
       f.x *= w.x;
@@ -420,8 +437,10 @@ struct Fwd : Place<V> {
           if (more) publish_state(q, at, end);
           else if (Y && p.h_last) p.h_last[b * p.D + c0 + l] = end;
         }
+        // read the pairs again rather than hold them over the wait
+        asm volatile("" ::: "memory");
         if (l < CW)
-#pragma unroll
+#pragma unroll 4
           for (int i = 0; i < NCH; ++i) {
             sh.in[i][l] = h;
             h = __builtin_fmaf(sh.pair[i][l].x, h, sh.pair[i][l].y);
@@ -456,6 +475,7 @@ struct Fwd : Place<V> {
           if (MASK && j >= live) o[v] = 0.f;
         }
         store_row<MASK, YF32 || !BF16, V>(sy, j, rows, o);
+        sy.next();
       }
     }
     return true;
@@ -463,7 +483,7 @@ struct Fwd : Place<V> {
 };
 
 template <bool BF16, bool YF32, bool Z, int V, bool Y>
-__global__ __launch_bounds__(NT) void gated_fwd_kernel(GatedParams p, Chain q, unsigned tiles, int64_t nseg) {
+__global__ __launch_bounds__(kFwdNT, kFwdWaves) void gated_fwd_kernel(GatedParams p, Chain q, unsigned tiles, int64_t nseg) {
   typedef Fwd<BF16, YF32, Z, V, Y> F;
   __shared__ typename F::Shared sh;
   F f(p);
@@ -506,7 +526,7 @@ struct Bwd : Place<V> {
   static constexpr int E = BF16 ? 2 : 4;
   static constexpr bool G32 = GF32 || !BF16;
   static constexpr int GE = G32 ? 4 : 2;
-  static constexpr int T = kBwdT;
+  static constexpr int T = kBwdT, NCH = kGatedBwdChunks;
   struct Shared {
     float P[NCH][CW], H[NCH][CW], O[NCH][CW];  // decay product, end state from zero, carry out from a zero carry
     float2 stack[kStack][CW];
@@ -517,11 +537,14 @@ struct Bwd : Place<V> {
   const GatedBwdParams& q;
   const GatedParams& p;
   Chan<V> ch;
-  // a, the input s i x (later the state before the step), g, r, i, 1 / s, 1 - a^2 and x of every step
-  float a[T][V], u[T][V], g[T][V], r[T][V], i[T][V], is[T][V], om[T][V], zf[Z ? T : 1][V];
+  // a, g, r, i, s, x of every step; zf = dy silu'(z), later the state before the step less i x a / s
+  float a[T][V], g[T][V], r[T][V], i[T][V], s[T][V], zf[T][V];
   Raw<BF16, V> xr[T];
 
   __device__ __forceinline__ Bwd(const GatedBwdParams& w) : q(w), p(w.f) {}
+
+  // What step j adds to the state.
+  __device__ __forceinline__ float input(int j, int v) const { return s[j][v] * (i[j][v] * elem(xr[j], v)); }
 
   // GRADS: everything of the chunk of the segment at t0; else only what the carry needs (a, g).
   template <bool MASK, bool GRADS>
@@ -564,23 +587,23 @@ struct Bwd : Place<V> {
         const float dy = elem(dr[j], v);
         g[j][v] = dy;
         if constexpr (Z) {
-          const float z = elem(zr[j], v), s = gate(z, 0.f);
-          g[j][v] = dy * (z * s);
-          if constexpr (GRADS) zf[j][v] = dy * (s * __builtin_fmaf(z, 1.f - s, 1.f));
+          const float z = elem(zr[j], v), sz = gate(z, 0.f);
+          g[j][v] = dy * (z * sz);
+          if constexpr (GRADS) zf[j][v] = dy * (sz * __builtin_fmaf(z, 1.f - sz, 1.f));
         }
         if constexpr (GRADS) {
           i[j][v] = gate(elem(gr[j], v), ch.nbx[v]);
-          om[j][v] = one_minus_sq(e, a[j][v]);
-          is[j][v] = om[j][v] > 0.f ? __builtin_amdgcn_rsqf(om[j][v]) : 0.f;
-          u[j][v] = om[j][v] * is[j][v] * (i[j][v] * elem(xr[j], v));
+          s[j][v] = __builtin_amdgcn_sqrtf(one_minus_sq(e, a[j][v]));
         }
         if (MASK && j >= live) {
           a[j][v] = 1.f;
           g[j][v] = 0.f;
-          if constexpr (GRADS) u[j][v] = 0.f;
         }
         cp[v] *= a[j][v];
-        if constexpr (GRADS) cH[v] = __builtin_fmaf(a[j][v], cH[v], u[j][v]);
+        if constexpr (GRADS) cH[v] = __builtin_fmaf(a[j][v], cH[v], MASK && j >= live ? 0.f : input(j, v));
+        // finished here: left for after the barriers, its factors would be held instead
+        if constexpr (GRADS && Z) asm volatile("" : "+v"(zf[j][v]));
+        if constexpr (GRADS) asm volatile("" : "+v"(g[j][v]));
       }
 #pragma unroll
     for (int j = T - 1; j >= 0; --j)
@@ -597,7 +620,7 @@ struct Bwd : Place<V> {
   // The segment's pair for the carry, by the first wave.
   __device__ __forceinline__ float2 fold(const Shared& sh, int l) const {
     float2 f = make_float2(1.f, 0.f);
-#pragma unroll
+#pragma unroll 4
     for (int w = NCH - 1; w >= 0; --w) {
       f.x *= sh.P[w][l];
       f.y = __builtin_fmaf(sh.P[w][l], f.y, sh.O[w][l]);
@@ -629,13 +652,15 @@ struct Bwd : Place<V> {
           if (seg > 0) publish_state(cn, at, end);
           else if (q.dh0) q.dh0[b * p.D + c0 + l] = end;
         }
+        // read the pairs again rather than hold them over the wait
+        asm volatile("" ::: "memory");
         if (l < CW) {
-#pragma unroll
+#pragma unroll 4
           for (int w = 0; w < NCH; ++w) {
             sh.h[w][l] = h;
             h = __builtin_fmaf(sh.P[w][l], h, sh.H[w][l]);
           }
-#pragma unroll
+#pragma unroll 4
           for (int w = NCH - 1; w >= 0; --w) {
             sh.m[w][l] = m;
             m = __builtin_fmaf(sh.P[w][l], m, sh.O[w][l]);
@@ -646,6 +671,15 @@ struct Bwd : Place<V> {
     }
     __syncthreads();
     if (!sh.found) return false;
+    // Products of these made before the barriers are made again: held over
+    // them they cost twice the registers that the factors do.
+#pragma unroll
+    for (int j = 0; j < T; ++j) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) asm volatile("" : "+v"(r[j][v]), "+v"(i[j][v]), "+v"(s[j][v]));
+#pragma unroll
+      for (uint32_t& x : xr[j].w) asm volatile("" : "+v"(x));
+    }
     float h[V], mi[V], A[V], sA[V], sba[V], sbx[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -661,16 +695,23 @@ struct Bwd : Place<V> {
       float o[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float hn = __builtin_fmaf(a[j][v], h[v], u[j][v]);
-        u[j][v] = h[v];
-        h[v] = hn;
+        const float hn = __builtin_fmaf(a[j][v], h[v], MASK && j >= live ? 0.f : input(j, v));
         if constexpr (Z) o[v] = MASK && j >= live ? 0.f : hn * zf[j][v];
+        const float is = s[j][v] > 0.f ? __builtin_amdgcn_rcpf(s[j][v]) : 0.f;
+        zf[j][v] = __builtin_fmaf(-(i[j][v] * elem(xr[j], v)) * a[j][v], is, h[v]);
+        h[v] = hn;
       }
-      if constexpr (Z) store_row<MASK, G32, V>(so, j, rows, o);
+      if constexpr (Z) {
+        store_row<MASK, G32, V>(so, j, rows, o);
+        so.next();
+      }
     }
     dx.set(q.dx, q.dxs_b, q.dxs_t, b, t0, c0, p.L, p.D, GE, T, chunk, lane * V, ok);
     da.set(q.dgate_a, q.dgas_b, q.dgas_t, b, t0, c0, p.L, p.D, GE, T, chunk, lane * V, ok);
     dg.set(q.dgate_x, q.dgxs_b, q.dgxs_t, b, t0, c0, p.L, p.D, GE, T, chunk, lane * V, ok);
+    dx.last(T);
+    da.last(T);
+    dg.last(T);
 #pragma unroll
     for (int j = T - 1; j >= 0; --j) {
       float ox[V], oa[V], og[V];
@@ -679,9 +720,8 @@ struct Bwd : Place<V> {
         const float x = elem(xr[j], v);
         const float lam = g[j][v] + mi[v];
         mi[v] = a[j][v] * lam;
-        // du = lam (a h_{t-1} - i x a^2 / s)
-        const float du = mi[v] * __builtin_fmaf(-(i[j][v] * x) * a[j][v], is[j][v], u[j][v]);
-        const float dv = lam * (om[j][v] * is[j][v]);
+        const float du = mi[v] * zf[j][v];  // lam (a h_{t-1} - i x a^2 / s)
+        const float dv = lam * s[j][v];
         ox[v] = dv * i[j][v];
         oa[v] = du * A[v] * __builtin_fmaf(-r[j][v], r[j][v], r[j][v]);
         og[v] = dv * x * __builtin_fmaf(-i[j][v], i[j][v], i[j][v]);
@@ -692,10 +732,13 @@ struct Bwd : Place<V> {
         sbx[v] += og[v];
       }
       store_row<MASK, G32, V>(dx, j, rows, ox);
+      dx.prev();
       store_row<MASK, G32, V>(da, j, rows, oa);
+      da.prev();
       store_row<MASK, G32, V>(dg, j, rows, og);
+      dg.prev();
     }
-    // The 16 chunks' sums, added in order.  P, H and O were last read before
+    // The chunks' sums, added in order.  P, H and O were last read before
     // the barrier.
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -719,7 +762,7 @@ struct Bwd : Place<V> {
 };
 
 template <bool BF16, bool GF32, bool Z, int V>
-__global__ __launch_bounds__(NT) void gated_bwd_kernel(GatedBwdParams q, Chain cn, unsigned tiles, int64_t nseg) {
+__global__ __launch_bounds__(kBwdNT, kBwdWaves) void gated_bwd_kernel(GatedBwdParams q, Chain cn, unsigned tiles, int64_t nseg) {
   typedef Bwd<BF16, GF32, Z, V> F;
   __shared__ typename F::Shared sh;
   const GatedParams& p = q.f;
@@ -824,9 +867,9 @@ void launch_fwd(const GatedParams& p, hipStream_t stream) {
   const dim3 grid = seg_grid<V>(p, nseg, tiles);
   const Chain q = make_chain(p, p.chain, nseg, stream);
   if (p.y)
-    hipLaunchKernelGGL((gated_fwd_kernel<BF16, YF32, Z, V, true>), grid, dim3(NT), 0, stream, p, q, tiles, nseg);
+    hipLaunchKernelGGL((gated_fwd_kernel<BF16, YF32, Z, V, true>), grid, dim3(kFwdNT), 0, stream, p, q, tiles, nseg);
   else
-    hipLaunchKernelGGL((gated_fwd_kernel<BF16, false, false, V, false>), grid, dim3(NT), 0, stream, p, q, tiles, nseg);
+    hipLaunchKernelGGL((gated_fwd_kernel<BF16, false, false, V, false>), grid, dim3(kFwdNT), 0, stream, p, q, tiles, nseg);
 }
 
 template <bool BF16, bool YF32, int V>
@@ -849,7 +892,7 @@ void launch_bwd(const GatedBwdParams& q, hipStream_t stream) {
   unsigned tiles;
   const dim3 grid = seg_grid<V>(p, nseg, tiles);
   const Chain cn = make_chain(p, p.chain, nseg, stream);
-  hipLaunchKernelGGL((gated_bwd_kernel<BF16, GF32, Z, V>), grid, dim3(NT), 0, stream, q, cn, tiles, nseg);
+  hipLaunchKernelGGL((gated_bwd_kernel<BF16, GF32, Z, V>), grid, dim3(kBwdNT), 0, stream, q, cn, tiles, nseg);
   launch_column_sums(q.part, p.batch * nseg, 3 * p.D, p.D, q.dA, q.dbias_a, q.dbias_x, stream);
 }
 

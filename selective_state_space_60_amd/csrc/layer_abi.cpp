@@ -113,8 +113,8 @@ GatedPlan plan_gated(int64_t batch, int64_t seqlen, int64_t dim) {
   GatedPlan pl;
   auto parts = [&](int64_t n) { return (seqlen + n - 1) / n; };
   pl.nk = parts(ssm::kGatedCkptSteps);
-  pl.fwd_seg = parts(ssm::kGatedChunks * ssm::kGatedFwdSteps);
-  pl.bwd_seg = parts(ssm::kGatedChunks * ssm::kGatedBwdSteps);
+  pl.fwd_seg = parts(ssm::kGatedFwdChunks * ssm::kGatedFwdSteps);
+  pl.bwd_seg = parts(ssm::kGatedBwdChunks * ssm::kGatedBwdSteps);
   pl.blocks = batch * ((dim + 31) / 32) + 7;  // at one channel per lane, rounded up to eight
   return pl;
 }

@@ -172,12 +172,13 @@ struct GatedParams {
 };
 
 // Tiling (also used by the host planner): a workgroup owns 32 lanes x (1 or 2)
-// channels over a segment of 16 chunks.
-constexpr int kGatedChunks = 16;
+// channels over a segment of 8 chunks.
+constexpr int kGatedFwdChunks = 8;
+constexpr int kGatedBwdChunks = 8;
 constexpr int kGatedFwdSteps = 16;  // steps per chunk, forward
 constexpr int kGatedBwdSteps = 8;   // steps per chunk, backward
 constexpr int kGatedCkptSteps = 64;
-constexpr int kGatedSpanSteps = 256;  // rows a kernel addresses from one base, at most
+constexpr int kGatedSpanSteps = 128;  // rows a kernel addresses from one base, at most
 constexpr int kGatedPolls = 1 << 16;  // tens of milliseconds; a wait is microseconds
 
 // Bytes of the words of nseg segments: a pair and a state per channel.
