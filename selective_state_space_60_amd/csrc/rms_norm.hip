@@ -36,6 +36,12 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
 }
 
+// Batch row and step of row r (fewer than 2^24 rows).
+__device__ __forceinline__ void split_row(int64_t r, int64_t batch, int64_t L, int64_t& b, int64_t& t) {
+  b = batch == 1 ? 0 : (uint32_t)r / (uint32_t)L;
+  t = r - b * L;
+}
+
 __device__ __forceinline__ float bf16_at(const void* p, int64_t i) {
   return __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16);
 }
@@ -43,7 +49,7 @@ __device__ __forceinline__ float bf16_at(const void* p, int64_t i) {
 // Columns [col, col + 8) of a row, of which the first n exist (n may be <= 0
 // or > 8); the others are 0.  Rows need only their element's alignment: wide
 // global accesses may be unaligned here.
-__device__ __forceinline__ void load8(const void* row, int type, int64_t col, int64_t n, float (&o)[V]) {
+__device__ __forceinline__ void load8(const void* row, int type, int col, int n, float (&o)[V]) {
   if (type == kNormBF16) {
     if (n >= V) {
       u32x4_t w;
@@ -67,7 +73,7 @@ __device__ __forceinline__ void load8(const void* row, int type, int64_t col, in
   }
 }
 
-__device__ __forceinline__ void store8(void* row, int type, int64_t col, int64_t n, const float (&o)[V]) {
+__device__ __forceinline__ void store8(void* row, int type, int col, int n, const float (&o)[V]) {
   if (type == kNormBF16) {
     if (n >= V) {
       u32x4_t w;
@@ -94,7 +100,7 @@ __device__ __forceinline__ void store8(void* row, int type, int64_t col, int64_t
 }
 
 // Eight values, already divided by their scale, to e4m3 (nearest even).
-__device__ __forceinline__ void store8_e4m3(void* row, int64_t col, int64_t n, const float (&o)[V]) {
+__device__ __forceinline__ void store8_e4m3(void* row, int col, int n, const float (&o)[V]) {
   u32x2_t w = {0, 0};
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -144,19 +150,28 @@ __device__ __forceinline__ float group_max(float v, int lanes) {
 template <int TPR, int CH>
 __global__ __launch_bounds__(NT) void norm_fwd_kernel(NormParams p, int64_t rows) {
   constexpr int WPR = TPR / 64;  // waves per row
+  const int D = (int)p.D;
   __shared__ float lds[2][4];
   const int lane = threadIdx.x % TPR, wave = threadIdx.x / 64;
   const int64_t r = (int64_t)blockIdx.x * (NT / TPR) + threadIdx.x / TPR;
   if (r >= rows) return;  // whole waves; with TPR == NT the whole workgroup
-  const int64_t b = r / p.L, t = r % p.L;
+  int64_t b, t;
+  split_row(r, p.batch, p.L, b, t);
   const int xe = p.x_type == kNormF32 ? 4 : 2, re = p.r_type == kNormF32 ? 4 : 2, oe = p.ro_type == kNormF32 ? 4 : 2;
   const void* x = (const char*)p.x + (b * p.xs_b + t * p.xs_t) * xe;
-  float f[CH][V];
+  float f[CH][V], w[CH][V];
   float ss = 0.f;
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
-    const int64_t col = (int64_t)(k * TPR + lane) * V;
-    load8(x, p.x_type, col, p.D - col, f[k]);
+    const int col = (k * TPR + lane) * V;
+    load8(x, p.x_type, col, D - col, f[k]);
+  }
+  // the weights come along with the row: asked for behind the reduction they
+  // would be a second wait (a wide row has too many to hold)
+  constexpr bool kEarly = CH <= 5;
+  if constexpr (kEarly) {
+#pragma unroll
+    for (int k = 0; k < CH; ++k) load8(p.weight, kNormF32, (k * TPR + lane) * V, D - (k * TPR + lane) * V, w[k]);
   }
   if (p.residual) {
     const void* res = (const char*)p.residual + (b * p.rs_b + t * p.rs_t) * re;
@@ -164,18 +179,18 @@ __global__ __launch_bounds__(NT) void norm_fwd_kernel(NormParams p, int64_t rows
     float g[CH][V];
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int64_t col = (int64_t)(k * TPR + lane) * V;
-      load8(res, p.r_type, col, p.D - col, g[k]);
+      const int col = (k * TPR + lane) * V;
+      load8(res, p.r_type, col, D - col, g[k]);
     }
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int64_t col = (int64_t)(k * TPR + lane) * V;
+      const int col = (k * TPR + lane) * V;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         f[k][i] += g[k][i];
         if (p.ro_type == kNormBF16) f[k][i] = (float)(__bf16)f[k][i];
       }
-      store8(out, p.ro_type, col, p.D - col, f[k]);
+      store8(out, p.ro_type, col, D - col, f[k]);
     }
   }
 #pragma unroll
@@ -192,12 +207,11 @@ __global__ __launch_bounds__(NT) void norm_fwd_kernel(NormParams p, int64_t rows
   float amax = 0.f;
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
-    const int64_t col = (int64_t)(k * TPR + lane) * V;
-    float w[V];
-    load8(p.weight, kNormF32, col, p.D - col, w);
+    const int col = (k * TPR + lane) * V;
+    if constexpr (!kEarly) load8(p.weight, kNormF32, col, D - col, w[k]);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      f[k][i] = f[k][i] * rstd * w[i];
+      f[k][i] = f[k][i] * rstd * w[k][i];
       amax = fmaxf(amax, fabsf(f[k][i]));
     }
   }
@@ -205,8 +219,8 @@ __global__ __launch_bounds__(NT) void norm_fwd_kernel(NormParams p, int64_t rows
   if (p.y_type != kNormE4M3) {
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int64_t col = (int64_t)(k * TPR + lane) * V;
-      store8(y, p.y_type, col, p.D - col, f[k]);
+      const int col = (k * TPR + lane) * V;
+      store8(y, p.y_type, col, D - col, f[k]);
     }
     return;
   }
@@ -218,23 +232,24 @@ __global__ __launch_bounds__(NT) void norm_fwd_kernel(NormParams p, int64_t rows
       amax = fmaxf(fmaxf(lds[1][0], lds[1][1]), fmaxf(lds[1][2], lds[1][3]));
     }
   }
-  const int64_t ng = p.group ? (p.D + p.group - 1) / p.group : 1;
+  const int shift = p.group == 32 ? 5 : p.group == 64 ? 6 : 7;  // of a group
+  const int64_t ng = p.group ? (D + (1 << shift) - 1) >> shift : 1;
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
-    const int64_t col = (int64_t)(k * TPR + lane) * V;
+    const int col = (k * TPR + lane) * V;
     float m = amax;
     if (p.group) {
       m = 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) m = fmaxf(m, fabsf(f[k][i]));
-      m = group_max(m, (int)p.group / V);
+      m = group_max(m, (1 << shift) / V);
     }
     const float scale = fmaxf(m / kE4M3Max, kMinScale);
     const float inv = 1.f / scale;
 #pragma unroll
     for (int i = 0; i < V; ++i) f[k][i] *= inv;
-    store8_e4m3(y, col, p.D - col, f[k]);
-    if (p.group ? col < p.D && col % p.group == 0 : col == 0) p.scale[r * ng + (p.group ? col / p.group : 0)] = scale;
+    store8_e4m3(y, col, D - col, f[k]);
+    if (p.group ? col < D && (col & ((1 << shift) - 1)) == 0 : col == 0) p.scale[r * ng + (p.group ? col >> shift : 0)] = scale;
   }
 }
 
@@ -244,6 +259,7 @@ __global__ __launch_bounds__(NT) void norm_fwd_kernel(NormParams p, int64_t rows
 template <int TPR, int CH>
 __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormBwdParams p, int64_t rows) {
   constexpr int RPB = NT / TPR;
+  const int D = (int)p.D;
   __shared__ float lds[2][2][4];
   const int lane = threadIdx.x % TPR, wave = threadIdx.x / 64, sub = threadIdx.x / TPR;
   const int de = p.dy_type == kNormF32 ? 4 : 2, re = p.row_type == kNormF32 ? 4 : 2;
@@ -256,26 +272,27 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormBwdParams p, int64_t r
   int buf = 0;
   // with TPR == NT every thread of the workgroup runs the same number of rounds
   for (int64_t r = (int64_t)blockIdx.x * RPB + sub; r < rows; r += (int64_t)gridDim.x * RPB, buf ^= 1) {
-    const int64_t b = r / p.L, t = r % p.L;
+    int64_t b, t;
+    split_row(r, p.batch, p.L, b, t);
     const void* dy = (const char*)p.dy + (b * p.dys_b + t * p.dys_t) * de;
     const void* row = (const char*)p.row + (b * p.rs_b + t * p.rs_t) * re;
     float f[CH][V], g[CH][V];
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int64_t col = (int64_t)(k * TPR + lane) * V;
-      load8(row, p.row_type, col, p.D - col, f[k]);
+      const int col = (k * TPR + lane) * V;
+      load8(row, p.row_type, col, D - col, f[k]);
     }
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int64_t col = (int64_t)(k * TPR + lane) * V;
-      load8(dy, p.dy_type, col, p.D - col, g[k]);
+      const int col = (k * TPR + lane) * V;
+      load8(dy, p.dy_type, col, D - col, g[k]);
     }
     float ss = 0.f, s1 = 0.f;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int64_t col = (int64_t)(k * TPR + lane) * V;
+      const int col = (k * TPR + lane) * V;
       float w[V];
-      load8(p.weight, kNormF32, col, p.D - col, w);
+      load8(p.weight, kNormF32, col, D - col, w);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         ss = __builtin_fmaf(f[k][i], f[k][i], ss);
@@ -299,11 +316,11 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormBwdParams p, int64_t r
     void* dx = (char*)p.dx + (b * p.dxs_b + t * p.dxs_t) * xe;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int64_t col = (int64_t)(k * TPR + lane) * V;
+      const int col = (k * TPR + lane) * V;
       float w[V], o[V];
-      load8(p.weight, kNormF32, col, p.D - col, w);
+      load8(p.weight, kNormF32, col, D - col, w);
       if (p.dres) {
-        load8(dres, p.dres_type, col, p.D - col, o);
+        load8(dres, p.dres_type, col, D - col, o);
       } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) o[i] = 0.f;
@@ -314,7 +331,7 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormBwdParams p, int64_t r
         acc[k][i] = __builtin_fmaf(g[k][i], hat, acc[k][i]);
         o[i] += __builtin_fmaf(rstd, g[k][i] * w[i], -hat * coef);
       }
-      store8(dx, p.dx_type, col, p.D - col, o);
+      store8(dx, p.dx_type, col, D - col, o);
     }
   }
   float* part = p.part + (int64_t)blockIdx.x * p.D;
@@ -336,8 +353,8 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormBwdParams p, int64_t r
   } else {
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int64_t col = (int64_t)(k * TPR + lane) * V;
-      store8(part, kNormF32, col, p.D - col, acc[k]);
+      const int col = (k * TPR + lane) * V;
+      store8(part, kNormF32, col, D - col, acc[k]);
     }
   }
 }
