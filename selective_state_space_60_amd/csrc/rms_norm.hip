@@ -287,6 +287,24 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormBwdParams p, int64_t r
       const int col = (k * TPR + lane) * V;
       load8(dy, p.dy_type, col, D - col, g[k]);
     }
+    // dres comes along with the row, and so do the weights: asked for behind
+    // the reduction they would be a second wait (a wide row has too many to hold)
+    constexpr bool kEarly = CH <= 2;
+    const void* dres = (const char*)p.dres + (b * p.drs_b + t * p.drs_t) * se;
+    float o[CH][V];
+    auto load_dres = [&](int k) {
+      const int col = (k * TPR + lane) * V;
+      if (p.dres) {
+        load8(dres, p.dres_type, col, D - col, o[k]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[k][i] = 0.f;
+      }
+    };
+    if constexpr (kEarly) {
+#pragma unroll
+      for (int k = 0; k < CH; ++k) load_dres(k);
+    }
     float ss = 0.f, s1 = 0.f;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
@@ -312,26 +330,20 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormBwdParams p, int64_t r
     }
     const float rstd = __builtin_amdgcn_rsqf(ss / (float)p.D + p.eps);
     const float coef = s1 * rstd / (float)p.D * rstd;  // mean(weight dy hat) rstd
-    const void* dres = (const char*)p.dres + (b * p.drs_b + t * p.drs_t) * se;
     void* dx = (char*)p.dx + (b * p.dxs_b + t * p.dxs_t) * xe;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
       const int col = (k * TPR + lane) * V;
-      float w[V], o[V];
+      float w[V];
       load8(p.weight, kNormF32, col, D - col, w);
-      if (p.dres) {
-        load8(dres, p.dres_type, col, D - col, o);
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = 0.f;
-      }
+      if constexpr (!kEarly) load_dres(k);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float hat = f[k][i] * rstd;
         acc[k][i] = __builtin_fmaf(g[k][i], hat, acc[k][i]);
-        o[i] += __builtin_fmaf(rstd, g[k][i] * w[i], -hat * coef);
+        o[k][i] += __builtin_fmaf(rstd, g[k][i] * w[i], -hat * coef);
       }
-      store8(dx, p.dx_type, col, D - col, o);
+      store8(dx, p.dx_type, col, D - col, o[k]);
     }
   }
   float* part = p.part + (int64_t)blockIdx.x * p.D;
@@ -359,9 +371,12 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormBwdParams p, int64_t r
   }
 }
 
-// A wave per row up to 4096 columns once the rows give every compute unit a
-// workgroup of four; a workgroup per row otherwise.
+// Forward: a wave per row up to 4096 columns once the rows give every compute
+// unit a workgroup of four; a workgroup per row otherwise.  Backward: a wave up
+// to 1024 columns only, since the sums of dweight take registers of their own
+// (4096 x 4096 bf16: 87 us with a wave per row, 39 us with a workgroup).
 bool wave_rows(int64_t rows, int64_t dim) { return dim <= 4096 && rows >= 1024; }
+bool wave_rows_bwd(int64_t rows, int64_t dim) { return dim <= 1024 && rows >= 1024; }
 
 template <int TPR, int CH>
 void launch_fwd(const NormParams& p, int64_t rows, hipStream_t stream) {
@@ -377,13 +392,21 @@ void launch_bwd(const NormBwdParams& p, int64_t rows, hipStream_t stream) {
 
 }  // namespace
 
+// As many workgroups as are resident at once: with more, a second, short round
+// follows (16384 x 5120: 167 us at 1024 workgroups, 228 us at 1280).  A thread
+// of up to 3 column groups leaves room for four workgroups a compute unit, of 4
+// for three, beyond that for one.  Two rows each at least, as each workgroup's
+// sums are written and read once (1001 x 1777: 14.0 us, with one row each 15.8).
 int norm_bwd_parts(int64_t rows, int64_t dim) {
-  const int64_t blocks = wave_rows(rows, dim) ? (rows + 3) / 4 : rows;
-  return (int)std::min<int64_t>(blocks, 768);
+  const bool wave = wave_rows_bwd(rows, dim);
+  const int64_t blocks = wave ? (rows + 3) / 4 : rows;
+  const int64_t ch = wave ? 1 : (dim + NT * V - 1) / (NT * V);
+  const int64_t cap = 256 * (ch <= 3 ? 4 : ch <= 4 ? 3 : 1);
+  return (int)std::min({blocks, cap, std::max<int64_t>(256, (blocks + 1) / 2)});
 }
 
-#define SSM_NORM_DISPATCH(LAUNCH, P)                      \
-  if (wave_rows(rows, (P).D)) {                           \
+#define SSM_NORM_DISPATCH(LAUNCH, P, WAVE)                \
+  if (WAVE(rows, (P).D)) {                           \
     const int64_t ch = ((P).D + 64 * V - 1) / (64 * V);   \
     if (ch <= 1) LAUNCH<64, 1>(P, rows, stream);          \
     else if (ch <= 2) LAUNCH<64, 2>(P, rows, stream);     \
@@ -403,13 +426,13 @@ int norm_bwd_parts(int64_t rows, int64_t dim) {
 
 hipError_t launch_rms_norm(const NormParams& p, hipStream_t stream) {
   const int64_t rows = p.batch * p.L;
-  SSM_NORM_DISPATCH(launch_fwd, p)
+  SSM_NORM_DISPATCH(launch_fwd, p, wave_rows)
   return hipGetLastError();
 }
 
 hipError_t launch_rms_norm_bwd(const NormBwdParams& p, hipStream_t stream) {
   const int64_t rows = p.batch * p.L;
-  SSM_NORM_DISPATCH(launch_bwd, p)
+  SSM_NORM_DISPATCH(launch_bwd, p, wave_rows_bwd)
   launch_column_sums(p.part, p.parts, p.D, p.D, p.dweight, nullptr, nullptr, stream);
   return hipGetLastError();
 }
