@@ -433,7 +433,9 @@ typedef struct {
  *              ckpt[b, k] = the state before step 64k, as ssm_gated_scan_bwd
  *              takes it with SSM_HAS_CKPT
  * io is SSM_F32 or SSM_BF16 and is the same for x, gate_a, gate_x, z.
- * Other flags are not accepted.  Outputs may not overlap inputs or each other.
+ * Other flags are not accepted.  Outputs may not overlap inputs or each other;
+ * here and in the entry points below, different columns of one row-major
+ * buffer (slices of one projection) do not overlap.
  * Segments of a sequence run side by side and pass the state on through the
  * workspace, so two calls that may overlap in time need workspaces of their
  * own.  A workgroup's wait for its predecessor is bounded; when it runs out

@@ -7,12 +7,18 @@ Order of the block ("Mamba ë…¼ë¬¸ ë¦¬ë·°", tildalice.io, Mamba ë¸”ë¡ ì•„í‚¤í…ì
 SelectiveSSM listing): in_proj to x and z; Conv1D + SiLU on x; x_proj to
 B | C | dt; dt_proj (with bias, softplus applied in the scan); the selective
 scan; y * SiLU(z); out_proj.
+
+``mamba_layer_fwd`` puts the block behind an RMS norm on a residual stream.
+``gated_layer_fwd`` / ``gated_layer_bwd`` are the same kind of layer around the
+gated linear recurrence, and ``gated_layer_step`` is its decode step, whose
+projections take 4-bit weights.
 """
 from __future__ import annotations
 
 import torch
 
-from . import causal_conv1d, selective_scan_fwd
+from . import (causal_conv1d, gated_scan_bwd, gated_scan_ckpt, gated_scan_fwd, gated_state_update, rms_norm,
+               rms_norm_bwd, selective_scan_fwd, w4_matvec, w4_quantize)
 
 
 class BlockWeights:
@@ -52,3 +58,83 @@ def mamba_block_fwd(u: torch.Tensor, w: BlockWeights, mark=None) -> torch.Tensor
     out = torch.mm(y.view(T, E), w.W_out_t).view(batch, L, M)           # out_proj
     if mark: mark("out_proj")
     return out
+
+
+def mamba_layer_fwd(u: torch.Tensor, residual: torch.Tensor, w: BlockWeights, norm_weight: torch.Tensor,
+                    eps: float = 1e-5):
+    """Pre-norm layer: adds u (batch, L, d_model) bf16 to the residual stream
+    (bf16 or fp32) and runs the block on its RMS norm.  Returns (block output,
+    new residual)."""
+    y, residual, _ = rms_norm(u, norm_weight, eps=eps, residual=residual)
+    return mamba_block_fwd(y, w), residual
+
+
+class GatedLayerWeights:
+    """Device weights of one pre-norm gated recurrent layer: d_model M, width
+    E.  norm (M,), A, bias_a, bias_x (E,) fp32; w_in (4 E, M) and w_out (M, E)
+    bf16, the rows of w_in in the order x, recurrence gate, input gate, z.
+    The GEMMs take the projections transposed, as BlockWeights keeps them; with
+    `group` (32, 64 or 128, a divisor of M and E) they are also kept in 4 bits
+    with a scale for each `group` columns, as the decode step takes them."""
+
+    def __init__(self, norm, w_in, w_out, A, bias_a, bias_x, group=None, eps=1e-5):
+        self.norm, self.A, self.bias_a, self.bias_x, self.eps = norm, A, bias_a, bias_x, eps
+        self.E, self.M = w_out.shape[1], w_out.shape[0]
+        self.w_in_t, self.w_out_t = w_in.t().contiguous(), w_out.t().contiguous()
+        if group is not None:
+            self.q_in, self.q_out = w4_quantize(w_in, group), w4_quantize(w_out, group)
+
+    def split(self, proj):
+        """x, recurrence gate, input gate, z: slices of a projection's output (or of its gradient)."""
+        return proj.split(self.E, -1)
+
+
+def gated_layer_fwd(u, residual, w: GatedLayerWeights, h0=None, lens=None, train=False):
+    """u: (batch, L, M) bf16; residual: (batch, L, M) bf16 or fp32; h0, lens as
+    in gated_scan_fwd.  Returns (output (batch, L, M) bf16, new residual, final
+    state (batch, E) fp32), and with train what gated_layer_bwd takes."""
+    batch, L, M = u.shape
+    y, residual, _ = rms_norm(u, w.norm, eps=w.eps, residual=residual)
+    proj = torch.mm(y.view(batch * L, M), w.w_in_t).view(batch, L, 4 * w.E)
+    x, ga, gx, z = w.split(proj)
+    ckpt = gated_scan_ckpt(batch, L, w.E, u.device) if train else None
+    h, state = gated_scan_fwd(x, ga, gx, w.A, w.bias_a, w.bias_x, z=z, h0=h0, lens=lens, want_hlast=True, ckpt=ckpt)
+    out = torch.mm(h.view(batch * L, w.E), w.w_out_t).view(batch, L, M)
+    if not train:
+        return out, residual, state
+    return out, residual, state, {"row": residual, "y": y, "proj": proj, "h": h, "h0": h0, "lens": lens, "ckpt": ckpt}
+
+
+def gated_layer_bwd(dout, dresidual, w: GatedLayerWeights, saved: dict, dstate=None) -> dict:
+    """Gradients of gated_layer_fwd(..., train=True): dout (batch, L, M) bf16
+    and dresidual (the residual's type) reach its outputs, dstate (batch, E)
+    its final state.  Returns du (of the layer input and of the residual alike,
+    the residual's type), dh0, and the weights' gradients dnorm, dA, dbias_a,
+    dbias_x (fp32), dw_in_t, dw_out_t (bf16, as the GEMMs hold the weights)."""
+    batch, L, M = dout.shape
+    T = batch * L
+    dout2 = dout.reshape(T, M)
+    dh = torch.mm(dout2, w.w_out_t.t().contiguous()).view(batch, L, w.E)
+    dw_out_t = torch.mm(saved["h"].view(T, w.E).t().contiguous(), dout2)
+    x, ga, gx, z = w.split(saved["proj"])
+    dproj = torch.empty_like(saved["proj"])
+    parts = dict(zip(("dx", "dgate_a", "dgate_x", "dz"), w.split(dproj)))
+    g = gated_scan_bwd(dh, x, ga, gx, w.A, w.bias_a, w.bias_x, z=z, h0=saved["h0"], lens=saved["lens"],
+                       dh_last=dstate, ckpt=saved["ckpt"], out=parts)
+    dproj2 = dproj.view(T, 4 * w.E)
+    dy = torch.mm(dproj2, w.w_in_t.t().contiguous()).view(batch, L, M)
+    dw_in_t = torch.mm(saved["y"].view(T, M).t().contiguous(), dproj2)
+    n = rms_norm_bwd(dy, saved["row"], w.norm, eps=w.eps, dres=dresidual, grad_dtype=dresidual.dtype)
+    return {"du": n["dx"], "dh0": g.get("dh0"), "dnorm": n["dweight"], "dA": g["dA"], "dbias_a": g["dbias_a"],
+            "dbias_x": g["dbias_x"], "dw_in_t": dw_in_t, "dw_out_t": dw_out_t}
+
+
+def gated_layer_step(u, residual, w: GatedLayerWeights, state):
+    """One token of each of up to 64 sequences: u (batch, M) bf16, residual
+    (batch, M), state (batch, E) fp32, advanced in place.  The projections are
+    products with the 4-bit weights.  Returns (output (batch, M) bf16, new
+    residual)."""
+    y, residual, _ = rms_norm(u, w.norm, eps=w.eps, residual=residual)
+    x, ga, gx, z = w.split(w4_matvec(y, *w.q_in))
+    h = gated_state_update(state, x, ga, gx, w.A, w.bias_a, w.bias_x, z=z)
+    return w4_matvec(h, *w.q_out), residual

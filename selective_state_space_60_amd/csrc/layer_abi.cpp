@@ -54,6 +54,38 @@ ssm_status check_out(bool on, const ssm_tensor_desc& t, int ndim, const int64_t*
   return non_overlapping(t) ? SSM_OK : SSM_ERR_STRIDE;
 }
 
+// One tensor of a call in memory.
+struct Placed {
+  const ssm_tensor_desc* t = nullptr;
+  uintptr_t at = 0;
+  Span span;
+};
+
+// Whether two tensors are different columns of one row-major buffer: all their
+// outer strides are whole multiples of one row, and within a row they do not
+// meet.  (Slices of one projection, or of its gradient, interleave so.)
+bool different_columns(const Placed& a, const Placed& b) {
+  int64_t row = 0;
+  for (const Placed* p : {&a, &b}) {
+    const ssm_tensor_desc& t = *p->t;
+    if (t.ndim < 2 || (t.shape[t.ndim - 1] > 1 && t.stride[t.ndim - 1] != 1)) return false;
+    for (int i = 0; i < t.ndim - 1; ++i)
+      if (t.shape[i] > 1 && t.stride[i] > 0) {
+        const int64_t bytes = t.stride[i] * esize(t.dtype);
+        if (!row || bytes < row) row = bytes;
+      }
+  }
+  if (!row) return false;
+  for (const Placed* p : {&a, &b})
+    for (int i = 0; i < p->t->ndim - 1; ++i)
+      if (p->t->shape[i] > 1 && p->t->stride[i] * esize(p->t->dtype) % row) return false;
+  const Placed& lo = a.at <= b.at ? a : b;
+  const Placed& hi = a.at <= b.at ? b : a;
+  const int64_t off = (int64_t)((hi.at - lo.at) % (uintptr_t)row);
+  auto width = [](const Placed& p) { return p.t->shape[p.t->ndim - 1] * esize(p.t->dtype); };
+  return off >= width(lo) && off + width(hi) <= row;
+}
+
 // The pointers of a call: presence, alignment, overlap.
 class Ptrs {
  public:
@@ -67,25 +99,28 @@ class Ptrs {
   ssm_status check(Span workspace = Span()) const {
     for (int i = 0; i < nout_; ++i) {
       for (int k = 0; k < nin_; ++k)
-        if (overlap(outs_[i], ins_[k])) return SSM_ERR_ALIAS;
+        if (meet(outs_[i], ins_[k])) return SSM_ERR_ALIAS;
       for (int k = i + 1; k < nout_; ++k)
-        if (overlap(outs_[i], outs_[k])) return SSM_ERR_ALIAS;
-      if (overlap(outs_[i], workspace)) return SSM_ERR_ALIAS;
+        if (meet(outs_[i], outs_[k])) return SSM_ERR_ALIAS;
+      if (overlap(outs_[i].span, workspace)) return SSM_ERR_ALIAS;
     }
     for (int k = 0; k < nin_; ++k)
-      if (overlap(workspace, ins_[k])) return SSM_ERR_ALIAS;
+      if (overlap(workspace, ins_[k].span)) return SSM_ERR_ALIAS;
     return SSM_OK;
   }
 
  private:
-  static ssm_status add(bool on, const ssm_tensor_desc& t, const void* ptr, int64_t align, Span* to, int& n) {
+  static bool meet(const Placed& a, const Placed& b) { return overlap(a.span, b.span) && !different_columns(a, b); }
+  static ssm_status add(bool on, const ssm_tensor_desc& t, const void* ptr, int64_t align, Placed* to, int& n) {
     if (!on) return SSM_OK;
     if (!ptr) return SSM_ERR_NULL;
     if (!aligned(ptr, align ? align : esize(t.dtype))) return SSM_ERR_ALIGN;
-    to[n++] = span_of(t, ptr);
+    to[n].t = &t;
+    to[n].at = (uintptr_t)ptr;
+    to[n++].span = span_of(t, ptr);
     return SSM_OK;
   }
-  Span ins_[16], outs_[12];
+  Placed ins_[16], outs_[12];
   int nin_ = 0, nout_ = 0;
 };
 

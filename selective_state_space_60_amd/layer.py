@@ -30,6 +30,7 @@ _plans: dict = {}
 # The current stream's handle without building a Stream object (a microsecond of a decode step's call).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _sig(tensors):
@@ -73,7 +74,7 @@ def _keep(key, plan):
 
 def _launch(plan, tensors, stream):
     """Run the plan on these tensors, on `stream` (default: the current stream of their device)."""
-    if plan.index != torch.cuda.current_device():
+    if plan.index != _current_device():
         with torch.cuda.device(plan.index):
             return _launch(plan, tensors, stream)
     handle = _raw_stream(plan.index) if stream is None else stream.cuda_stream
@@ -99,9 +100,9 @@ def _empty(stream, shape, dtype, device):
 
 
 def _like(stream, t, dtype=None):
-    """Contiguous memory of t's shape."""
+    """Memory of t's shape, dense (contiguous unless t is a dense permutation)."""
     if stream is None:
-        return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
+        return torch.empty_like(t) if dtype is None else torch.empty_like(t, dtype=dtype)
     return _empty(stream, t.shape, dtype or t.dtype, t.device)
 
 
@@ -150,19 +151,25 @@ def gated_scan_fwd(x, gate_a, gate_x, A, bias_a=None, bias_x=None, z=None, h0=No
 
 
 def gated_scan_bwd(dy, x, gate_a, gate_x, A, bias_a=None, bias_x=None, z=None, h0=None, lens=None, dh_last=None,
-                   ckpt=None, stream=None) -> dict:
+                   ckpt=None, out=None, stream=None) -> dict:
     """Gradients of sum(dy * y) + sum(dh_last * h_last) for y, h_last =
     gated_scan_fwd(x, gate_a, gate_x, A, bias_a, bias_x, z, h0, lens) (see
     include/ssm.h).  ckpt: the forward's checkpoints of the same inputs;
-    without them they are recomputed.
+    without them they are recomputed.  out: optional dict with memory for any
+    of dx, dgate_a, dgate_x, dz (slices of one projection's gradient, say).
 
     Returns a dict: dx, dgate_a, dgate_x, dz (if z), all of dy's dtype (x's or
     fp32), and fp32 dA, dbias_a, dbias_x (dim,; if given) and dh0 (if h0)."""
     ins = (x, gate_a, gate_x, A, bias_a, bias_x, z, h0, lens, ckpt, dy, dh_last)
-    key = ("gated_scan_bwd", _sig(ins))
+    given = tuple([out.get(k) for k in ("dx", "dgate_a", "dgate_x", "dz")]) if out else (None,) * 4
+    key = ("gated_scan_bwd", _sig(ins), _sig(given) if out else None)
     plan = _plans.get(key)
-    out = {"dx": _like(stream, dy), "dgate_a": _like(stream, dy), "dgate_x": _like(stream, dy),
-           "dz": None if z is None else _like(stream, dy), "dA": _like(stream, A),
+    dx, dga, dgx, dz = [_like(stream, dy) if t is None else t for t in given[:3]] + [given[3]]
+    if z is None:
+        dz = None
+    elif dz is None:
+        dz = _like(stream, dy)
+    out = {"dx": dx, "dgate_a": dga, "dgate_x": dgx, "dz": dz, "dA": _like(stream, A),
            "dbias_a": None if bias_a is None else _like(stream, bias_a),
            "dbias_x": None if bias_x is None else _like(stream, bias_x),
            "dh0": None if h0 is None else _like(stream, h0)}

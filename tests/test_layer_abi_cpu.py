@@ -168,6 +168,29 @@ def test_gated_bwd_workspace():
     assert call(p.dA, m.value) == S.SSM_ERR_ALIAS
 
 
+def test_columns_of_one_buffer():
+    """Gradients as columns of one matrix interleave without overlapping;
+    columns that meet, or rows of another length, are refused."""
+    L, D, wide = 100, 8, 32
+    for shift, status in ((0, S.SSM_ERR_WORKSPACE), (1, S.SSM_ERR_ALIAS)):
+        d, p = gated_bwd(L=L, D=D, flags=BWD_ALL)
+        for k, name in enumerate(("dx", "dgate_a", "dgate_x", "dz")):
+            setattr(d, name, td((2, L, D), "bf16", (L * wide, wide, 1)))
+            setattr(p, name, (1 << 45) + 2 * (k * D - (shift if k == 2 else 0)))
+        assert S.lib().ssm_gated_scan_bwd(ctypes.byref(d), ctypes.byref(p), None, 0, None) == status
+    d, p = gated_bwd(L=L, D=D, flags=BWD_ALL)
+    d.dx, p.dx = td((2, L, D), "bf16", (L * wide, wide, 1)), 1 << 45
+    d.dz, p.dz = td((2, L, D), "bf16", (L * (wide + 4), wide + 4, 1)), (1 << 45) + 16
+    assert S.lib().ssm_gated_scan_bwd(ctypes.byref(d), ctypes.byref(p), None, 0, None) == S.SSM_ERR_ALIAS
+    # y into a free column block of the buffer that holds the inputs: only the workspace is missing
+    for col, status in ((3, S.SSM_ERR_WORKSPACE), (2, S.SSM_ERR_ALIAS)):
+        d, p = gated(L=300)
+        for name, k in (("x", 0), ("gate_a", 1), ("gate_x", 2), ("y", col)):
+            setattr(d, name, td((2, 300, 8), "bf16", (300 * wide, wide, 1)))
+            setattr(p, name, (1 << 45) + 16 * k)
+        assert S.lib().ssm_gated_scan_fwd(ctypes.byref(d), ctypes.byref(p), None, 0, None) == status
+
+
 def gated_update(batch=3, D=8, io="bf16", flags=0):
     d, p = S.GatedUpdateDesc(), S.GatedUpdatePtrs()
     d.batch, d.dim, d.flags = batch, D, flags
