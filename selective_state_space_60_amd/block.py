@@ -95,11 +95,11 @@ def gated_layer_fwd(u, residual, w: GatedLayerWeights, h0=None, lens=None, train
     state (batch, E) fp32), and with train what gated_layer_bwd takes."""
     batch, L, M = u.shape
     y, residual, _ = rms_norm(u, w.norm, eps=w.eps, residual=residual)
-    proj = torch.mm(y.view(batch * L, M), w.w_in_t).view(batch, L, 4 * w.E)
+    proj = torch.mm(y.reshape(batch * L, M), w.w_in_t).view(batch, L, 4 * w.E)
     x, ga, gx, z = w.split(proj)
     ckpt = gated_scan_ckpt(batch, L, w.E, u.device) if train else None
     h, state = gated_scan_fwd(x, ga, gx, w.A, w.bias_a, w.bias_x, z=z, h0=h0, lens=lens, want_hlast=True, ckpt=ckpt)
-    out = torch.mm(h.view(batch * L, w.E), w.w_out_t).view(batch, L, M)
+    out = torch.mm(h.reshape(batch * L, w.E), w.w_out_t).view(batch, L, M)
     if not train:
         return out, residual, state
     return out, residual, state, {"row": residual, "y": y, "proj": proj, "h": h, "h0": h0, "lens": lens, "ckpt": ckpt}
@@ -115,7 +115,7 @@ def gated_layer_bwd(dout, dresidual, w: GatedLayerWeights, saved: dict, dstate=N
     T = batch * L
     dout2 = dout.reshape(T, M)
     dh = torch.mm(dout2, w.w_out_t.t().contiguous()).view(batch, L, w.E)
-    dw_out_t = torch.mm(saved["h"].view(T, w.E).t().contiguous(), dout2)
+    dw_out_t = torch.mm(saved["h"].reshape(T, w.E).t().contiguous(), dout2)
     x, ga, gx, z = w.split(saved["proj"])
     dproj = torch.empty_like(saved["proj"])
     parts = dict(zip(("dx", "dgate_a", "dgate_x", "dz"), w.split(dproj)))
@@ -123,7 +123,7 @@ def gated_layer_bwd(dout, dresidual, w: GatedLayerWeights, saved: dict, dstate=N
                        dh_last=dstate, ckpt=saved["ckpt"], out=parts)
     dproj2 = dproj.view(T, 4 * w.E)
     dy = torch.mm(dproj2, w.w_in_t.t().contiguous()).view(batch, L, M)
-    dw_in_t = torch.mm(saved["y"].view(T, M).t().contiguous(), dproj2)
+    dw_in_t = torch.mm(saved["y"].reshape(T, M).t().contiguous(), dproj2)
     n = rms_norm_bwd(dy, saved["row"], w.norm, eps=w.eps, dres=dresidual, grad_dtype=dresidual.dtype)
     return {"du": n["dx"], "dh0": g.get("dh0"), "dnorm": n["dweight"], "dA": g["dA"], "dbias_a": g["dbias_a"],
             "dbias_x": g["dbias_x"], "dw_in_t": dw_in_t, "dw_out_t": dw_out_t}

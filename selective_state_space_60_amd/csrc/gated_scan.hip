@@ -62,7 +62,7 @@ static_assert(kBwdSeg % kGatedCkptSteps == 0, "every backward segment starts at 
 static_assert(kFwdSeg <= kGatedSpanSteps && kBwdSeg <= kGatedSpanSteps, "a segment's rows fit the offsets");
 
 constexpr uint32_t kRsrcWord3 = 0x00020000u;  // raw (unformatted) buffer access
-constexpr uint32_t kMaxRange = 0x40000000u;   // the host keeps a round's rows below this
+constexpr uint32_t kMaxRange = 0x40000000u;   // the host keeps a segment's rows below this
 constexpr uint32_t kFar = 0x7FFFFFF0u;        // past every range: loads give 0, stores are dropped
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, int64_t bytes) {
@@ -70,7 +70,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, int64_t by
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)range, (int)kRsrcWord3);
 }
 
-// The rows [t, L) of channels [c, D) of batch row b, as one buffer.  A round
+// The rows [t, L) of channels [c, D) of batch row b, as one buffer.  A segment
 // that lies inside the sequence addresses only rows of it; one that crosses
 // its end sends the rows behind it to kFar.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_from(const void* p, int64_t sb, int64_t st, int64_t b,
@@ -84,7 +84,7 @@ struct Raw {
   uint32_t w[BF16 ? (V + 1) / 2 : V];
 };
 
-// Byte offset of a row of the round: the lane's own offset `off` and the row's
+// Byte offset of a row of the segment: the lane's own offset `off` and the row's
 // `row` (block-uniform, in a scalar register).
 template <bool BF16, int V>
 __device__ __forceinline__ Raw<BF16, V> load(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t row) {
@@ -173,7 +173,7 @@ __device__ __forceinline__ int64_t row_len(const GatedParams& p, int64_t b) {
   return n < 0 ? 0 : n > p.L ? p.L : n;
 }
 
-// One stream of a tile: its buffer for a round, the lane's offset of the first
+// One stream of a tile: its buffer for a segment, the lane's offset of the first
 // row of its chunk and the row stride, in bytes.
 struct Stream {
   __amdgpu_buffer_rsrc_t r;
@@ -206,17 +206,22 @@ struct Stream {
 };
 
 // The current row, number j of the chunk, and on to the next; with MASK rows
-// from `n` on are sent out of range.
+// from `n` on are sent out of range.  The range check takes the scalar offset
+// off the range, so that offset must stay below it: it does where the whole
+// segment lies inside the sequence, and with MASK it is 0.
 template <bool MASK, bool BF16, int V>
 __device__ __forceinline__ Raw<BF16, V> load_row(Stream& s, int j, int n) {
-  const Raw<BF16, V> o = load<BF16, V>(s.r, !MASK || j < n ? s.off : kFar, s.at);
+  Raw<BF16, V> o;
+  if constexpr (MASK) o = load<BF16, V>(s.r, j < n ? s.off + s.at : kFar, 0);
+  else o = load<BF16, V>(s.r, s.off, s.at);
   s.next();
   return o;
 }
 
 template <bool MASK, bool F32, int V>
 __device__ __forceinline__ void store_row(const Stream& s, int j, int n, const float (&o)[V]) {
-  store<F32, V>(s.r, !MASK || j < n ? s.off : kFar, s.at, o);
+  if constexpr (MASK) store<F32, V>(s.r, j < n ? s.off + s.at : kFar, 0, o);
+  else store<F32, V>(s.r, s.off, s.at, o);
 }
 
 // ------------------------------------------------------------------ segments

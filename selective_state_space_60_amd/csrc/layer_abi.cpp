@@ -15,8 +15,9 @@ using namespace ssm::abi;
 
 namespace {
 
-constexpr int64_t kMaxBlocks512 = (int64_t)1 << 23;  // a launch holds fewer than 2^32 threads
-constexpr int64_t kMaxBlocks256 = (int64_t)1 << 24;
+// a launch holds fewer than 2^32 threads: blocks of 1024, 512, 256
+constexpr int64_t kMaxBlocks1024 = (int64_t)1 << 22, kMaxBlocks512 = (int64_t)1 << 23,
+                  kMaxBlocks256 = (int64_t)1 << 24;
 constexpr int64_t kMaxSpan = (int64_t)1 << 30;       // bytes a kernel addresses from one base
 
 // Sizes whose products stay far from overflowing.
@@ -141,7 +142,7 @@ constexpr uint32_t kGatedBwdFlags = kGatedInFlags | SSM_HAS_CKPT | SSM_HAS_DHLAS
 // tile of channels; with more than one, words pass the state on.
 struct GatedPlan {
   int64_t nk = 0, fwd_seg = 0, bwd_seg = 0;
-  int64_t blocks = 0;  // of one segment
+  bool fits = false;  // the grids and the words
 };
 
 GatedPlan plan_gated(int64_t batch, int64_t seqlen, int64_t dim) {
@@ -150,12 +151,10 @@ GatedPlan plan_gated(int64_t batch, int64_t seqlen, int64_t dim) {
   pl.nk = parts(ssm::kGatedCkptSteps);
   pl.fwd_seg = parts(ssm::kGatedFwdChunks * ssm::kGatedFwdSteps);
   pl.bwd_seg = parts(ssm::kGatedBwdChunks * ssm::kGatedBwdSteps);
-  pl.blocks = batch * ((dim + 31) / 32) + 7;  // at one channel per lane, rounded up to eight
+  const int64_t tiles = (dim + 31) / 32;  // at one channel per lane
+  pl.fits = batch * tiles + 7 < kMaxBlocks256 && tiles < kMaxBlocks1024 && pl.bwd_seg < ((int64_t)1 << 30) &&
+            (__int128)pl.bwd_seg * batch * dim * 12 < ((int64_t)1 << 35);
   return pl;
-}
-
-bool gated_grid_ok(const GatedPlan& pl) {
-  return pl.blocks < kMaxBlocks512 && pl.bwd_seg < ((int64_t)1 << 30);
 }
 
 // A segment's rows must fit the 32-bit offsets of the kernel.
@@ -219,7 +218,7 @@ ssm_status validate_gated(const ssm_gated_desc* d) {
   SSM_TRY(check_out(d->flags & SSM_WANT_HLAST, d->h_last, 2, sh.bd, d->h_last.dtype == SSM_F32, false, true));
   SSM_TRY(check_out(d->flags & SSM_WANT_CKPT, d->ckpt, 3, sh.ck, d->ckpt.dtype == SSM_F32, false, true));
   if (!gated_fits(d->y)) return SSM_ERR_UNSUPPORTED;
-  if (!gated_grid_ok(plan_gated(d->batch, d->seqlen, d->dim))) return SSM_ERR_UNSUPPORTED;
+  if (!plan_gated(d->batch, d->seqlen, d->dim).fits) return SSM_ERR_UNSUPPORTED;
   return SSM_OK;
 }
 
@@ -289,7 +288,7 @@ ssm_status validate_gated_bwd(const ssm_gated_bwd_desc* d) {
   if (!gated_fits(d->dy) || !gated_fits(d->dx) || !gated_fits(d->dgate_a) || !gated_fits(d->dgate_x) ||
       ((f & SSM_HAS_Z) && !gated_fits(d->dz)))
     return SSM_ERR_UNSUPPORTED;
-  if (!gated_grid_ok(plan_gated(d->batch, d->seqlen, d->dim))) return SSM_ERR_UNSUPPORTED;
+  if (!plan_gated(d->batch, d->seqlen, d->dim).fits) return SSM_ERR_UNSUPPORTED;
   return SSM_OK;
 }
 

@@ -116,6 +116,10 @@ __device__ __forceinline__ void store8_e4m3(void* row, int col, int n, const flo
   }
 }
 
+// 1 / sqrt(v), correctly rounded steps: the hardware's estimate takes a
+// subnormal mean (tiny rows, eps 0) for zero.  Once a row.
+__device__ __forceinline__ float inv_root(float v) { return 1.f / __builtin_sqrtf(v); }
+
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
   return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
@@ -203,7 +207,7 @@ __global__ __launch_bounds__(NT) void norm_fwd_kernel(NormParams p, int64_t rows
     __syncthreads();
     ss = (lds[0][0] + lds[0][1]) + (lds[0][2] + lds[0][3]);
   }
-  const float rstd = __builtin_amdgcn_rsqf(ss / (float)p.D + p.eps);
+  const float rstd = inv_root(ss / (float)D + p.eps);
   float amax = 0.f;
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
@@ -328,8 +332,8 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormBwdParams p, int64_t r
       ss = (lds[buf][0][0] + lds[buf][0][1]) + (lds[buf][0][2] + lds[buf][0][3]);
       s1 = (lds[buf][1][0] + lds[buf][1][1]) + (lds[buf][1][2] + lds[buf][1][3]);
     }
-    const float rstd = __builtin_amdgcn_rsqf(ss / (float)p.D + p.eps);
-    const float coef = s1 * rstd / (float)p.D * rstd;  // mean(weight dy hat) rstd
+    const float rstd = inv_root(ss / (float)D + p.eps);
+    const float coef = s1 * rstd / (float)D * rstd;  // mean(weight dy hat) rstd
     void* dx = (char*)p.dx + (b * p.dxs_b + t * p.dxs_t) * xe;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
