@@ -5,12 +5,13 @@
 //   y   = weight row rstd,  rstd = rsqrt(mean(row^2) + eps)
 //
 // Bound by HBM: a row is read once, kept in registers across the reduction
-// and written once.  One wave owns a row of up to 4096 columns when there are
-// rows enough to fill the card (no barrier, 4 rows a workgroup); a workgroup
-// of four waves owns a longer row, or a short one of a few-row problem, where
-// the row's own latency is the time.  A lane holds groups of 8 consecutive
-// columns: 16-byte loads of bf16, and an e4m3 group of 32, 64 or 128 columns
-// is 4, 8 or 16 neighbouring lanes, whose largest value is found with DPP.
+// and written once (16384 x 2560, bf16 in, fp32 residual in and out, bf16 out:
+// 95 us, 5.3 TB/s; a large copy runs at 4.7).  A workgroup of four waves owns a
+// row, or a wave each of four narrow rows (no barrier).  A lane holds groups of
+// 8 consecutive columns: 16-byte loads of bf16, and an e4m3 group of 32, 64 or
+// 128 columns is 4, 8 or 16 neighbouring lanes, whose largest value is found
+// with DPP.  A few hundred rows take one pass of latencies (333 x 5120 to e4m3:
+// 7.5 us, of which a launch is 2.5).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -172,7 +173,7 @@ __global__ __launch_bounds__(NT) void norm_fwd_kernel(NormParams p, int64_t rows
   }
   // the weights come along with the row: asked for behind the reduction they
   // would be a second wait (a wide row has too many to hold)
-  constexpr bool kEarly = CH <= 5;
+  constexpr bool kEarly = CH <= 4;
   if constexpr (kEarly) {
 #pragma unroll
     for (int k = 0; k < CH; ++k) load8(p.weight, kNormF32, (k * TPR + lane) * V, D - (k * TPR + lane) * V, w[k]);
@@ -375,12 +376,12 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormBwdParams p, int64_t r
   }
 }
 
-// Forward: a wave per row up to 4096 columns once the rows give every compute
-// unit a workgroup of four; a workgroup per row otherwise.  Backward: a wave up
-// to 1024 columns only, since the sums of dweight take registers of their own
-// (4096 x 4096 bf16: 87 us with a wave per row, 39 us with a workgroup).
-bool wave_rows(int64_t rows, int64_t dim) { return dim <= 4096 && rows >= 1024; }
-bool wave_rows_bwd(int64_t rows, int64_t dim) { return dim <= 1024 && rows >= 1024; }
+// A wave per row for narrow rows, once they are enough to fill the card; a
+// workgroup per row otherwise.  Measured with the residual's addition, a wave
+// against a workgroup per row: 16384 x 768 33 us against 42, 2048 x 256 3.7
+// against 5.1; but 16384 x 2560 104 against 95, 1024 x 768 4.5 against 4.3,
+// 256 x 2560 5.4 against 3.9.  Backward 4096 x 4096: 87 against 39.
+bool wave_rows(int64_t rows, int64_t dim) { return dim <= 1024 && rows >= 2048; }
 
 template <int TPR, int CH>
 void launch_fwd(const NormParams& p, int64_t rows, hipStream_t stream) {
@@ -402,23 +403,17 @@ void launch_bwd(const NormBwdParams& p, int64_t rows, hipStream_t stream) {
 // for three, beyond that for one.  Two rows each at least, as each workgroup's
 // sums are written and read once (1001 x 1777: 14.0 us, with one row each 15.8).
 int norm_bwd_parts(int64_t rows, int64_t dim) {
-  const bool wave = wave_rows_bwd(rows, dim);
+  const bool wave = wave_rows(rows, dim);
   const int64_t blocks = wave ? (rows + 3) / 4 : rows;
   const int64_t ch = wave ? 1 : (dim + NT * V - 1) / (NT * V);
   const int64_t cap = 256 * (ch <= 3 ? 4 : ch <= 4 ? 3 : 1);
   return (int)std::min({blocks, cap, std::max<int64_t>(256, (blocks + 1) / 2)});
 }
 
-#define SSM_NORM_DISPATCH(LAUNCH, P, WAVE)                \
-  if (WAVE(rows, (P).D)) {                           \
-    const int64_t ch = ((P).D + 64 * V - 1) / (64 * V);   \
-    if (ch <= 1) LAUNCH<64, 1>(P, rows, stream);          \
-    else if (ch <= 2) LAUNCH<64, 2>(P, rows, stream);     \
-    else if (ch <= 3) LAUNCH<64, 3>(P, rows, stream);     \
-    else if (ch <= 4) LAUNCH<64, 4>(P, rows, stream);     \
-    else if (ch <= 5) LAUNCH<64, 5>(P, rows, stream);     \
-    else if (ch <= 6) LAUNCH<64, 6>(P, rows, stream);     \
-    else LAUNCH<64, 8>(P, rows, stream);                  \
+#define SSM_NORM_DISPATCH(LAUNCH, P)                      \
+  if (wave_rows(rows, (P).D)) {                           \
+    if ((P).D <= 64 * V) LAUNCH<64, 1>(P, rows, stream);  \
+    else LAUNCH<64, 2>(P, rows, stream);                  \
   } else {                                                \
     const int64_t ch = ((P).D + NT * V - 1) / (NT * V);   \
     if (ch <= 1) LAUNCH<NT, 1>(P, rows, stream);          \
@@ -430,13 +425,13 @@ int norm_bwd_parts(int64_t rows, int64_t dim) {
 
 hipError_t launch_rms_norm(const NormParams& p, hipStream_t stream) {
   const int64_t rows = p.batch * p.L;
-  SSM_NORM_DISPATCH(launch_fwd, p, wave_rows)
+  SSM_NORM_DISPATCH(launch_fwd, p)
   return hipGetLastError();
 }
 
 hipError_t launch_rms_norm_bwd(const NormBwdParams& p, hipStream_t stream) {
   const int64_t rows = p.batch * p.L;
-  SSM_NORM_DISPATCH(launch_bwd, p, wave_rows_bwd)
+  SSM_NORM_DISPATCH(launch_bwd, p)
   launch_column_sums(p.part, p.parts, p.D, p.D, p.dweight, nullptr, nullptr, stream);
   return hipGetLastError();
 }

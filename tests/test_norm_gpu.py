@@ -35,7 +35,7 @@ def make(rows, dim, dt, residual=None, seed=0):
 
 SIZES = [(1, 1), (3, 7), (2, 8), (5, 9), (4, 511), (3, 512), (2, 513), (7, 2047), (2, 2048), (3, 2056), (2, 4097),
          (1, 8200), (2, 16384), (1030, 40), (1025, 520), (1500, 1025), (1024, 1536), (1024, 2049), (1026, 2560),
-         (1024, 2570), (1024, 4096)]
+         (1024, 2570), (1024, 4096), (2047, 264), (2048, 7), (2050, 512), (2049, 513), (2051, 1024), (2048, 1025)]
 PAIRS = [(F32, None), (F32, F32), (BF16, None), (BF16, BF16), (BF16, F32)]
 
 
@@ -62,7 +62,7 @@ def test_forward_backward(size, dt, res):
 
 @pytest.mark.parametrize("group", [0, 32, 64, 128])
 @pytest.mark.parametrize("size", [(3, 5), (2, 32), (4, 100), (3, 128), (2, 1000), (3, 2049), (2, 5120), (1, 16384),
-                                  (1100, 72), (1030, 1537)], ids=lambda s: "%dx%d" % s)
+                                  (1100, 72), (1030, 1537), (2050, 72), (2049, 1000)], ids=lambda s: "%dx%d" % s)
 def test_e4m3(size, group):
     """Scales are the group's largest |y| / 448; values the nearest e4m3 of
     y / scale (half a step: 2^-4 of the value, 2^-10 below the normals)."""
