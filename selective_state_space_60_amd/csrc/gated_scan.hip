@@ -33,6 +33,10 @@
 //   lam_t = g_t + m_t,  m_{t-1} = a_t lam_t
 // is affine in the carry m as well, with the same product P, and its carry is
 // found among the later segments in the same way.
+//
+// Measured: forward 4 x 4096 x 5120 bf16 with z 191 us (4.4 TB/s; VALU 55 %
+// busy; 243 us with 16 chunks a segment and fewer waves), 1 x 131072 x 1536 fp32
+// 622 us (5.2 TB/s); backward 8 x 2048 x 1536 bf16 with z 121 us (3.7 TB/s).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -1,6 +1,6 @@
 """GPU parity of the gated linear recurrence (ssm_gated_scan_fwd / _bwd,
 ssm_gated_state_update) against its fp64 definition, step by step, at sizes
-where a chunk (8 and 16 steps), a round (128 and 256), a checkpoint (64) or a
+where a chunk (8 and 16 steps), a segment (64 and 128), a checkpoint (64) or a
 channel tile (32 and 64) ends inside, starts or is missed by one."""
 import pytest
 
