@@ -11,7 +11,8 @@ a shape costs a lookup; pointers and values are never kept.
 from __future__ import annotations
 
 import ctypes
-import struct
+import importlib.util
+import os
 
 import torch
 
@@ -33,14 +34,35 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
+MARSHAL_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_marshal.so")
+
+
+def _bind():
+    """Put the native module's functions (csrc/marshal.cpp) in the place of the two below."""
+    global _sig, _run
+    if not os.path.exists(MARSHAL_PATH):
+        raise ImportError("_marshal.so is not built (run __graft_entry__.build()): " + MARSHAL_PATH)
+    spec = importlib.util.spec_from_file_location(__package__ + "._marshal", MARSHAL_PATH)
+    native = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(native)
+    _sig, _run = native.signature, native.launch
+
+
 def _sig(tensors):
-    """What a descriptor depends on: type, shape, strides and device of each tensor."""
-    return tuple([None if t is None else (t.dtype, t.shape, t.stride(), t.get_device()) for t in tensors])
+    """What a descriptor depends on: type, device, sizes and strides of each tensor."""
+    _bind()
+    return _sig(tensors)
+
+
+def _run(*args):
+    """The status of an entry point called on a tuple of tensors."""
+    _bind()
+    return _run(*args)
 
 
 class _Plan:
     """An entry point with a descriptor of fixed shapes, and the workspace size it asks for."""
-    __slots__ = ("entry", "fn", "desc", "address", "pack", "index", "nbytes")
+    __slots__ = ("entry", "fn", "desc", "address", "index", "nbytes")
 
     def __init__(self, entry, Desc, names, sizes, flags, tensors, size_entry=None):
         index = tensors[0].get_device()
@@ -55,10 +77,10 @@ class _Plan:
         d.flags = flags
         for name, t in zip(names, tensors):
             setattr(d, name, tensor_desc(t))
-        self.entry, self.fn, self.index, self.desc = entry, getattr(lib(), entry), index, d
-        self.address = ctypes.addressof(d)
-        self.pack = struct.Struct("%dP" % len(names)).pack  # the pointer structs hold one pointer per name
-        self.nbytes = None
+        # the pointer structs of these entry points hold one pointer per tensor, in the order of `names`
+        self.entry, self.index, self.desc, self.address = entry, index, d, ctypes.addressof(d)
+        self.fn = ctypes.cast(getattr(lib(), entry), ctypes.c_void_p).value
+        self.nbytes = -1  # an entry point without a workspace
         if size_entry is not None:
             n = ctypes.c_size_t()
             _check(getattr(lib(), size_entry)(self.address, ctypes.byref(n)), size_entry)
@@ -78,14 +100,10 @@ def _launch(plan, tensors, stream):
         with torch.cuda.device(plan.index):
             return _launch(plan, tensors, stream)
     handle = _raw_stream(plan.index) if stream is None else stream.cuda_stream
-    ptrs = plan.pack(*[0 if t is None else t.data_ptr() for t in tensors])
-    if plan.nbytes is None:
-        status = plan.fn(plan.address, ptrs, handle)
-    elif plan.nbytes == 0:
-        status = plan.fn(plan.address, ptrs, None, 0, handle)
-    else:
+    ws = None
+    if plan.nbytes > 0:
         ws = _empty(stream, (plan.nbytes,), torch.uint8, tensors[0].device)
-        status = plan.fn(plan.address, ptrs, ws.data_ptr(), plan.nbytes, handle)
+    status = _run(plan.fn, plan.address, tensors, 0 if ws is None else ws.data_ptr(), plan.nbytes, handle)
     if status:
         _check(status, plan.entry)
 
