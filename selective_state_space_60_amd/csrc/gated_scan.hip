@@ -596,9 +596,10 @@ struct Bwd : Place<V> {
         const float dy = elem(dr[j], v);
         g[j][v] = dy;
         if constexpr (Z) {
-          const float z = elem(zr[j], v), sz = gate(z, 0.f);
-          g[j][v] = dy * (z * sz);
-          if constexpr (GRADS) zf[j][v] = dy * (sz * __builtin_fmaf(z, 1.f - sz, 1.f));
+          // dy silu(z) and dy silu'(z) = dy sig(z) + dy silu(z) (1 - sig(z))
+          const float z = elem(zr[j], v), sz = gate(z, 0.f), ds = dy * sz;
+          g[j][v] = ds * z;
+          if constexpr (GRADS) zf[j][v] = __builtin_fmaf(g[j][v], 1.f - sz, ds);
         }
         if constexpr (GRADS) {
           i[j][v] = gate(elem(gr[j], v), ch.nbx[v]);
@@ -730,11 +731,12 @@ struct Bwd : Place<V> {
         const float lam = g[j][v] + mi[v];
         mi[v] = a[j][v] * lam;
         const float du = mi[v] * zf[j][v];  // lam (a h_{t-1} - i x a^2 / s)
-        const float dv = lam * s[j][v];
-        ox[v] = dv * i[j][v];
-        oa[v] = du * A[v] * __builtin_fmaf(-r[j][v], r[j][v], r[j][v]);
-        og[v] = dv * x * __builtin_fmaf(-i[j][v], i[j][v], i[j][v]);
+        ox[v] = lam * s[j][v] * i[j][v];
+        // dA = du r, dgate_a = dA A (1 - r), dgate_x = dx x (1 - i)
         float dA = du * r[j][v];
+        const float ga = dA * A[v], gx = ox[v] * x;
+        oa[v] = __builtin_fmaf(-r[j][v], ga, ga);
+        og[v] = __builtin_fmaf(-i[j][v], gx, gx);
         if (MASK && j >= live) ox[v] = oa[v] = og[v] = dA = 0.f;
         sA[v] += dA;
         sba[v] += oa[v];
