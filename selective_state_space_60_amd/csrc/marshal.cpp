@@ -85,11 +85,11 @@ PyObject* launch(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
       PyErr_SetString(PyExc_ValueError, "no entry point, or too many tensors");
       return nullptr;
     }
-    const void* ptrs[kMaxTensors];
+    void* ptrs[kMaxTensors];
     for (Py_ssize_t i = 0; i < n; ++i) {
       const at::Tensor* t;
       if (!tensor_of(PyTuple_GET_ITEM(args[2], i), &t)) return nullptr;
-      ptrs[i] = t ? t->const_data_ptr() : nullptr;
+      ptrs[i] = t ? t->mutable_data_ptr() : nullptr;
     }
     int status;
     Py_BEGIN_ALLOW_THREADS

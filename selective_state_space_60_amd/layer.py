@@ -118,10 +118,12 @@ def _empty(stream, shape, dtype, device):
 
 
 def _like(stream, t, dtype=None):
-    """Memory of t's shape, dense (contiguous unless t is a dense permutation)."""
+    """Memory of t's shape, dense (contiguous unless t is a dense permutation).
+    Its strides follow from t's alone: a plan's key does not hold them."""
     if stream is None:
         return torch.empty_like(t) if dtype is None else torch.empty_like(t, dtype=dtype)
-    return _empty(stream, t.shape, dtype or t.dtype, t.device)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t, dtype=dtype)
 
 
 # -------------------------------------------------- gated linear recurrence
@@ -168,6 +170,9 @@ def gated_scan_fwd(x, gate_a, gate_x, A, bias_a=None, bias_x=None, z=None, h0=No
     return y, h_last
 
 
+_GATED_OUT = ("dx", "dgate_a", "dgate_x", "dz")
+
+
 def gated_scan_bwd(dy, x, gate_a, gate_x, A, bias_a=None, bias_x=None, z=None, h0=None, lens=None, dh_last=None,
                    ckpt=None, out=None, stream=None) -> dict:
     """Gradients of sum(dy * y) + sum(dh_last * h_last) for y, h_last =
@@ -179,7 +184,11 @@ def gated_scan_bwd(dy, x, gate_a, gate_x, A, bias_a=None, bias_x=None, z=None, h
     Returns a dict: dx, dgate_a, dgate_x, dz (if z), all of dy's dtype (x's or
     fp32), and fp32 dA, dbias_a, dbias_x (dim,; if given) and dh0 (if h0)."""
     ins = (x, gate_a, gate_x, A, bias_a, bias_x, z, h0, lens, ckpt, dy, dh_last)
-    given = tuple([out.get(k) for k in ("dx", "dgate_a", "dgate_x", "dz")]) if out else (None,) * 4
+    given = (None,) * 4
+    if out:
+        given = tuple([out.get(k) for k in _GATED_OUT])
+        if not out.keys() <= set(_GATED_OUT):
+            raise ValueError("gated_scan_bwd: out takes " + ", ".join(_GATED_OUT))
     key = ("gated_scan_bwd", _sig(ins), _sig(given) if out else None)
     plan = _plans.get(key)
     dx, dga, dgx, dz = [_like(stream, dy) if t is None else t for t in given[:3]] + [given[3]]

@@ -347,6 +347,12 @@ def test_wrappers_refuse_host_tensors():
             call()
 
 
+def test_backward_refuses_unknown_outputs():
+    x, v = torch.zeros(2, 4, 8), torch.zeros(8)
+    with pytest.raises(ValueError, match="dgate_a"):
+        S.gated_scan_bwd(x, x, x, x, v, out={"dA": v})
+
+
 def test_quantize_on_the_host():
     w = torch.tensor([[7.0, -7.0, 0.0, 1.0] * 8, [0.0] * 32])
     packed, scale = S.w4_quantize(w, group=32)
@@ -355,3 +361,27 @@ def test_quantize_on_the_host():
     for bad in (lambda: S.w4_quantize(w, group=16), lambda: S.w4_quantize(w, group=64)):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_signatures():
+    """What a call's descriptor is looked up by tells apart type, shape,
+    strides and absence, and does not depend on address or values."""
+    from selective_state_space_60_amd import layer
+
+    def sig(*tensors):
+        return layer._sig(tensors)
+
+    a = torch.zeros(4, 6)
+    assert sig(a) == sig(torch.ones(4, 6)) and sig(a, None) != sig(a) != sig(None, a)
+    others = [torch.zeros(6, 4), torch.zeros(4, 6, dtype=torch.bfloat16), torch.zeros(4, 12)[:, ::2],
+              torch.zeros(4, 12)[:, :6], torch.zeros(1, 4, 6), torch.zeros(1, 6).expand(4, 6)]
+    assert len({sig(t) for t in others + [a]}) == len(others) + 1
+    for bad in (3, [a]):
+        with pytest.raises(TypeError):
+            sig(bad)
+    with pytest.raises(TypeError):
+        layer._sig([a])
+    with pytest.raises((TypeError, ValueError)):
+        layer._run(0, 0, (a,), 0, -1, 0)
+    with pytest.raises(TypeError):
+        layer._run(1, 2, 3)

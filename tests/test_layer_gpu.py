@@ -213,6 +213,44 @@ def test_streams():
     assert torch.equal(y, y2)
 
 
+def test_permuted_rows_on_a_stream():
+    """Rows laid out (L, batch, dim): the outputs' layout, and with it what a
+    repeated call is looked up by, is the same on a given stream and without."""
+    banner("permuted rows, streams")
+    side = torch.cuda.Stream()
+    flip = lambda v: v.transpose(0, 1).contiguous().transpose(0, 1)  # noqa: E731
+    t, dy = scan_inputs(3, 200, 48, 7), torch.randn(3, 200, 48, device="cuda")
+    x, w = torch.randn(3, 50, 96, device="cuda"), torch.rand(96, device="cuda")
+    want, y = train_scan(t, dy), ssm.rms_norm(x, w)[0]
+    bwd = ssm.rms_norm_bwd(x, x, w)
+    t = {k: flip(v) if v.dim() == 3 else v for k, v in t.items()}
+    dy, x = flip(dy), flip(x)
+    torch.cuda.synchronize()
+    for stream in (None, side, None):
+        got = train_scan(t, dy, stream=stream)
+        y2, again = ssm.rms_norm(x, w, stream=stream)[0], ssm.rms_norm_bwd(x, x, w, stream=stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), stream
+        assert torch.equal(y2, y) and torch.equal(again["dx"], bwd["dx"])
+    t = {k: v[:, 0] if v.dim() == 3 else v for k, v in t.items() if k != "h0"}
+    state = torch.zeros(3, 48, device="cuda")
+    one = [ssm.gated_state_update(state.clone(), **t, stream=s) for s in (None, side, None)]
+    torch.cuda.synchronize()
+    assert torch.equal(one[0], one[1]) and torch.equal(one[0], one[2])
+
+
+def test_lazy_copy_of_a_state():
+    """A state that shares its memory with another tensor until it is written
+    is written alone."""
+    banner("lazy copy")
+    t = {k: v[:, 0] if v.dim() == 3 else v for k, v in scan_inputs(2, 1, 64, 8).items() if k != "h0"}
+    first = torch.randn(2, 64, device="cuda")
+    state, keep = torch._lazy_clone(first), first.clone()
+    ssm.gated_state_update(state, **t)
+    torch.cuda.synchronize()
+    assert torch.equal(first, keep) and not torch.equal(state, keep)
+
+
 def test_wrappers_check_their_arguments():
     x = torch.zeros(2, 4, 8, device="cuda")
     v = torch.zeros(8, device="cuda")
