@@ -632,7 +632,8 @@ typedef struct {
  * zero is 8 without SSM_HAS_ZERO.  Products are bf16 matrix-core products of
  * x with q + 16 (exact in bf16), summed in fp32 by groups; 16 + zero times the
  * group's sum of x is taken off before the group's scale.  A row of x that
- * holds an infinity or a NaN has NaN in its whole row of y.
+ * holds an infinity or a NaN has NaN in its whole row of y; with |x| below
+ * 2^112 no group's sum overflows.
  *   x      : (rows, ins) BF16               rows contiguous and 16-byte aligned
  *   weight : (outs, ins/2) U8 contiguous, 16-byte aligned
  *   scale  : (outs, ins/group) F32 or BF16  contiguous

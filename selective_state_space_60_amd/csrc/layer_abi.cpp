@@ -138,7 +138,7 @@ constexpr uint32_t kGatedInFlags = SSM_HAS_Z | SSM_HAS_H0 | SSM_HAS_BIAS_A | SSM
 constexpr uint32_t kGatedFlags = kGatedInFlags | SSM_WANT_HLAST | SSM_WANT_CKPT;
 constexpr uint32_t kGatedBwdFlags = kGatedInFlags | SSM_HAS_CKPT | SSM_HAS_DHLAST;
 
-// The sequence is cut into segments of 16 chunks, one workgroup each for a
+// The sequence is cut into segments of 8 chunks, one workgroup each for a
 // tile of channels; with more than one, words pass the state on.
 struct GatedPlan {
   int64_t nk = 0, fwd_seg = 0, bwd_seg = 0;

@@ -114,3 +114,15 @@ def test_quantize():
     x = torch.randn(3, 256, generator=g).to(BF16)
     y = ssm.w4_matvec(x.cuda(), packed.cuda(), s.cuda(), y_dtype=F32)
     check(y, x, packed, s, None, None, 64)
+
+
+def test_large_rows():
+    """|x| just below 2^112: no group's sum overflows, zero points of 255 included."""
+    banner("w4 large x")
+    x, w, s, _, _ = make(2, 512, 40, 128, False, False, seed=9, scale_dtype=F32)
+    x = (torch.sign(x.float()) * 2.0 ** 111 * 1.9).to(BF16)
+    x[0] = x[0].abs()
+    z = torch.full((40, 4), 255, dtype=torch.uint8)
+    for zero in (None, z):
+        y = ssm.w4_matvec(x.cuda(), w.cuda(), s.cuda(), zero=None if zero is None else zero.cuda(), y_dtype=F32)
+        check(y, x, w, s, zero, None, 128)
