@@ -26,10 +26,18 @@
 // weights (i, i + 4); x is put into the same order with v_perm before it is
 // stored.
 //
-// A workgroup owns 16 or 32 outputs; its eight waves take every eighth step of
-// 128 of k each, on their own: once a step's operands are in LDS the next
-// step's loads are issued into the same registers, ahead of the products.  The
-// waves' sums are added in order through LDS.
+// A workgroup owns 16 or 32 outputs of 16 rows; its eight waves take every
+// eighth step of 128 of k each, on their own: once a step's operands are in LDS
+// the next step's loads are issued into the same registers, ahead of the
+// products.  The waves' sums are added in order through LDS.  More rows are more
+// workgroups, which read the weights again from L2: all rows in one workgroup
+// (64 x 2560 -> 10240: 25.7 us against 16.8) leave a compute unit two of them
+// and its neighbour one.
+//
+// Measured: 1 x 2560 -> 10240 6.5 us, 16 x 5120 -> 2560 6.0 (a launch is 2.3),
+// 4 x 5120 -> 20480 16.4 (3.3 TB/s of weights).  A lane's step is some 110
+// VALU operations for 64 weights, 64 of them bringing weights into bf16.  Two
+// steps of loads in flight are no better (16 x 5120 -> 2560: 6.6), for their registers.
 #include <hip/hip_runtime.h>
 
 #include "ssm_internal.h"
@@ -54,8 +62,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, int64_t by
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)range, (int)kRsrcWord3);
 }
 
-__device__ __forceinline__ u32x4_t load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-  return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
+__device__ __forceinline__ u32x4_t load16(__amdgpu_buffer_rsrc_t r, uint32_t off, int step) {
+  return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, step, 0));
 }
 
 // dword j of lane group g <-> dword g of lane group j
@@ -91,25 +99,32 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// MT tiles of 16 rows, NL tiles of 16 outputs, GS = group / 32, SF32: fp32
-// scales.  Without zero points their buffer is empty and gives zeros.
-template <int MT, int NL, int GS, bool SF32>
-__global__ __launch_bounds__(NT) void w4_kernel(W4Params p) {
+// XR loads of four rows of x (4 where a tile of 16 may be full), NL tiles of 16
+// outputs, GS = group / 32, SF32: fp32 scales.  Without zero points their
+// buffer is empty and gives zeros.
+template <int XR, int NL, int GS, bool SF32>
+__global__ __launch_bounds__(NT, 4) void w4_kernel(W4Params p, unsigned xtiles) {
   constexpr int NG = 4 / GS;                      // scale groups of a step
   constexpr int SN = (16 * NL * NG + 63) / 64;    // loads of a step's scales
   constexpr int es = SF32 ? 4 : 2;
   struct Stage {
-    u32x4_t w[NL][64], x[256];
-    float2 sc[16 * NL * NG];                      // (scale, -(16 + zero))
+    u32x4_t w[NL][64], x[XR * 64];
+    float2 sc[SN * 64];                           // (scale, -(16 + zero))
   };
   __shared__ union {
     Stage st[W];
-    float sum[W][MT * NL * 4][64];
+    float sum[W][NL * 4][64];
   } sh;
-  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+  const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int col = lane % 16, kg = lane / 16;
-  const int64_t n0 = (int64_t)blockIdx.x * (16 * NL);
-  const int nrows = (int)(p.outs - n0 < 16 * NL ? p.outs - n0 : 16 * NL);
+  // grid.x tiles of outputs, then the same with the next rows (y): with eight, a
+  // tile's weights are read again on the same XCD.  A tile behind the last
+  // runs with every access out of range: a test up here would be a wait for
+  // the first arguments ahead of the others.
+  const int m0 = (int)blockIdx.y * 16;
+  const int64_t n0 = ((int64_t)blockIdx.z * xtiles + blockIdx.x) * (16 * NL);
+  const int64_t left = p.outs - n0;
+  const int nrows = left < 0 ? 0 : left < 16 * NL ? (int)left : 16 * NL;
   const int ins = (int)p.ins, half = ins / 2, groups = ins / (32 * GS), rows = (int)p.rows;
   const int steps = (ins + KS - 1) / KS;
   const __amdgpu_buffer_rsrc_t rw = rsrc(p.weight + n0 * half, (int64_t)nrows * half);
@@ -118,74 +133,75 @@ __global__ __launch_bounds__(NT) void w4_kernel(W4Params p) {
   const __amdgpu_buffer_rsrc_t rx = rsrc(p.x, ((p.rows - 1) * p.xs_m + p.ins) * 2);
   const float zbase = p.zero ? -16.f : -24.f;
   Stage& st = sh.st[wave];
-  // row order of the loads: weights row lane / 4, unit lane % 4; x row lane / 16 (+ 4 i), unit lane % 16
+  // Row order of the loads: weights row lane / 4, unit lane % 4; x row lane /
+  // 16 (+ 4 i), unit lane % 16.  The lane's offsets within a step; rows that
+  // do not exist are out of range.
   const int wrow = lane / 4, wunit = (lane % 4) ^ (wrow / 4);
-  const uint32_t woff = (uint32_t)wrow * (uint32_t)half + (uint32_t)wunit * 16;
-  const uint32_t xstride = (uint32_t)(p.xs_m * 2);
+  uint32_t woff[NL], xoff[XR], soff[SN];
+#pragma unroll
+  for (int n = 0; n < NL; ++n)
+    woff[n] = n * 16 + wrow < nrows ? (uint32_t)(n * 16 + wrow) * (uint32_t)half + (uint32_t)wunit * 16 : kFar;
+#pragma unroll
+  for (int i = 0; i < XR; ++i) {
+    const int row = m0 + 4 * i + kg;
+    xoff[i] = row < rows ? (uint32_t)row * (uint32_t)(p.xs_m * 2) + (uint32_t)col * 16 : kFar;
+  }
+#pragma unroll
+  for (int i = 0; i < SN; ++i) {
+    const int e = lane + i * 64;
+    soff[i] = e / NG < nrows ? (uint32_t)(e / NG * groups + e % NG) : kFar / 4;
+  }
+  // The last step may end early: its x and scales are zeros there (weights of
+  // the next row, which are finite, meet x of zero).
+  const uint32_t xend = (steps - 1) * KS + col * 8 < ins ? 0 : kFar;
+  const uint32_t send = (steps - 1) * NG + lane % NG < groups ? 0 : kFar / 4;
   // operand order of the reads
   const int wread = col * 4 + (kg ^ (col / 4));
-  f32x4_t acc[MT][NL];
+  const int xrow = col % (XR * 4);
+  f32x4_t acc[NL];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int n = 0; n < NL; ++n) acc[m][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int n = 0; n < NL; ++n) acc[n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   // held in registers: with two literals the and and the or stay two instructions
   uint32_t mask = 0x00780078u, base = 0x41804180u;
   asm volatile("" : "+s"(mask), "+v"(base));
   const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, u32x4_t{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
 
-  u32x4_t wq[NL], xq[4];
-  uint32_t sc[SN], zc[SN];
-  // Loads of step s; behind the last step, output or row: zeros.
-  auto load_x = [&](int s, int m) {
-    const int k = s * KS + (lane % 16) * 8;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (m * 16 + 4 * i >= rows) break;  // uniform; rows that do not exist are left as they are
-      const int row = m * 16 + 4 * i + kg;
-      xq[i] = load16(rx, k < ins && row < rows ? (uint32_t)row * xstride + (uint32_t)(k * 2) : kFar);
-    }
+  // A step's loads.  Behind the last step they are made too, out of range:
+  // where paths with and without a load meet, the compiler waits for all.
+  struct Loads {
+    u32x4_t w[NL], x[XR];
+    uint32_t sc[SN], z[SN];
   };
-  auto load_w = [&](int s) {
-    const int k0 = s * KS;
+  auto load = [&](Loads& l, int s) {
+    const bool past = s >= steps;
+    const int at = past ? 0 : s;
+    const uint32_t far = past ? kFar : 0;
+    const uint32_t fx = s == steps - 1 ? xend : far, fs = s == steps - 1 ? send : far / 4;
 #pragma unroll
-    for (int n = 0; n < NL; ++n)
-      wq[n] = load16(rw, k0 + wunit * 32 < ins && n * 16 + wrow < nrows
-                             ? woff + (uint32_t)(n * 16) * (uint32_t)half + (uint32_t)(k0 / 2) : kFar);
+    for (int n = 0; n < NL; ++n) l.w[n] = load16(rw, woff[n] | far, at * (KS / 2));
 #pragma unroll
     for (int i = 0; i < SN; ++i) {
-      const int e = lane + i * 64, row = e / NG, gi = s * NG + e % NG;
-      const uint32_t at = row < nrows && gi < groups ? (uint32_t)(row * groups + gi) : kFar / 4;
-      if constexpr (SF32) sc[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, (int)(at * 4), 0, 0);
-      else sc[i] = __builtin_amdgcn_raw_buffer_load_b16(rs, (int)(at * 2), 0, 0);
-      zc[i] = __builtin_amdgcn_raw_buffer_load_b8(rz, (int)at, 0, 0);
+      const uint32_t e = soff[i] | fs;
+      if constexpr (SF32) l.sc[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, (int)(e * 4), at * NG * 4, 0);
+      else l.sc[i] = __builtin_amdgcn_raw_buffer_load_b16(rs, (int)(e * 2), at * NG * 2, 0);
+      l.z[i] = __builtin_amdgcn_raw_buffer_load_b8(rz, (int)e, p.zero ? at * NG : 0, 0);
     }
-  };
-  auto stage_x = [&](int m) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (m * 16 + 4 * i >= rows) break;
-      const int row = 4 * i + kg;
-      st.x[row * 16 + (lane % 16 ^ row)] = reorder(xq[i]);
-    }
+    for (int i = 0; i < XR; ++i) l.x[i] = load16(rx, xoff[i] | fx, at * (KS * 2));
   };
-  if (wave < steps) {
-    load_w(wave);
-    load_x(wave, 0);
-  }
-  for (int s = wave; s < steps; s += W) {
+  auto step = [&](Loads& l, int s) {
     wave_sync();
 #pragma unroll
-    for (int n = 0; n < NL; ++n) st.w[n][lane] = wq[n];
-    stage_x(0);
+    for (int n = 0; n < NL; ++n) st.w[n][lane] = l.w[n];
 #pragma unroll
     for (int i = 0; i < SN; ++i)
-      if (lane + i * 64 < 16 * NL * NG)
-        st.sc[lane + i * 64] = make_float2(__uint_as_float(SF32 ? sc[i] : sc[i] << 16), zbase - (float)zc[i]);
-    if (s + W < steps) {
-      load_w(s + W);
-      if constexpr (MT == 1) load_x(s + W, 0);
+      st.sc[lane + i * 64] = make_float2(__uint_as_float(SF32 ? l.sc[i] : l.sc[i] << 16), zbase - (float)l.z[i]);
+#pragma unroll
+    for (int i = 0; i < XR; ++i) {
+      const int row = 4 * i + kg;
+      st.x[row * 16 + (col ^ row)] = reorder(l.x[i]);
     }
+    load(l, s + W);
     wave_sync();
     u32x4_t d[NL];
 #pragma unroll
@@ -194,57 +210,40 @@ __global__ __launch_bounds__(NT) void w4_kernel(W4Params p) {
       transpose4(d[n]);
     }
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      if (m * 16 >= rows) break;  // uniform
-      bf16x8_t xa[4];
+    for (int g = 0; g < NG; ++g) {
+      f32x4_t sx = {0.f, 0.f, 0.f, 0.f}, ga[NL];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) xa[j] = __builtin_bit_cast(bf16x8_t, st.x[col * 16 + ((4 * j + kg) ^ col)]);
-      if constexpr (MT > 1) {  // the next tile's rows, or the next step's first
-        const bool last = m == MT - 1 || (m + 1) * 16 >= rows;
-        if (!last || s + W < steps) load_x(last ? s + W : s, last ? 0 : m + 1);
+      for (int n = 0; n < NL; ++n) ga[n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int jj = 0; jj < GS; ++jj) {
+        const int j = g * GS + jj;
+        const bf16x8_t xa = __builtin_bit_cast(bf16x8_t, st.x[xrow * 16 + ((4 * j + kg) ^ xrow)]);
+        sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa, ones, sx, 0, 0, 0);
+#pragma unroll
+        for (int n = 0; n < NL; ++n)
+          ga[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa, widen(d[n][j], mask, base), ga[n], 0, 0, 0);
       }
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        f32x4_t sx = {0.f, 0.f, 0.f, 0.f}, ga[NL];
+      for (int n = 0; n < NL; ++n) {
+        const float2 f = st.sc[(n * 16 + col) * NG + g];
 #pragma unroll
-        for (int n = 0; n < NL; ++n) ga[n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int jj = 0; jj < GS; ++jj) {
-          const int j = g * GS + jj;
-          sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa[j], ones, sx, 0, 0, 0);
-#pragma unroll
-          for (int n = 0; n < NL; ++n)
-            ga[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa[j], widen(d[n][j], mask, base), ga[n], 0, 0, 0);
-        }
-#pragma unroll
-        for (int n = 0; n < NL; ++n) {
-          const float2 f = st.sc[(n * 16 + col) * NG + g];
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            acc[m][n][r] = __builtin_fmaf(f.x, __builtin_fmaf(f.y, sx[r], ga[n][r]), acc[m][n][r]);
-        }
-      }
-      if constexpr (MT > 1) {
-        if (m < MT - 1 && (m + 1) * 16 < rows) {
-          wave_sync();
-          stage_x(m + 1);
-          wave_sync();
-        }
+        for (int r = 0; r < 4; ++r) acc[n][r] = __builtin_fmaf(f.x, __builtin_fmaf(f.y, sx[r], ga[n][r]), acc[n][r]);
       }
     }
-  }
+  };
+  Loads l;
+  load(l, wave);
+  for (int s = wave; s < steps; s += W) step(l, s);
   __syncthreads();  // the stages are done with
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int n = 0; n < NL; ++n)
 #pragma unroll
-    for (int n = 0; n < NL; ++n)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) sh.sum[wave][(m * NL + n) * 4 + r][lane] = acc[m][n][r];
+    for (int r = 0; r < 4; ++r) sh.sum[wave][n * 4 + r][lane] = acc[n][r];
   __syncthreads();
-  for (int i = tid; i < MT * NL * 4 * 64; i += NT) {
+  for (int i = threadIdx.x; i < NL * 4 * 64; i += NT) {
     const int l = i % 64, q = i / 64;
-    const int64_t m = (q / (NL * 4)) * 16 + (l / 16) * 4 + q % 4;
-    const int64_t n = n0 + (q / 4 % NL) * 16 + l % 16;
+    const int64_t m = m0 + (l / 16) * 4 + q % 4;
+    const int64_t n = n0 + (q / 4) * 16 + l % 16;
     if (m >= p.rows || n >= p.outs) continue;
     float sum = p.bias ? p.bias[n * p.bs_n] : 0.f;
 #pragma unroll
@@ -254,30 +253,39 @@ __global__ __launch_bounds__(NT) void w4_kernel(W4Params p) {
   }
 }
 
-template <int MT, int NL, int GS>
+template <int XR, int NL, int GS>
 void launch_s(const W4Params& p, hipStream_t stream) {
-  const dim3 grid((unsigned)((p.outs + 16 * NL - 1) / (16 * NL)));
-  if (p.scale_f32) hipLaunchKernelGGL((w4_kernel<MT, NL, GS, true>), grid, dim3(NT), 0, stream, p);
-  else hipLaunchKernelGGL((w4_kernel<MT, NL, GS, false>), grid, dim3(NT), 0, stream, p);
+  const unsigned mtiles = (unsigned)((p.rows + 15) / 16), ntiles = (unsigned)((p.outs + 16 * NL - 1) / (16 * NL));
+  const unsigned xtiles = mtiles == 1 ? ntiles : 8 * (ntiles / (8 * 65535) + 1);  // z at most 65535
+  const dim3 grid(xtiles, mtiles, (ntiles + xtiles - 1) / xtiles);
+  if (p.scale_f32) hipLaunchKernelGGL((w4_kernel<XR, NL, GS, true>), grid, dim3(NT), 0, stream, p, xtiles);
+  else hipLaunchKernelGGL((w4_kernel<XR, NL, GS, false>), grid, dim3(NT), 0, stream, p, xtiles);
 }
 
-template <int MT, int NL>
+template <int XR, int NL>
 void launch_g(const W4Params& p, hipStream_t stream) {
-  if (p.group == 32) launch_s<MT, NL, 1>(p, stream);
-  else if (p.group == 64) launch_s<MT, NL, 2>(p, stream);
-  else launch_s<MT, NL, 4>(p, stream);
+  if (p.group == 32) launch_s<XR, NL, 1>(p, stream);
+  else if (p.group == 64) launch_s<XR, NL, 2>(p, stream);
+  else launch_s<XR, NL, 4>(p, stream);
+}
+
+template <int XR>
+void launch_n(const W4Params& p, hipStream_t stream) {
+  // 32 outputs a workgroup share x's way through LDS, once there are more than
+  // three tiles of 16 a compute unit (16 against 32: 1 x 2560 -> 14336 7.6 us
+  // against 7.2, 64 x 2560 -> 10240 21.8 against 16.8; but 1 x 2560 -> 10240
+  // 6.5 against 6.8, 16 x 5120 -> 2560 6.0 against 7.8).
+  const int64_t tiles = (p.rows + 15) / 16 * ((p.outs + 15) / 16);
+  if (tiles > 3 * 256) launch_g<XR, 2>(p, stream);
+  else launch_g<XR, 1>(p, stream);
 }
 
 }  // namespace
 
 hipError_t launch_w4_matvec(const W4Params& p, hipStream_t stream) {
-  // Up to 16 rows, 32 outputs a workgroup share x's way through LDS (1 x 2560 ->
-  // 10240: 7.0 us against 7.7 with 16); 16 outputs where 32 would leave compute
-  // units without a workgroup.
-  if (p.rows > 32) launch_g<4, 1>(p, stream);
-  else if (p.rows > 16) launch_g<2, 1>(p, stream);
-  else if (p.outs >= 32 * 256) launch_g<1, 2>(p, stream);
-  else launch_g<1, 1>(p, stream);
+  // one load of x a lane and step instead of four (1 x 2560 -> 10240: 6.5 us against 8.4)
+  if (p.rows <= 4) launch_n<1>(p, stream);
+  else launch_n<4>(p, stream);
   return hipGetLastError();
 }
 
