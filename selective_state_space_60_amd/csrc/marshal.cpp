@@ -1,10 +1,12 @@
-// The two per-call steps of the Python binding that touch every tensor, as a
-// CPython module: reading what a descriptor depends on, and handing the data
-// pointers to an entry point of libssm.  In Python they take 3 us of a decode
-// step's call (ten tensors; a kernel launch is 2.5 us), here 0.4 us.
+// The per-call steps of the Python binding that touch every tensor, as a
+// CPython module: reading what a descriptor depends on, allocating outputs and
+// workspace, and handing the data pointers to an entry point of libssm.
+// Reading and handing over take 3 us of a decode step's call in Python (ten
+// tensors; a kernel launch is 2.5 us) and 0.4 us here.
 #include <Python.h>
 
-#include <ATen/core/Tensor.h>
+#include <ATen/ATen.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
@@ -65,20 +67,78 @@ PyObject* signature(PyObject*, PyObject* arg) {
   });
 }
 
-// launch(entry, descriptor, tensors, workspace, bytes, stream): the entry
-// point's status.  All but the tensors are addresses or sizes; bytes < 0: an
-// entry point without a workspace.
+// The type of a dtype or, for None, of `t`; a Python error and false otherwise.
+bool type_of(PyObject* o, const at::Tensor& t, at::ScalarType* type) {
+  if (o == Py_None) {
+    *type = t.scalar_type();
+  } else if (THPDtype_Check(o)) {
+    *type = reinterpret_cast<THPDtype*>(o)->scalar_type;
+  } else {
+    PyErr_SetString(PyExc_TypeError, "expected a dtype or None");
+    return false;
+  }
+  return true;
+}
+
+// like(tensor, dtype): memory of the tensor's shape and, if it is dense, strides.
+PyObject* like(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  const at::Tensor* t;
+  if (nargs != 2) {
+    PyErr_SetString(PyExc_TypeError, "like(tensor, dtype)");
+    return nullptr;
+  }
+  if (!tensor_of(args[0], &t)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    at::ScalarType type;
+    if (!t) {
+      PyErr_SetString(PyExc_TypeError, "expected a tensor");
+      return nullptr;
+    }
+    if (!type_of(args[1], *t, &type)) return nullptr;
+    at::AutoDispatchBelowADInplaceOrView plain;
+    return THPVariable_Wrap(at::empty_like(*t, t->options().dtype(type)));
+  });
+}
+
+// empty(tensor, shape, dtype): contiguous memory on the tensor's device.
+PyObject* empty(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  const at::Tensor* t;
+  if (nargs != 3 || !PyTuple_Check(args[1])) {
+    PyErr_SetString(PyExc_TypeError, "empty(tensor, shape, dtype)");
+    return nullptr;
+  }
+  if (!tensor_of(args[0], &t)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    at::ScalarType type;
+    if (!t) {
+      PyErr_SetString(PyExc_TypeError, "expected a tensor");
+      return nullptr;
+    }
+    if (!type_of(args[2], *t, &type)) return nullptr;
+    at::DimVector shape;
+    for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(args[1]); ++i) {
+      shape.push_back(PyLong_AsLongLong(PyTuple_GET_ITEM(args[1], i)));
+      if (PyErr_Occurred()) return nullptr;
+    }
+    at::AutoDispatchBelowADInplaceOrView plain;
+    return THPVariable_Wrap(at::empty(shape, t->options().dtype(type)));
+  });
+}
+
+// launch(entry, descriptor, tensors, bytes, stream): the entry point's status.
+// Entry, descriptor and stream are addresses.  bytes: size of the workspace,
+// which is allocated on the first tensor's device for the current stream; < 0:
+// an entry point without one.
 PyObject* launch(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
-  if (nargs != 6 || !PyTuple_Check(args[2])) {
-    PyErr_SetString(PyExc_TypeError, "launch(entry, descriptor, tensors, workspace, bytes, stream)");
+  if (nargs != 5 || !PyTuple_Check(args[2])) {
+    PyErr_SetString(PyExc_TypeError, "launch(entry, descriptor, tensors, bytes, stream)");
     return nullptr;
   }
   return guarded([&]() -> PyObject* {
     void* const entry = PyLong_AsVoidPtr(args[0]);
     void* const desc = PyLong_AsVoidPtr(args[1]);
-    void* const ws = PyLong_AsVoidPtr(args[3]);
-    const long long bytes = PyLong_AsLongLong(args[4]);
-    void* const stream = PyLong_AsVoidPtr(args[5]);
+    const long long bytes = PyLong_AsLongLong(args[3]);
+    void* const stream = PyLong_AsVoidPtr(args[4]);
     if (PyErr_Occurred()) return nullptr;
     const Py_ssize_t n = PyTuple_GET_SIZE(args[2]);
     if (!entry || n > kMaxTensors) {
@@ -86,17 +146,29 @@ PyObject* launch(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
       return nullptr;
     }
     void* ptrs[kMaxTensors];
+    const at::Tensor* first = nullptr;
     for (Py_ssize_t i = 0; i < n; ++i) {
       const at::Tensor* t;
       if (!tensor_of(PyTuple_GET_ITEM(args[2], i), &t)) return nullptr;
       ptrs[i] = t ? t->mutable_data_ptr() : nullptr;
+      if (!first) first = t;
+    }
+    at::Tensor ws;
+    if (bytes > 0) {
+      if (!first) {
+        PyErr_SetString(PyExc_ValueError, "no tensor");
+        return nullptr;
+      }
+      at::AutoDispatchBelowADInplaceOrView plain;
+      ws = at::empty({(int64_t)bytes}, first->options().dtype(at::kByte));
     }
     int status;
     Py_BEGIN_ALLOW_THREADS
     if (bytes < 0)
       status = ((int (*)(const void*, const void*, void*))entry)(desc, ptrs, stream);
     else
-      status = ((int (*)(const void*, const void*, void*, size_t, void*))entry)(desc, ptrs, ws, (size_t)bytes, stream);
+      status = ((int (*)(const void*, const void*, void*, size_t, void*))entry)(
+          desc, ptrs, bytes ? ws.mutable_data_ptr() : nullptr, (size_t)bytes, stream);
     Py_END_ALLOW_THREADS
     return PyLong_FromLong(status);
   });
@@ -104,6 +176,8 @@ PyObject* launch(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
 
 PyMethodDef methods[] = {
     {"signature", signature, METH_O, "Type, device, sizes and strides of a tuple of tensors, as bytes."},
+    {"like", (PyCFunction)(void (*)(void))like, METH_FASTCALL, "Memory like a tensor's, of a dtype or (None) its own."},
+    {"empty", (PyCFunction)(void (*)(void))empty, METH_FASTCALL, "Contiguous memory on a tensor's device."},
     {"launch", (PyCFunction)(void (*)(void))launch, METH_FASTCALL, "Call an entry point on a tuple of tensors."},
     {nullptr, nullptr, 0, nullptr}};
 

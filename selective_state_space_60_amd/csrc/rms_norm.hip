@@ -6,12 +6,12 @@
 //
 // Bound by HBM: a row is read once, kept in registers across the reduction
 // and written once (16384 x 2560, bf16 in, fp32 residual in and out, bf16 out:
-// 95 us, 5.3 TB/s; a large copy runs at 4.7).  A workgroup of four waves owns a
-// row, or a wave each of four narrow rows (no barrier).  A lane holds groups of
-// 8 consecutive columns: 16-byte loads of bf16, and an e4m3 group of 32, 64 or
-// 128 columns is 4, 8 or 16 neighbouring lanes, whose largest value is found
-// with DPP.  A few hundred rows take one pass of latencies (333 x 5120 to e4m3:
-// 7.5 us, of which a launch is 2.5).
+// 95 us, 5.3 TB/s; a large copy runs at 4.7).  A workgroup of four or eight waves
+// owns a row, or a wave each of four narrow rows (no barrier).  A lane holds
+// groups of 8 consecutive columns: 16-byte loads of bf16, and an e4m3 group of
+// 32, 64 or 128 columns is 4, 8 or 16 neighbouring lanes, whose largest value is
+// found with DPP.  Few rows take one pass of latencies (1 x 2560 2.8 us, 333 x 5120 to
+// e4m3 6.8, of which a launch is 2.3).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -24,6 +24,7 @@ namespace {
 
 constexpr int NT = 256;
 constexpr int V = 8;  // consecutive columns per lane
+constexpr int kRowShift = 22;  // workgroups of a grid's x: fewer than 2^32 threads
 constexpr float kE4M3Max = 448.f;
 constexpr float kMinScale = 1.17549435e-38f;  // 2^-126: a group of zeros divides by a normal number
 
@@ -137,6 +138,13 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 
+// The total of a row's waves.
+template <int N>
+__device__ __forceinline__ float waves_sum(const float (&v)[N]) {
+  if constexpr (N == 8) return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+  else return (v[0] + v[1]) + (v[2] + v[3]);
+}
+
 // The largest over aligned groups of `lanes` (4, 8, 16 or 64), in every lane.
 __device__ __forceinline__ float group_max(float v, int lanes) {
   v = fmaxf(v, dpp<0xB1>(v));
@@ -150,16 +158,17 @@ __device__ __forceinline__ float group_max(float v, int lanes) {
   return v;
 }
 
-// TPR threads per row (64: a wave, or the workgroup's 256), CH groups of
+// TPR threads per row (64: a wave, or the workgroup's 256 or 512), CH groups of
 // 8 columns per thread: dim <= TPR * 8 * CH.
 template <int TPR, int CH>
-__global__ __launch_bounds__(NT) void norm_fwd_kernel(NormParams p, int64_t rows) {
+__global__ __launch_bounds__(TPR > NT ? TPR : NT) void norm_fwd_kernel(NormParams p, int64_t rows) {
   constexpr int WPR = TPR / 64;  // waves per row
+  constexpr int RPB = TPR > NT ? 1 : NT / TPR;
   const int D = (int)p.D;
-  __shared__ float lds[2][4];
+  __shared__ float lds[2][WPR];
   const int lane = threadIdx.x % TPR, wave = threadIdx.x / 64;
-  const int64_t r = (int64_t)blockIdx.x * (NT / TPR) + threadIdx.x / TPR;
-  if (r >= rows) return;  // whole waves; with TPR == NT the whole workgroup
+  const int64_t r = ((int64_t)blockIdx.y << kRowShift | blockIdx.x) * RPB + threadIdx.x / TPR;
+  if (r >= rows) return;  // whole waves; otherwise the whole workgroup
   int64_t b, t;
   split_row(r, p.batch, p.L, b, t);
   const int xe = p.x_type == kNormF32 ? 4 : 2, re = p.r_type == kNormF32 ? 4 : 2, oe = p.ro_type == kNormF32 ? 4 : 2;
@@ -206,7 +215,7 @@ __global__ __launch_bounds__(NT) void norm_fwd_kernel(NormParams p, int64_t rows
   if constexpr (WPR > 1) {
     if (threadIdx.x % 64 == 0) lds[0][wave] = ss;
     __syncthreads();
-    ss = (lds[0][0] + lds[0][1]) + (lds[0][2] + lds[0][3]);
+    ss = waves_sum<WPR>(lds[0]);
   }
   const float rstd = inv_root(ss / (float)D + p.eps);
   float amax = 0.f;
@@ -234,7 +243,9 @@ __global__ __launch_bounds__(NT) void norm_fwd_kernel(NormParams p, int64_t rows
     if constexpr (WPR > 1) {
       if (threadIdx.x % 64 == 0) lds[1][wave] = amax;
       __syncthreads();
-      amax = fmaxf(fmaxf(lds[1][0], lds[1][1]), fmaxf(lds[1][2], lds[1][3]));
+      amax = lds[1][0];
+#pragma unroll
+      for (int i = 1; i < WPR; ++i) amax = fmaxf(amax, lds[1][i]);
     }
   }
   const int shift = p.group == 32 ? 5 : p.group == 64 ? 6 : 7;  // of a group
@@ -254,7 +265,8 @@ __global__ __launch_bounds__(NT) void norm_fwd_kernel(NormParams p, int64_t rows
 #pragma unroll
     for (int i = 0; i < V; ++i) f[k][i] *= inv;
     store8_e4m3(y, col, D - col, f[k]);
-    if (p.group ? col < D && (col & ((1 << shift) - 1)) == 0 : col == 0) p.scale[r * ng + (p.group ? col >> shift : 0)] = scale;
+    if (p.group ? col < D && (col & ((1 << shift) - 1)) == 0 : col == 0)
+      p.scale[r * ng + (p.group ? col >> shift : 0)] = scale;
   }
 }
 
@@ -262,10 +274,10 @@ __global__ __launch_bounds__(NT) void norm_fwd_kernel(NormParams p, int64_t rows
 // Workgroups walk the rows with a stride and keep dweight's sums of their rows
 // in registers; the four waves' sums are added in order through LDS.
 template <int TPR, int CH>
-__global__ __launch_bounds__(NT) void norm_bwd_kernel(NormBwdParams p, int64_t rows) {
-  constexpr int RPB = NT / TPR;
+__global__ __launch_bounds__(TPR > NT ? TPR : NT) void norm_bwd_kernel(NormBwdParams p, int64_t rows) {
+  constexpr int RPB = TPR > NT ? 1 : NT / TPR, WPR = TPR / 64;
   const int D = (int)p.D;
-  __shared__ float lds[2][2][4];
+  __shared__ float lds[2][2][WPR];
   const int lane = threadIdx.x % TPR, wave = threadIdx.x / 64, sub = threadIdx.x / TPR;
   const int de = p.dy_type == kNormF32 ? 4 : 2, re = p.row_type == kNormF32 ? 4 : 2;
   const int se = p.dres_type == kNormF32 ? 4 : 2, xe = p.dx_type == kNormF32 ? 4 : 2;
@@ -275,7 +287,7 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormBwdParams p, int64_t r
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[k][i] = 0.f;
   int buf = 0;
-  // with TPR == NT every thread of the workgroup runs the same number of rounds
+  // with a workgroup a row every thread runs the same number of rounds
   for (int64_t r = (int64_t)blockIdx.x * RPB + sub; r < rows; r += (int64_t)gridDim.x * RPB, buf ^= 1) {
     int64_t b, t;
     split_row(r, p.batch, p.L, b, t);
@@ -330,8 +342,8 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormBwdParams p, int64_t r
         lds[buf][1][wave] = s1;
       }
       __syncthreads();
-      ss = (lds[buf][0][0] + lds[buf][0][1]) + (lds[buf][0][2] + lds[buf][0][3]);
-      s1 = (lds[buf][1][0] + lds[buf][1][1]) + (lds[buf][1][2] + lds[buf][1][3]);
+      ss = waves_sum<WPR>(lds[buf][0]);
+      s1 = waves_sum<WPR>(lds[buf][1]);
     }
     const float rstd = inv_root(ss / (float)D + p.eps);
     const float coef = s1 * rstd / (float)D * rstd;  // mean(weight dy hat) rstd
@@ -376,62 +388,90 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormBwdParams p, int64_t r
   }
 }
 
-// A wave per row for narrow rows, once they are enough to fill the card; a
-// workgroup per row otherwise.  Measured with the residual's addition, a wave
-// against a workgroup per row: 16384 x 768 33 us against 42, 2048 x 256 3.7
-// against 5.1; but 16384 x 2560 104 against 95, 1024 x 768 4.5 against 4.3,
-// 256 x 2560 5.4 against 3.9.  Backward 4096 x 4096: 87 against 39.
+// Threads of a row.  A wave for narrow rows, once they are enough to fill the
+// card; otherwise a workgroup of 256 or, for wide rows, 512.  Measured with the
+// residual's addition, a wave against 256: 16384 x 768 33 us against 42, 2048 x
+// 256 3.7 against 5.1; but 1024 x 768 4.5 against 4.3, 256 x 2560 5.4 against
+// 3.9.  512 against 256: 1 x 2560 2.8 us against 3.3, 1024 x 4096 13.7 against
+// 14.0, 4096 x 4096 38.4 against 40.9, 8192 x 8192 to e4m3 46.5 against 52.5; but
+// 8192 x 4096 without a residual 23.9 against 21.9.
 bool wave_rows(int64_t rows, int64_t dim) { return dim <= 1024 && rows >= 2048; }
+
+int fwd_threads(int64_t rows, int64_t dim, bool residual) {
+  if (wave_rows(rows, dim)) return 64;
+  return dim > 4096 || (dim > 2048 && (rows <= 1024 || residual)) ? 512 : 256;
+}
+
+// Backward: 512 against 256: 333 x 5120 13.4 us against 15.4, 8192 x 8192 106
+// against 122 (256 threads would hold four column groups each, at three waves a
+// SIMD); but 16384 x 2560 118 against 107.
+int bwd_threads(int64_t rows, int64_t dim) {
+  if (wave_rows(rows, dim)) return 64;
+  return dim > 3 * NT * V || (dim > 2048 && rows <= 1024) ? 512 : 256;
+}
 
 template <int TPR, int CH>
 void launch_fwd(const NormParams& p, int64_t rows, hipStream_t stream) {
-  constexpr int RPB = NT / TPR;
-  hipLaunchKernelGGL((norm_fwd_kernel<TPR, CH>), dim3((unsigned)((rows + RPB - 1) / RPB)), dim3(NT), 0, stream, p,
-                     rows);
+  constexpr int RPB = TPR > NT ? 1 : NT / TPR;
+  const int64_t blocks = (rows + RPB - 1) / RPB, x = std::min<int64_t>(blocks, 1 << kRowShift);
+  hipLaunchKernelGGL((norm_fwd_kernel<TPR, CH>), dim3((unsigned)x, (unsigned)((blocks + x - 1) / x)), dim3(RPB * TPR),
+                     0, stream, p, rows);
 }
 
 template <int TPR, int CH>
 void launch_bwd(const NormBwdParams& p, int64_t rows, hipStream_t stream) {
-  hipLaunchKernelGGL((norm_bwd_kernel<TPR, CH>), dim3((unsigned)p.parts), dim3(NT), 0, stream, p, rows);
+  hipLaunchKernelGGL((norm_bwd_kernel<TPR, CH>), dim3((unsigned)p.parts), dim3(TPR > NT ? TPR : NT), 0, stream, p,
+                     rows);
 }
 
 }  // namespace
 
 // As many workgroups as are resident at once: with more, a second, short round
-// follows (16384 x 5120: 167 us at 1024 workgroups, 228 us at 1280).  A thread
-// of up to 3 column groups leaves room for four workgroups a compute unit, of 4
-// for three, beyond that for one.  Two rows each at least, as each workgroup's
-// sums are written and read once (1001 x 1777: 14.0 us, with one row each 15.8).
+// follows (16384 x 5120: 167 us at 1024 workgroups, 228 us at 1280).  A compute
+// unit holds four workgroups of 256 threads or of 512 with one column group each,
+// two of 512 with more.  Two rows each at least, as each workgroup's sums are
+// written and read once (1001 x 1777: 14.0 us, with one row each 15.8).
 int norm_bwd_parts(int64_t rows, int64_t dim) {
-  const bool wave = wave_rows(rows, dim);
-  const int64_t blocks = wave ? (rows + 3) / 4 : rows;
-  const int64_t ch = wave ? 1 : (dim + NT * V - 1) / (NT * V);
-  const int64_t cap = 256 * (ch <= 3 ? 4 : ch <= 4 ? 3 : 1);
+  const int threads = bwd_threads(rows, dim);
+  const int64_t blocks = threads == 64 ? (rows + 3) / 4 : rows;
+  const int64_t cap = 256 * (threads == 512 && dim > 512 * V ? 2 : 4);
   return (int)std::min({blocks, cap, std::max<int64_t>(256, (blocks + 1) / 2)});
 }
 
-#define SSM_NORM_DISPATCH(LAUNCH, P)                      \
-  if (wave_rows(rows, (P).D)) {                           \
-    if ((P).D <= 64 * V) LAUNCH<64, 1>(P, rows, stream);  \
-    else LAUNCH<64, 2>(P, rows, stream);                  \
-  } else {                                                \
-    const int64_t ch = ((P).D + NT * V - 1) / (NT * V);   \
-    if (ch <= 1) LAUNCH<NT, 1>(P, rows, stream);          \
-    else if (ch <= 2) LAUNCH<NT, 2>(P, rows, stream);     \
-    else if (ch <= 3) LAUNCH<NT, 3>(P, rows, stream);     \
-    else if (ch <= 4) LAUNCH<NT, 4>(P, rows, stream);     \
-    else LAUNCH<NT, 8>(P, rows, stream);                  \
-  }
-
 hipError_t launch_rms_norm(const NormParams& p, hipStream_t stream) {
   const int64_t rows = p.batch * p.L;
-  SSM_NORM_DISPATCH(launch_fwd, p)
+  const int threads = fwd_threads(rows, p.D, p.residual != nullptr);
+  const int64_t ch = (p.D + threads * V - 1) / (threads * V);
+  if (threads == 64) {
+    if (ch <= 1) launch_fwd<64, 1>(p, rows, stream);
+    else launch_fwd<64, 2>(p, rows, stream);
+  } else if (threads == 256) {
+    if (ch <= 1) launch_fwd<256, 1>(p, rows, stream);
+    else launch_fwd<256, 2>(p, rows, stream);
+  } else {
+    if (ch <= 1) launch_fwd<512, 1>(p, rows, stream);
+    else if (ch <= 2) launch_fwd<512, 2>(p, rows, stream);
+    else launch_fwd<512, 4>(p, rows, stream);
+  }
   return hipGetLastError();
 }
 
 hipError_t launch_rms_norm_bwd(const NormBwdParams& p, hipStream_t stream) {
   const int64_t rows = p.batch * p.L;
-  SSM_NORM_DISPATCH(launch_bwd, p)
+  const int threads = bwd_threads(rows, p.D);
+  const int64_t ch = (p.D + threads * V - 1) / (threads * V);
+  if (threads == 64) {
+    if (ch <= 1) launch_bwd<64, 1>(p, rows, stream);
+    else launch_bwd<64, 2>(p, rows, stream);
+  } else if (threads == 256) {
+    if (ch <= 1) launch_bwd<256, 1>(p, rows, stream);
+    else if (ch <= 2) launch_bwd<256, 2>(p, rows, stream);
+    else launch_bwd<256, 3>(p, rows, stream);
+  } else {
+    if (ch <= 1) launch_bwd<512, 1>(p, rows, stream);
+    else if (ch <= 2) launch_bwd<512, 2>(p, rows, stream);
+    else launch_bwd<512, 4>(p, rows, stream);
+  }
   launch_column_sums(p.part, p.parts, p.D, p.D, p.dweight, nullptr, nullptr, stream);
   return hipGetLastError();
 }

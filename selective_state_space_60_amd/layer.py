@@ -38,14 +38,14 @@ MARSHAL_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_marsha
 
 
 def _bind():
-    """Put the native module's functions (csrc/marshal.cpp) in the place of the two below."""
-    global _sig, _run
+    """Put the native module's functions (csrc/marshal.cpp) in the place of the four below."""
+    global _sig, _run, _new_like, _new
     if not os.path.exists(MARSHAL_PATH):
         raise ImportError("_marshal.so is not built (run __graft_entry__.build()): " + MARSHAL_PATH)
     spec = importlib.util.spec_from_file_location(__package__ + "._marshal", MARSHAL_PATH)
     native = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(native)
-    _sig, _run = native.signature, native.launch
+    _sig, _run, _new_like, _new = native.signature, native.launch, native.like, native.empty
 
 
 def _sig(tensors):
@@ -55,9 +55,21 @@ def _sig(tensors):
 
 
 def _run(*args):
-    """The status of an entry point called on a tuple of tensors."""
+    """The status of an entry point called on a tuple of tensors, with a workspace of its own."""
     _bind()
     return _run(*args)
+
+
+def _new_like(t, dtype):
+    """Memory like t's, of a dtype or (None) its own."""
+    _bind()
+    return _new_like(t, dtype)
+
+
+def _new(t, shape, dtype):
+    """Contiguous memory on t's device."""
+    _bind()
+    return _new(t, shape, dtype)
 
 
 class _Plan:
@@ -99,31 +111,31 @@ def _launch(plan, tensors, stream):
     if plan.index != _current_device():
         with torch.cuda.device(plan.index):
             return _launch(plan, tensors, stream)
-    handle = _raw_stream(plan.index) if stream is None else stream.cuda_stream
-    ws = None
-    if plan.nbytes > 0:
-        ws = _empty(stream, (plan.nbytes,), torch.uint8, tensors[0].device)
-    status = _run(plan.fn, plan.address, tensors, 0 if ws is None else ws.data_ptr(), plan.nbytes, handle)
+    if stream is None:
+        status = _run(plan.fn, plan.address, tensors, plan.nbytes, _raw_stream(plan.index))
+    else:
+        with torch.cuda.stream(stream):  # the workspace belongs to its pool
+            status = _run(plan.fn, plan.address, tensors, plan.nbytes, stream.cuda_stream)
     if status:
         _check(status, plan.entry)
 
 
-def _empty(stream, shape, dtype, device):
-    """Memory for a call on `stream`: it belongs to that stream's pool, so that
-    freeing it early is safe there."""
+def _empty(stream, t, shape, dtype):
+    """Memory on t's device for a call on `stream`: it belongs to that stream's
+    pool, so that freeing it early is safe there."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _new(t, shape, dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _new(t, shape, dtype)
 
 
 def _like(stream, t, dtype=None):
     """Memory of t's shape, dense (contiguous unless t is a dense permutation).
     Its strides follow from t's alone: a plan's key does not hold them."""
     if stream is None:
-        return torch.empty_like(t) if dtype is None else torch.empty_like(t, dtype=dtype)
+        return _new_like(t, dtype)
     with torch.cuda.stream(stream):
-        return torch.empty_like(t, dtype=dtype)
+        return _new_like(t, dtype)
 
 
 # -------------------------------------------------- gated linear recurrence
@@ -156,7 +168,7 @@ def gated_scan_fwd(x, gate_a, gate_x, A, bias_a=None, bias_x=None, z=None, h0=No
         y = _like(stream, x, y_dtype)
     h_last = None
     if want_hlast:
-        h_last = _empty(stream, (x.shape[0], x.shape[2]), torch.float32, x.device)
+        h_last = _empty(stream, x, (x.shape[0], x.shape[2]), torch.float32)
     tensors = (x, gate_a, gate_x, A, bias_a, bias_x, z, y, h0, h_last, lens, ckpt)
     if plan is None:
         batch, L, dim = x.shape
@@ -264,8 +276,8 @@ def rms_norm(x, weight, eps=1e-5, residual=None, residual_dtype=None, residual_o
         residual_out = _like(stream, x, residual_dtype or residual.dtype)
     scale = None
     if y.dtype == torch.float8_e4m3fn:
-        scale = _empty(stream, x.shape[:-1] + ((x.shape[-1] + group - 1) // group if group > 0 else 1,),
-                       torch.float32, x.device)
+        scale = _empty(stream, x, x.shape[:-1] + ((x.shape[-1] + group - 1) // group if group > 0 else 1,),
+                       torch.float32)
     tensors = (x, residual, weight, y, residual_out, scale)
     if plan is None:
         x3 = _rows(x)
@@ -333,7 +345,7 @@ def w4_matvec(x, weight, scale, zero=None, bias=None, y_dtype=None, y=None, stre
     key = ("w4_matvec", y_dtype, _sig((x, weight, scale, zero, bias, y)))
     plan = _plans.get(key)
     if y is None:
-        y = _empty(stream, (x.shape[0], weight.shape[0]), y_dtype or x.dtype, x.device)
+        y = _empty(stream, x, (x.shape[0], weight.shape[0]), y_dtype)
     tensors = (x, weight, scale, zero, bias, y)
     if plan is None:
         rows, ins = x.shape

@@ -382,6 +382,14 @@ def test_signatures():
     with pytest.raises(TypeError):
         layer._sig([a])
     with pytest.raises((TypeError, ValueError)):
-        layer._run(0, 0, (a,), 0, -1, 0)
+        layer._run(0, 0, (a,), -1, 0)
     with pytest.raises(TypeError):
         layer._run(1, 2, 3)
+    for call in (lambda: layer._new_like(None, None), lambda: layer._new_like(a, 3), lambda: layer._new(a, [2], None),
+                 lambda: layer._new(a, ("2",), None)):
+        with pytest.raises(TypeError):
+            call()
+    flip = torch.zeros(3, 4).t()
+    assert layer._new_like(flip, torch.bfloat16).stride() == flip.stride()
+    e = layer._new(a.requires_grad_(), (2, 5), None)
+    assert e.shape == (2, 5) and e.dtype == a.dtype and not e.requires_grad

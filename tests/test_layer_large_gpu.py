@@ -55,6 +55,17 @@ def test_long_norm():
     assert torch.equal(g, ssm.rms_norm_bwd(y2, res2, w, dres=x[-3:])["dx"])
 
 
+def test_many_rows_of_a_norm():
+    """2^22 + 3 rows of a workgroup each: more than a grid's first dimension holds."""
+    banner("2^22 + 3 rows")
+    R, D = (1 << 22) + 3, 1032
+    x = torch.empty(R, D, dtype=torch.bfloat16, device="cuda").normal_()
+    w = torch.rand(D, device="cuda")
+    y = ssm.rms_norm(x, w)[0]
+    for cut in (slice(0, 5), slice(R - 7, R)):
+        assert torch.equal(y[cut], ssm.rms_norm(x[cut], w)[0])
+
+
 def test_large_weights():
     """2^20 + 5 outputs of 5120: 2.7e9 bytes of weights."""
     banner("large 4-bit matrix")

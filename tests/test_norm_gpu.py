@@ -60,6 +60,14 @@ def test_forward_backward(size, dt, res):
     ref.check(got["dweight"], dw, mw, rel(dim) + (rows / 64 + 128) * ref.U32, "dweight")
 
 
+@pytest.mark.parametrize("dt,res", [(BF16, None), (BF16, F32), (F32, None)], ids=lambda v: str(v).replace("torch.", ""))
+@pytest.mark.parametrize("size", [(1025, 2049), (1025, 4096), (1025, 4097), (1030, 6144), (1030, 6145), (1100, 8192),
+                                  (1025, 8193), (5, 2049), (1, 4096)], ids=lambda s: "%dx%d" % s)
+def test_workgroup_sizes(size, dt, res):
+    """Both sides of the split between workgroups of 256 and 512 threads a row."""
+    test_forward_backward(size, dt, res)
+
+
 @pytest.mark.parametrize("group", [0, 32, 64, 128])
 @pytest.mark.parametrize("size", [(3, 5), (2, 32), (4, 100), (3, 128), (2, 1000), (3, 2049), (2, 5120), (1, 16384),
                                   (1100, 72), (1030, 1537), (2050, 72), (2049, 1000)], ids=lambda s: "%dx%d" % s)
@@ -156,3 +164,9 @@ def test_gradients_against_differences():
                              ("dweight", dw, loss(row.double(), w.double() + e * dw), loss(row.double(), w.double() - e * dw))):
         terms = got[key].double().cpu() * vec
         assert abs((hi - lo) / (2 * e) - float(terms.sum())) <= 1e-5 * float(terms.abs().sum()), key
+
+
+@pytest.mark.parametrize("group", [0, 128])
+def test_e4m3_workgroup_sizes(group):
+    for size in ((1025, 2049), (1030, 6145), (3, 8200)):
+        test_e4m3(size, group)
