@@ -108,6 +108,8 @@ def _keep(key, plan):
 
 def _launch(plan, tensors, stream):
     """Run the plan on these tensors, on `stream` (default: the current stream of their device)."""
+    if stream is not None and stream.device.index != plan.index:
+        raise ValueError("%s: the stream is on another device than the tensors" % plan.entry)
     if plan.index != _current_device():
         with torch.cuda.device(plan.index):
             return _launch(plan, tensors, stream)

@@ -347,6 +347,13 @@ def test_wrappers_refuse_host_tensors():
             call()
 
 
+def test_a_stream_of_another_device_is_refused():
+    from types import SimpleNamespace
+    from selective_state_space_60_amd import layer
+    with pytest.raises(ValueError, match="another device"):
+        layer._launch(SimpleNamespace(index=0, entry="e"), (), SimpleNamespace(device=torch.device("cuda", 1)))
+
+
 def test_backward_refuses_unknown_outputs():
     x, v = torch.zeros(2, 4, 8), torch.zeros(8)
     with pytest.raises(ValueError, match="dgate_a"):
