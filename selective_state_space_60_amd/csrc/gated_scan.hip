@@ -59,8 +59,9 @@ constexpr int kFwdNT = LC * kGatedFwdChunks, kFwdSeg = kGatedFwdChunks * kFwdT;
 constexpr int kBwdNT = LC * kGatedBwdChunks, kBwdSeg = kGatedBwdChunks * kBwdT;
 // Waves per SIMD that the registers are cut to: 128 and 168 hold a chunk of
 // two channels without a spill (4 x 4096 x 5120 forward at 3 waves: 247 us
-// against 197).
-constexpr int kFwdWaves = 4, kBwdWaves = 3;
+// against 197); four streams of fp32 do not fit 128 (8 x 2048 x 1536 with z at 4
+// waves: 114 us, at 3: 109).
+constexpr int kFwdWaves = 4, kFwdWaves32 = 3, kBwdWaves = 3;
 static_assert(kGatedCkptSteps % kFwdT == 0 && kFwdSeg % kGatedCkptSteps == 0, "checkpoints fall on chunks");
 static_assert(kBwdSeg % kGatedCkptSteps == 0, "every backward segment starts at a checkpoint");
 static_assert(kFwdSeg <= kGatedSpanSteps && kBwdSeg <= kGatedSpanSteps, "a segment's rows fit the offsets");
@@ -334,6 +335,15 @@ struct Place {
   }
 };
 
+// The kernel's first argument read anew: what only a rare or a late part needs
+// is loaded there, not held in (or spilled from) scalar registers until then.
+template <class P>
+__device__ __forceinline__ const P& args_anew() {
+  auto at = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(at));
+  return *(const P*)(const __attribute__((address_space(4))) P*)at;
+}
+
 // ------------------------------------------------------------------- forward
 template <bool BF16, bool YF32, bool Z, int V, bool Y>
 struct Fwd : Place<V> {
@@ -492,7 +502,8 @@ struct Fwd : Place<V> {
 };
 
 template <bool BF16, bool YF32, bool Z, int V, bool Y>
-__global__ __launch_bounds__(kFwdNT, kFwdWaves) void gated_fwd_kernel(GatedParams p, Chain q, unsigned tiles, int64_t nseg) {
+__global__ __launch_bounds__(kFwdNT, !BF16 && Z && V == 2 ? kFwdWaves32 : kFwdWaves) void gated_fwd_kernel(
+    GatedParams p, Chain q, unsigned tiles, int64_t nseg) {
   typedef Fwd<BF16, YF32, Z, V, Y> F;
   __shared__ typename F::Shared sh;
   F f(p);
@@ -506,18 +517,21 @@ __global__ __launch_bounds__(kFwdNT, kFwdWaves) void gated_fwd_kernel(GatedParam
       return;
   }
   // Not found in time: the segments before this one, from the start.
-  float h = h0;
-  for (int64_t k = 0; k < f.k; ++k) {
+  F late(args_anew<GatedParams>());
+  late.set(late.p, tiles, nseg);
+  late.ch.load(late.p, late.c, late.ok);
+  float h = late.p.h0 && l < F::CW && late.c0 + l < late.p.D ? late.p.h0[late.b * late.p.D + late.c0 + l] : 0.f;
+  for (int64_t k = 0; k < late.k; ++k) {
     __syncthreads();  // the last fold has read the pairs
-    f.template scan_chunk<true, false>(k * kFwdSeg, sh);
+    late.template scan_chunk<true, false>(k * kFwdSeg, sh);
     __syncthreads();
     if (l < 64) {
-      const float2 w = f.fold(sh, l < F::CW ? l : 0);
+      const float2 w = late.fold(sh, l < F::CW ? l : 0);
       h = __builtin_fmaf(w.x, h, w.y);
     }
   }
   __syncthreads();
-  f.template segment<true>(q, sh, true, h);
+  late.template segment<true>(q, sh, true, h);
 }
 
 // ------------------------------------------------------------------ backward
@@ -690,6 +704,12 @@ struct Bwd : Place<V> {
 #pragma unroll
       for (uint32_t& x : xr[j].w) asm volatile("" : "+v"(x));
     }
+    // bf16 with z: four outputs' addresses on top of the inputs' spill (8 x 2048 x
+    // 1536 127 us, read anew 124; but fp32 203 against 237, bf16 without z 106
+    // against 109)
+    constexpr bool kAnew = BF16 && Z;
+    const GatedBwdParams& q = kAnew ? args_anew<GatedBwdParams>() : this->q;
+    const GatedParams& p = q.f;
     float h[V], mi[V], A[V], sA[V], sba[V], sbx[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -773,7 +793,8 @@ struct Bwd : Place<V> {
 };
 
 template <bool BF16, bool GF32, bool Z, int V>
-__global__ __launch_bounds__(kBwdNT, kBwdWaves) void gated_bwd_kernel(GatedBwdParams q, Chain cn, unsigned tiles, int64_t nseg) {
+__global__ __launch_bounds__(kBwdNT, kBwdWaves) void gated_bwd_kernel(GatedBwdParams q, Chain cn, unsigned tiles,
+                                                                        int64_t nseg) {
   typedef Bwd<BF16, GF32, Z, V> F;
   __shared__ typename F::Shared sh;
   const GatedParams& p = q.f;
@@ -789,18 +810,23 @@ __global__ __launch_bounds__(kBwdNT, kBwdWaves) void gated_bwd_kernel(GatedBwdPa
       return;
   }
   // Not found in time: the segments behind this one, from the end.
-  float m = m0;
-  for (int64_t s = nseg - 1; s > seg; --s) {
+  F late(args_anew<GatedBwdParams>());
+  late.set(late.p, tiles, nseg);
+  late.ch.load(late.p, late.c, late.ok);
+  float m = late.q.dh_last && l < F::CW && late.c0 + l < late.p.D ? late.q.dh_last[late.b * late.p.D + late.c0 + l]
+                                                                  : 0.f;
+  const int64_t last = nseg - 1 - late.k;
+  for (int64_t s = nseg - 1; s > last; --s) {
     __syncthreads();
-    f.template scan_chunk<true, false>(s * kBwdSeg, sh);
+    late.template scan_chunk<true, false>(s * kBwdSeg, sh);
     __syncthreads();
     if (l < 64) {
-      const float2 w = f.fold(sh, l < F::CW ? l : 0);
+      const float2 w = late.fold(sh, l < F::CW ? l : 0);
       m = __builtin_fmaf(w.x, m, w.y);
     }
   }
   __syncthreads();
-  f.template segment<true>(cn, sh, seg, true, m);
+  late.template segment<true>(cn, sh, last, true, m);
 }
 
 // ---------------------------------------------------------------- one token
@@ -940,8 +966,19 @@ bool gated_pairs(const GatedParams& p) {
 
 }  // namespace
 
+// Two channels a lane, unless so few workgroups come of it that latency is all:
+// with one, a wave has half the work.  bf16 forward, one against two channels:
+// 1 x 16 x 2560 (40 workgroups of two) 6.0 us against 7.5, 1 x 300 x 2560 (120)
+// 10.0 against 10.6, 1 x 2048 x 640 (160) 13.4 against 12.9; fp32 with z 1 x 2048
+// x 1536 (384) 17.9 against 19.5, 2 x 2048 x 1536 (768) 32.5 against 30.0;
+// backward in step.
+bool wide_tiles(const GatedParams& p, int64_t segment) {
+  const int64_t workgroups = (p.D + 2 * LC - 1) / (2 * LC) * p.batch * ((p.L + segment - 1) / segment);
+  return workgroups > (p.io_bf16 ? 128 : 384);
+}
+
 hipError_t launch_gated_scan(const GatedParams& p, hipStream_t stream) {
-  if (gated_pairs(p)) launch_fwd_io<2>(p, stream);
+  if (gated_pairs(p) && wide_tiles(p, kFwdSeg)) launch_fwd_io<2>(p, stream);
   else launch_fwd_io<1>(p, stream);
   return hipGetLastError();
 }
@@ -951,7 +988,7 @@ hipError_t launch_gated_scan_bwd(const GatedBwdParams& q, hipStream_t stream) {
   const bool pairs = gated_pairs(q.f) && pair_rows(q.dy, ge, q.dys_b, q.dys_t) &&
                      pair_rows(q.dx, ge, q.dxs_b, q.dxs_t) && pair_rows(q.dgate_a, ge, q.dgas_b, q.dgas_t) &&
                      pair_rows(q.dgate_x, ge, q.dgxs_b, q.dgxs_t) && pair_rows(q.dz, ge, q.dzs_b, q.dzs_t);
-  if (pairs) launch_bwd_io<2>(q, stream);
+  if (pairs && wide_tiles(q.f, kBwdSeg)) launch_bwd_io<2>(q, stream);
   else launch_bwd_io<1>(q, stream);
   return hipGetLastError();
 }

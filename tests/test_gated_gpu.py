@@ -166,6 +166,49 @@ def test_no_wait_gives_the_same_bits(io, size):
             assert torch.equal(out[k], v), k
 
 
+@pytest.mark.parametrize("io,size", [("bf16", (131, 150, 64)), ("bf16", (70, 257, 66)), ("bf16", (129, 1, 62)),
+                                     ("bf16", (2, 5000, 128)), ("f32", (200, 260, 64)), ("f32", (197, 129, 130)),
+                                     ("f32", (400, 1, 64)), ("f32", (3, 5000, 256))],
+                         ids=lambda v: v if isinstance(v, str) else "x".join(map(str, v)))
+@pytest.mark.parametrize("z", [True, False])
+def test_two_channels_a_lane(io, size, z):
+    """Enough workgroups for two channels a lane, with lengths, whose rows
+    behind the end hold infinities and NaN."""
+    banner("gated wide %s %s z %s" % (io, size, z))
+    b, L, D = size
+    lens = [(37 * i) % (L + 2) if i % 3 else L for i in range(b)]
+    t = make(b, L, D, io, z=z, h0=z, lens=lens, seed=sum(size))
+    for k, v in (("x", float("nan")), ("ga", float("inf")), ("gx", float("nan")), ("dy", float("-inf"))):
+        for i in range(0, b, max(1, b // 8)):
+            t[k][i, min(lens[i], L):] = v
+    c = up(t)
+    ckpt = ssm.gated_scan_ckpt(b, L, D)
+    y, h = forward(c, want_hlast=True, ckpt=ckpt)
+    check_all(t, c, y, h, backward(c, ckpt=ckpt), "from checkpoints")
+    check_all(t, c, y, h, backward(c), "recomputed")
+
+
+@pytest.mark.parametrize("io,size", [("bf16", (2, 2000, 322)), ("f32", (2, 2000, 834))])
+def test_no_wait_of_two_channels_a_lane(io, size):
+    test_no_wait_gives_the_same_bits(io, size)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_one_and_two_channels_a_lane_agree(io):
+    """A row's result does not depend on how many rows come with it."""
+    banner("gated one and two channels %s" % io)
+    b, L, D = 220, 260, 64
+    t = make(b, L, D, io, seed=12)
+    c = up(t)
+    y, h = forward(c, want_hlast=True)
+    g = backward(c)
+    few = {k: v[:3] if k not in ("A", "ba", "bx") and v is not None else v for k, v in c.items()}
+    y2, h2 = forward(few, want_hlast=True)
+    g2 = backward(few)
+    assert torch.equal(y[:3], y2) and torch.equal(h[:3], h2)
+    assert all(torch.equal(g[k][:3], g2[k]) for k in ("dx", "dgate_a", "dgate_x", "dz", "dh0"))
+
+
 def test_repeated_calls_give_the_same_bits():
     """The chain of segments does not make the result depend on timing."""
     c = up(make(1, 20000, 64, "f32", seed=33))
