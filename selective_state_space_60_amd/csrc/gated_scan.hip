@@ -36,7 +36,7 @@
 //
 // Measured: forward 4 x 4096 x 5120 bf16 with z 191 us (4.4 TB/s; VALU 55 %
 // busy; 243 us with 16 chunks a segment and fewer waves), 1 x 131072 x 1536 fp32
-// 622 us (5.2 TB/s); backward 8 x 2048 x 1536 bf16 with z 119.5 us (3.8 TB/s).
+// 622 us (5.2 TB/s); backward 8 x 2048 x 1536 bf16 with z 112 us (4.0 TB/s).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
