@@ -75,6 +75,24 @@ __device__ __forceinline__ void load8(const void* row, int type, int col, int n,
   }
 }
 
+// The same of bf16 as loaded, and brought to fp32.
+__device__ __forceinline__ u32x4_t load8_raw(const void* row, int col, int n) {
+  u32x4_t w = {0, 0, 0, 0};
+  if (n >= V) {
+    __builtin_memcpy(&w, (const uint16_t*)row + col, 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < n) w[i / 2] |= (uint32_t)((const uint16_t*)row)[col + i] << (16 * (i & 1));
+  }
+  return w;
+}
+
+__device__ __forceinline__ void widen8(u32x4_t w, float (&o)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) o[i] = __uint_as_float((i & 1) ? (w[i / 2] & 0xFFFF0000u) : (w[i / 2] << 16));
+}
+
 __device__ __forceinline__ void store8(void* row, int type, int col, int n, const float (&o)[V]) {
   if (type == kNormBF16) {
     if (n >= V) {
@@ -272,9 +290,18 @@ __global__ __launch_bounds__(TPR > NT ? TPR : NT) void norm_fwd_kernel(NormParam
 
 // ------------------------------------------------------------------ backward
 // Workgroups walk the rows with a stride and keep dweight's sums of their rows
-// in registers; the four waves' sums are added in order through LDS.
+// in registers; the four waves' sums are added in order through LDS.  AHEAD, for
+// bf16 rows and gradients: the next row's, 8 registers for 8 columns, are asked
+// for before this row's sums (16384 x 768 36.9 -> 32.0 us, 16384 x 2560 111 -> 85,
+// 4096 x 16384 145 -> 102).  Not where they would cost a wave a SIMD (256 threads
+// with three column groups: 173 us at 16384 x 5120 against 203; 512 with two: 106
+// at 8192 x 8192 either way).
 template <int TPR, int CH>
-__global__ __launch_bounds__(TPR > NT ? TPR : NT) void norm_bwd_kernel(NormBwdParams p, int64_t rows) {
+constexpr bool kAhead = !(TPR == 256 && CH == 3) && !(TPR == 512 && CH == 2);
+
+template <int TPR, int CH, bool AHEAD>
+__global__ __launch_bounds__(TPR > NT ? TPR : NT, AHEAD && TPR == 256 && CH == 2 ? 4 : 1) void norm_bwd_kernel(
+    NormBwdParams p, int64_t rows) {
   constexpr int RPB = TPR > NT ? 1 : NT / TPR, WPR = TPR / 64;
   const int D = (int)p.D;
   __shared__ float lds[2][2][WPR];
@@ -287,22 +314,46 @@ __global__ __launch_bounds__(TPR > NT ? TPR : NT) void norm_bwd_kernel(NormBwdPa
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[k][i] = 0.f;
   int buf = 0;
+  u32x4_t nf[AHEAD ? CH : 1], ng[AHEAD ? CH : 1];
+  auto load_next = [&](int64_t r) {
+    int64_t b, t;
+    split_row(r, p.batch, p.L, b, t);
+    const void* dy = (const char*)p.dy + (b * p.dys_b + t * p.dys_t) * 2;
+    const void* row = (const char*)p.row + (b * p.rs_b + t * p.rs_t) * 2;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int col = (k * TPR + lane) * V;
+      nf[k] = load8_raw(row, col, D - col);
+      ng[k] = load8_raw(dy, col, D - col);
+    }
+  };
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  int64_t r = (int64_t)blockIdx.x * RPB + sub;
+  if (AHEAD && r < rows) load_next(r);
   // with a workgroup a row every thread runs the same number of rounds
-  for (int64_t r = (int64_t)blockIdx.x * RPB + sub; r < rows; r += (int64_t)gridDim.x * RPB, buf ^= 1) {
+  for (; r < rows; r += step, buf ^= 1) {
     int64_t b, t;
     split_row(r, p.batch, p.L, b, t);
     const void* dy = (const char*)p.dy + (b * p.dys_b + t * p.dys_t) * de;
     const void* row = (const char*)p.row + (b * p.rs_b + t * p.rs_t) * re;
     float f[CH][V], g[CH][V];
+    if constexpr (AHEAD) {
 #pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      const int col = (k * TPR + lane) * V;
-      load8(row, p.row_type, col, D - col, f[k]);
-    }
+      for (int k = 0; k < CH; ++k) {
+        widen8(nf[k], f[k]);
+        widen8(ng[k], g[k]);
+      }
+    } else {
 #pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      const int col = (k * TPR + lane) * V;
-      load8(dy, p.dy_type, col, D - col, g[k]);
+      for (int k = 0; k < CH; ++k) {
+        const int col = (k * TPR + lane) * V;
+        load8(row, p.row_type, col, D - col, f[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        const int col = (k * TPR + lane) * V;
+        load8(dy, p.dy_type, col, D - col, g[k]);
+      }
     }
     // dres comes along with the row, and so do the weights: asked for behind
     // the reduction they would be a second wait (a wide row has too many to hold)
@@ -322,6 +373,7 @@ __global__ __launch_bounds__(TPR > NT ? TPR : NT) void norm_bwd_kernel(NormBwdPa
 #pragma unroll
       for (int k = 0; k < CH; ++k) load_dres(k);
     }
+    if constexpr (AHEAD) load_next(r + step < rows ? r + step : r);
     float ss = 0.f, s1 = 0.f;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
@@ -420,8 +472,14 @@ void launch_fwd(const NormParams& p, int64_t rows, hipStream_t stream) {
 
 template <int TPR, int CH>
 void launch_bwd(const NormBwdParams& p, int64_t rows, hipStream_t stream) {
-  hipLaunchKernelGGL((norm_bwd_kernel<TPR, CH>), dim3((unsigned)p.parts), dim3(TPR > NT ? TPR : NT), 0, stream, p,
-                     rows);
+  if constexpr (kAhead<TPR, CH>)
+    if (p.row_type == kNormBF16 && p.dy_type == kNormBF16) {
+      hipLaunchKernelGGL((norm_bwd_kernel<TPR, CH, true>), dim3((unsigned)p.parts), dim3(TPR > NT ? TPR : NT), 0,
+                         stream, p, rows);
+      return;
+    }
+  hipLaunchKernelGGL((norm_bwd_kernel<TPR, CH, false>), dim3((unsigned)p.parts), dim3(TPR > NT ? TPR : NT), 0, stream,
+                     p, rows);
 }
 
 }  // namespace
@@ -434,7 +492,7 @@ void launch_bwd(const NormBwdParams& p, int64_t rows, hipStream_t stream) {
 int norm_bwd_parts(int64_t rows, int64_t dim) {
   const int threads = bwd_threads(rows, dim);
   const int64_t blocks = threads == 64 ? (rows + 3) / 4 : rows;
-  const int64_t cap = 256 * (threads == 512 && dim > 512 * V ? 2 : 4);
+  const int64_t cap = 256 * (threads <= 256 || dim <= 512 * V ? 4 : dim <= 2 * 512 * V ? 2 : 1);
   return (int)std::min({blocks, cap, std::max<int64_t>(256, (blocks + 1) / 2)});
 }
 

@@ -166,6 +166,25 @@ def test_gradients_against_differences():
         assert abs((hi - lo) / (2 * e) - float(terms.sum())) <= 1e-5 * float(terms.abs().sum()), key
 
 
+@pytest.mark.parametrize("res", [None, BF16, F32], ids=lambda v: str(v).replace("torch.", ""))
+@pytest.mark.parametrize("size", [(9000, 40), (8200, 769), (2000, 1500), (3000, 2050), (1500, 4096), (700, 8193),
+                                  (300, 16384), (1, 1024), (257, 9000)], ids=lambda s: "%dx%d" % s)
+def test_backward_of_several_rows_a_workgroup(size, res):
+    """bf16 gradients with odd strides: the loads of the row that comes next
+    reach no further than the last."""
+    rows, dim = size
+    banner("norm backward %s %s" % (size, res))
+    x, r, w, dy, dres = make(rows, dim, BF16, res, seed=rows + dim)
+    row = ref.norm_row(x, r)
+    wide = torch.full((rows, dim + 3), float("nan"), dtype=BF16, device="cuda")
+    wide[:, 1:dim + 1] = dy.cuda()
+    got = ssm.rms_norm_bwd(wide[:, 1:dim + 1], row.cuda(), w.cuda(), eps=EPS,
+                           dres=None if dres is None else dres.cuda())
+    dx, dw, mx, mw = ref.norm_bwd(dy, row, w, EPS, dres)
+    ref.check(got["dx"], dx, mx, 3 * rel(dim), "dx")
+    ref.check(got["dweight"], dw, mw, rel(dim) + (rows / 64 + 128) * ref.U32, "dweight")
+
+
 @pytest.mark.parametrize("group", [0, 128])
 def test_e4m3_workgroup_sizes(group):
     for size in ((1025, 2049), (1030, 6145), (3, 8200)):
