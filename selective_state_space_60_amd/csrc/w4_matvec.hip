@@ -41,13 +41,14 @@
 #include <hip/hip_runtime.h>
 
 #include "ssm_internal.h"
+#include "w4_loads.h"
 
 namespace ssm {
 namespace {
 
-constexpr int W = 8;     // waves
+using namespace w4;
+
 constexpr int NT = W * 64;
-constexpr int KS = 128;  // k of a step: one 16-byte load of weights per lane and tile
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
@@ -55,7 +56,6 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr uint32_t kRsrcWord3 = 0x00020000u;
 constexpr uint32_t kMaxRange = 0x7FFFFF00u;  // the host keeps every range below
-constexpr uint32_t kFar = 0x7FFFFFF0u;       // past every range: loads give 0
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, int64_t bytes) {
   const uint32_t range = bytes < (int64_t)kMaxRange ? (uint32_t)bytes : kMaxRange;
@@ -105,7 +105,7 @@ __device__ __forceinline__ void wave_sync() {
 template <int XR, int NL, int GS, bool SF32>
 __global__ __launch_bounds__(NT, 4) void w4_kernel(W4Params p, unsigned xtiles) {
   constexpr int NG = 4 / GS;                      // scale groups of a step
-  constexpr int SN = (16 * NL * NG + 63) / 64;    // loads of a step's scales
+  constexpr int SN = scale_loads(NL, NG);         // loads of a step's scales
   constexpr int es = SF32 ? 4 : 2;
   struct Stage {
     u32x4_t w[NL][64], x[XR * 64];
@@ -117,16 +117,14 @@ __global__ __launch_bounds__(NT, 4) void w4_kernel(W4Params p, unsigned xtiles) 
   } sh;
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int col = lane % 16, kg = lane / 16;
-  // grid.x tiles of outputs, then the same with the next rows (y): with eight, a
-  // tile's weights are read again on the same XCD.  A tile behind the last
-  // runs with every access out of range: a test up here would be a wait for
-  // the first arguments ahead of the others.
+  // A tile behind the last output has no rows and no steps: its loads are out of
+  // range by the lane offset, at scalar offset 0 (a test up here would be a wait
+  // for the first arguments ahead of the others).
   const int m0 = (int)blockIdx.y * 16;
   const int64_t n0 = ((int64_t)blockIdx.z * xtiles + blockIdx.x) * (16 * NL);
-  const int64_t left = p.outs - n0;
-  const int nrows = left < 0 ? 0 : left < 16 * NL ? (int)left : 16 * NL;
+  const int nrows = tile_rows(p.outs, n0, 16 * NL);
   const int ins = (int)p.ins, half = ins / 2, groups = ins / (32 * GS), rows = (int)p.rows;
-  const int steps = (ins + KS - 1) / KS;
+  const int steps = tile_steps(ins, nrows);
   const __amdgpu_buffer_rsrc_t rw = rsrc(p.weight + n0 * half, (int64_t)nrows * half);
   const __amdgpu_buffer_rsrc_t rs = rsrc((const char*)p.scale + n0 * groups * es, (int64_t)nrows * groups * es);
   const __amdgpu_buffer_rsrc_t rz = rsrc(p.zero ? p.zero + n0 * groups : nullptr, p.zero ? (int64_t)nrows * groups : 0);
@@ -139,22 +137,12 @@ __global__ __launch_bounds__(NT, 4) void w4_kernel(W4Params p, unsigned xtiles) 
   const int wrow = lane / 4, wunit = (lane % 4) ^ (wrow / 4);
   uint32_t woff[NL], xoff[XR], soff[SN];
 #pragma unroll
-  for (int n = 0; n < NL; ++n)
-    woff[n] = n * 16 + wrow < nrows ? (uint32_t)(n * 16 + wrow) * (uint32_t)half + (uint32_t)wunit * 16 : kFar;
+  for (int n = 0; n < NL; ++n) woff[n] = weight_offset(n * 16 + wrow, wunit, nrows, half);
 #pragma unroll
-  for (int i = 0; i < XR; ++i) {
-    const int row = m0 + 4 * i + kg;
-    xoff[i] = row < rows ? (uint32_t)row * (uint32_t)(p.xs_m * 2) + (uint32_t)col * 16 : kFar;
-  }
+  for (int i = 0; i < XR; ++i) xoff[i] = x_offset(m0 + 4 * i + kg, col, rows, p.xs_m);
 #pragma unroll
-  for (int i = 0; i < SN; ++i) {
-    const int e = lane + i * 64;
-    soff[i] = e / NG < nrows ? (uint32_t)(e / NG * groups + e % NG) : kFar / 4;
-  }
-  // The last step may end early: its x and scales are zeros there (weights of
-  // the next row, which are finite, meet x of zero).
-  const uint32_t xend = (steps - 1) * KS + col * 8 < ins ? 0 : kFar;
-  const uint32_t send = (steps - 1) * NG + lane % NG < groups ? 0 : kFar / 4;
+  for (int i = 0; i < SN; ++i) soff[i] = scale_entry(lane + i * 64, NG, nrows, groups);
+  const uint32_t xend = x_end(steps, col, ins), send = scale_end(steps, lane, NG, groups);
   // operand order of the reads
   const int wread = col * 4 + (kg ^ (col / 4));
   const int xrow = col % (XR * 4);
@@ -173,21 +161,18 @@ __global__ __launch_bounds__(NT, 4) void w4_kernel(W4Params p, unsigned xtiles) 
     uint32_t sc[SN], z[SN];
   };
   auto load = [&](Loads& l, int s) {
-    const bool past = s >= steps;
-    const int at = past ? 0 : s;
-    const uint32_t far = past ? kFar : 0;
-    const uint32_t fx = s == steps - 1 ? xend : far, fs = s == steps - 1 ? send : far / 4;
+    const Step q = step_at(s, steps, xend, send);
 #pragma unroll
-    for (int n = 0; n < NL; ++n) l.w[n] = load16(rw, woff[n] | far, at * (KS / 2));
+    for (int n = 0; n < NL; ++n) l.w[n] = load16(rw, woff[n] | q.w, weight_step(q));
 #pragma unroll
     for (int i = 0; i < SN; ++i) {
-      const uint32_t e = soff[i] | fs;
-      if constexpr (SF32) l.sc[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, (int)(e * 4), at * NG * 4, 0);
-      else l.sc[i] = __builtin_amdgcn_raw_buffer_load_b16(rs, (int)(e * 2), at * NG * 2, 0);
-      l.z[i] = __builtin_amdgcn_raw_buffer_load_b8(rz, (int)e, p.zero ? at * NG : 0, 0);
+      const uint32_t e = soff[i] | q.s;
+      if constexpr (SF32) l.sc[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, (int)(e * 4), scale_step(q, NG) * 4, 0);
+      else l.sc[i] = __builtin_amdgcn_raw_buffer_load_b16(rs, (int)(e * 2), scale_step(q, NG) * 2, 0);
+      l.z[i] = __builtin_amdgcn_raw_buffer_load_b8(rz, (int)e, p.zero ? scale_step(q, NG) : 0, 0);
     }
 #pragma unroll
-    for (int i = 0; i < XR; ++i) l.x[i] = load16(rx, xoff[i] | fx, at * (KS * 2));
+    for (int i = 0; i < XR; ++i) l.x[i] = load16(rx, xoff[i] | q.x, x_step(q));
   };
   auto step = [&](Loads& l, int s) {
     wave_sync();
@@ -255,11 +240,10 @@ __global__ __launch_bounds__(NT, 4) void w4_kernel(W4Params p, unsigned xtiles) 
 
 template <int XR, int NL, int GS>
 void launch_s(const W4Params& p, hipStream_t stream) {
-  const unsigned mtiles = (unsigned)((p.rows + 15) / 16), ntiles = (unsigned)((p.outs + 16 * NL - 1) / (16 * NL));
-  const unsigned xtiles = mtiles == 1 ? ntiles : 8 * (ntiles / (8 * 65535) + 1);  // z at most 65535
-  const dim3 grid(xtiles, mtiles, (ntiles + xtiles - 1) / xtiles);
-  if (p.scale_f32) hipLaunchKernelGGL((w4_kernel<XR, NL, GS, true>), grid, dim3(NT), 0, stream, p, xtiles);
-  else hipLaunchKernelGGL((w4_kernel<XR, NL, GS, false>), grid, dim3(NT), 0, stream, p, xtiles);
+  const Grid g = grid_of(p.rows, p.outs, 16 * NL);
+  const dim3 grid(g.x, g.y, g.z);
+  if (p.scale_f32) hipLaunchKernelGGL((w4_kernel<XR, NL, GS, true>), grid, dim3(NT), 0, stream, p, g.x);
+  else hipLaunchKernelGGL((w4_kernel<XR, NL, GS, false>), grid, dim3(NT), 0, stream, p, g.x);
 }
 
 template <int XR, int NL>
