@@ -415,7 +415,11 @@ typedef struct {
  *      y[b,t,d] = h_t * silu(z[b,t,d])               (h_t without SSM_HAS_Z)
  * A is real, normally negative (exp(A) is the decay at an open gate); s_t
  * keeps the state's variance at the input's.  The recurrence is evaluated in
- * fp32; 1 - a_t^2 keeps its relative accuracy for decays near 1.
+ * fp32; 1 - a_t^2 keeps its relative accuracy for decays near 1.  Products of
+ * up to 128 decays are formed in fp32 too: with A > 0 (nothing enters the
+ * state: s_t = 0) a state that is not zero is infinite once such a product
+ * passes the largest fp32.  A state that has become infinite is infinite or
+ * NaN from then on.
  * Lengths: with SSM_HAS_LENS row b counts lens[b] steps, taken into
  * [0, seqlen] by the kernel: later steps leave the state as it is (h_last is
  * the state after step lens[b] - 1, or h0), their inputs have no influence,

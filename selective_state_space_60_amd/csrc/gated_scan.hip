@@ -229,6 +229,13 @@ __device__ __forceinline__ void store_row(const Stream& s, int j, int n, const f
   else store<F32, V>(s.r, s.off, s.at, o);
 }
 
+// What leaves a chunk or a segment with the pair (P, H) that h enters.  The
+// product P of up to 128 decays passes the largest fp32 where A > 0 (no decay
+// of A <= 0 does); a state of zero, which such decays leave at zero, stays so.
+__device__ __forceinline__ float pass_on(float P, float h, float H) {
+  return h == 0.f ? H : __builtin_fmaf(P, h, H);
+}
+
 // ------------------------------------------------------------------ segments
 // Words of the segments of one sequence: agg holds (P, H) of a segment, inc
 // its end state.  All bits set means not yet written (the launch fills them);
@@ -299,7 +306,7 @@ __device__ __forceinline__ bool entering(const Chain& q, int64_t k, int64_t at, 
   }
   // own writes of this lane: no barrier between them and these reads
   for (int d = depth - 1; d >= 0; --d)
-    if (lane < CW) h = __builtin_fmaf(stack[d][lane].x, h, stack[d][lane].y);
+    if (lane < CW) h = pass_on(stack[d][lane].x, h, stack[d][lane].y);
   return true;
 }
 
@@ -427,7 +434,7 @@ struct Fwd : Place<V> {
     for (int q = 0; q < NCH; ++q) {
       const float2 w = sh.pair[q][ch_lane];
       f.x *= w.x;
-      f.y = __builtin_fmaf(w.x, f.y, w.y);
+      f.y = pass_on(w.x, f.y, w.y);
     }
     return f;
   }
@@ -452,7 +459,7 @@ struct Fwd : Place<V> {
       if (!found) found = entering<CW>(q, k, at, mine, sh.stack, l, h);
       if (found) {
         if (mine) {
-          const float end = __builtin_fmaf(f.x, h, f.y);
+          const float end = pass_on(f.x, h, f.y);
           if (more) publish_state(q, at, end);
           else if (Y && p.h_last) p.h_last[b * p.D + c0 + l] = end;
         }
@@ -462,7 +469,7 @@ struct Fwd : Place<V> {
 #pragma unroll 4
           for (int i = 0; i < NCH; ++i) {
             sh.in[i][l] = h;
-            h = __builtin_fmaf(sh.pair[i][l].x, h, sh.pair[i][l].y);
+            h = pass_on(sh.pair[i][l].x, h, sh.pair[i][l].y);
           }
       }
       if (l == 0) sh.found = found;
@@ -527,7 +534,7 @@ __global__ __launch_bounds__(kFwdNT, !BF16 && Z && V == 2 ? kFwdWaves32 : kFwdWa
     __syncthreads();
     if (l < 64) {
       const float2 w = late.fold(sh, l < F::CW ? l : 0);
-      h = __builtin_fmaf(w.x, h, w.y);
+      h = pass_on(w.x, h, w.y);
     }
   }
   __syncthreads();
@@ -647,7 +654,7 @@ struct Bwd : Place<V> {
 #pragma unroll 4
     for (int w = NCH - 1; w >= 0; --w) {
       f.x *= sh.P[w][l];
-      f.y = __builtin_fmaf(sh.P[w][l], f.y, sh.O[w][l]);
+      f.y = pass_on(sh.P[w][l], f.y, sh.O[w][l]);
     }
     return f;
   }
@@ -672,7 +679,7 @@ struct Bwd : Place<V> {
       if (!found) found = entering<CW>(cn, k, at, mine, sh.stack, l, m);
       if (found) {
         if (mine) {
-          const float end = __builtin_fmaf(f.x, m, f.y);
+          const float end = pass_on(f.x, m, f.y);
           if (seg > 0) publish_state(cn, at, end);
           else if (q.dh0) q.dh0[b * p.D + c0 + l] = end;
         }
@@ -682,12 +689,12 @@ struct Bwd : Place<V> {
 #pragma unroll 4
           for (int w = 0; w < NCH; ++w) {
             sh.h[w][l] = h;
-            h = __builtin_fmaf(sh.P[w][l], h, sh.H[w][l]);
+            h = pass_on(sh.P[w][l], h, sh.H[w][l]);
           }
 #pragma unroll 4
           for (int w = NCH - 1; w >= 0; --w) {
             sh.m[w][l] = m;
-            m = __builtin_fmaf(sh.P[w][l], m, sh.O[w][l]);
+            m = pass_on(sh.P[w][l], m, sh.O[w][l]);
           }
         }
       }
@@ -822,7 +829,7 @@ __global__ __launch_bounds__(kBwdNT, kBwdWaves) void gated_bwd_kernel(GatedBwdPa
     __syncthreads();
     if (l < 64) {
       const float2 w = late.fold(sh, l < F::CW ? l : 0);
-      m = __builtin_fmaf(w.x, m, w.y);
+      m = pass_on(w.x, m, w.y);
     }
   }
   __syncthreads();
