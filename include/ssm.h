@@ -447,8 +447,8 @@ typedef struct {
  * the state that enters its segment from the start of the sequence, by the
  * same operations.  SSM_NO_WAIT makes every workgroup do so: the same bits,
  * at a cost that grows with the square of the length.
- * Limit: 128 rows of any (batch, seqlen, dim) tensor must span less than
- * 1 GiB (SSM_ERR_UNSUPPORTED otherwise). */
+ * Limit: 128 rows of any (batch, seqlen, dim) tensor of more than one step
+ * must span less than 1 GiB (SSM_ERR_UNSUPPORTED otherwise). */
 #define SSM_GATED_CKPT_STEPS 64
 
 typedef struct {

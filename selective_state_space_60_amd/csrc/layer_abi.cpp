@@ -157,9 +157,12 @@ GatedPlan plan_gated(int64_t batch, int64_t seqlen, int64_t dim) {
   return pl;
 }
 
+// Elements from one step to the next; a single step's stride addresses nothing.
+int64_t time_stride(const ssm_tensor_desc& t) { return t.shape[1] > 1 ? t.stride[1] : 0; }
+
 // A segment's rows must fit the 32-bit offsets of the kernel.
 bool gated_fits(const ssm_tensor_desc& t) {
-  return (ssm::kGatedSpanSteps * (__int128)t.stride[1] + 64) * esize(t.dtype) < kMaxSpan;
+  return (ssm::kGatedSpanSteps * (__int128)time_stride(t) + 64) * esize(t.dtype) < kMaxSpan;
 }
 
 struct GatedShapes {
@@ -235,10 +238,10 @@ ssm::GatedParams gated_params(const D& d, const P& p) {
   q.h0 = (f & SSM_HAS_H0) ? p.h0 : nullptr;
   q.lens = (f & SSM_HAS_LENS) ? p.lens : nullptr;
   q.batch = d.batch; q.L = d.seqlen; q.D = d.dim;
-  q.xs_b = d.x.stride[0]; q.xs_t = d.x.stride[1];
-  q.gas_b = d.gate_a.stride[0]; q.gas_t = d.gate_a.stride[1];
-  q.gxs_b = d.gate_x.stride[0]; q.gxs_t = d.gate_x.stride[1];
-  if (q.z) { q.zs_b = d.z.stride[0]; q.zs_t = d.z.stride[1]; }
+  q.xs_b = d.x.stride[0]; q.xs_t = time_stride(d.x);
+  q.gas_b = d.gate_a.stride[0]; q.gas_t = time_stride(d.gate_a);
+  q.gxs_b = d.gate_x.stride[0]; q.gxs_t = time_stride(d.gate_x);
+  if (q.z) { q.zs_b = d.z.stride[0]; q.zs_t = time_stride(d.z); }
   q.As_d = d.A.stride[0];
   if (q.bias_a) q.bas_d = d.bias_a.stride[0];
   if (q.bias_x) q.bxs_d = d.bias_x.stride[0];
@@ -481,7 +484,7 @@ ssm_status ssm_gated_scan_fwd(const ssm_gated_desc* d, const ssm_gated_ptrs* p, 
   if (need && !aligned(workspace, 256)) return SSM_ERR_ALIGN;
   ssm::GatedParams q = gated_params(*d, *p);
   q.y = p->y;
-  q.ys_b = d->y.stride[0]; q.ys_t = d->y.stride[1];
+  q.ys_b = d->y.stride[0]; q.ys_t = time_stride(d->y);
   q.y_f32 = d->y.dtype == SSM_F32;
   q.h_last = (d->flags & SSM_WANT_HLAST) ? p->h_last : nullptr;
   q.ckpt = (d->flags & SSM_WANT_CKPT) ? p->ckpt : nullptr;
@@ -520,11 +523,11 @@ ssm_status ssm_gated_scan_bwd(const ssm_gated_bwd_desc* d, const ssm_gated_bwd_p
   q.dbias_a = (f & SSM_HAS_BIAS_A) ? p->dbias_a : nullptr;
   q.dbias_x = (f & SSM_HAS_BIAS_X) ? p->dbias_x : nullptr;
   q.dh0 = (f & SSM_HAS_H0) ? p->dh0 : nullptr;
-  q.dys_b = d->dy.stride[0]; q.dys_t = d->dy.stride[1];
-  q.dxs_b = d->dx.stride[0]; q.dxs_t = d->dx.stride[1];
-  q.dgas_b = d->dgate_a.stride[0]; q.dgas_t = d->dgate_a.stride[1];
-  q.dgxs_b = d->dgate_x.stride[0]; q.dgxs_t = d->dgate_x.stride[1];
-  if (q.dz) { q.dzs_b = d->dz.stride[0]; q.dzs_t = d->dz.stride[1]; }
+  q.dys_b = d->dy.stride[0]; q.dys_t = time_stride(d->dy);
+  q.dxs_b = d->dx.stride[0]; q.dxs_t = time_stride(d->dx);
+  q.dgas_b = d->dgate_a.stride[0]; q.dgas_t = time_stride(d->dgate_a);
+  q.dgxs_b = d->dgate_x.stride[0]; q.dgxs_t = time_stride(d->dgate_x);
+  if (q.dz) { q.dzs_b = d->dz.stride[0]; q.dzs_t = time_stride(d->dz); }
   q.g_f32 = d->dy.dtype == SSM_F32;
   if (!(f & SSM_HAS_CKPT)) {
     const hipError_t e = ssm::launch_gated_scan(q.f, st);  // y is null: checkpoints only
