@@ -125,34 +125,39 @@ PyObject* empty(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   });
 }
 
-// launch(entry, descriptor, tensors, bytes, stream): the entry point's status.
-// Entry, descriptor and stream are addresses.  bytes: size of the workspace,
-// which is allocated on the first tensor's device for the current stream; < 0:
-// an entry point without one.
+// launch(entry, descriptor, tensors, written, bytes, stream): the entry point's
+// status.  Entry, descriptor and stream are addresses.  written: bit i says that
+// tensor i is written; the others are only read, so that a lazily copied one
+// stays shared.  bytes: size of the workspace, which is allocated on the first
+// tensor's device for the current stream; < 0: an entry point without one.
 PyObject* launch(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
-  if (nargs != 5 || !PyTuple_Check(args[2])) {
-    PyErr_SetString(PyExc_TypeError, "launch(entry, descriptor, tensors, bytes, stream)");
+  if (nargs != 6 || !PyTuple_Check(args[2])) {
+    PyErr_SetString(PyExc_TypeError, "launch(entry, descriptor, tensors, written, bytes, stream)");
     return nullptr;
   }
   return guarded([&]() -> PyObject* {
     void* const entry = PyLong_AsVoidPtr(args[0]);
     void* const desc = PyLong_AsVoidPtr(args[1]);
-    const long long bytes = PyLong_AsLongLong(args[3]);
-    void* const stream = PyLong_AsVoidPtr(args[4]);
+    const unsigned long written = PyLong_AsUnsignedLong(args[3]);
+    const long long bytes = PyLong_AsLongLong(args[4]);
+    void* const stream = PyLong_AsVoidPtr(args[5]);
     if (PyErr_Occurred()) return nullptr;
     const Py_ssize_t n = PyTuple_GET_SIZE(args[2]);
     if (!entry || n > kMaxTensors) {
       PyErr_SetString(PyExc_ValueError, "no entry point, or too many tensors");
       return nullptr;
     }
-    void* ptrs[kMaxTensors];
+    const void* ptrs[kMaxTensors];
     const at::Tensor* first = nullptr;
-    for (Py_ssize_t i = 0; i < n; ++i) {
-      const at::Tensor* t;
-      if (!tensor_of(PyTuple_GET_ITEM(args[2], i), &t)) return nullptr;
-      ptrs[i] = t ? t->mutable_data_ptr() : nullptr;
-      if (!first) first = t;
-    }
+    // the written ones first: one that is read as well gets its own memory there
+    for (const bool write : {true, false})
+      for (Py_ssize_t i = 0; i < n; ++i) {
+        const at::Tensor* t;
+        if ((written >> i & 1) != write) continue;
+        if (!tensor_of(PyTuple_GET_ITEM(args[2], i), &t)) return nullptr;
+        ptrs[i] = !t ? nullptr : write ? t->mutable_data_ptr() : t->const_data_ptr();
+        if (t && (!first || i == 0)) first = t;
+      }
     at::Tensor ws;
     if (bytes > 0) {
       if (!first) {

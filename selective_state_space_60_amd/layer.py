@@ -74,9 +74,9 @@ def _new(t, shape, dtype):
 
 class _Plan:
     """An entry point with a descriptor of fixed shapes, and the workspace size it asks for."""
-    __slots__ = ("entry", "fn", "desc", "address", "index", "nbytes")
+    __slots__ = ("entry", "fn", "desc", "address", "index", "written", "nbytes")
 
-    def __init__(self, entry, Desc, names, sizes, flags, tensors, size_entry=None):
+    def __init__(self, entry, Desc, names, sizes, flags, tensors, written, size_entry=None):
         index = tensors[0].get_device()
         if index < 0:
             raise ValueError("%s: tensors must be on a GPU" % entry)
@@ -92,6 +92,7 @@ class _Plan:
         # the pointer structs of these entry points hold one pointer per tensor, in the order of `names`
         self.entry, self.index, self.desc, self.address = entry, index, d, ctypes.addressof(d)
         self.fn = ctypes.cast(getattr(lib(), entry), ctypes.c_void_p).value
+        self.written = sum(1 << i for i, name in enumerate(names) if name in written)
         self.nbytes = -1  # an entry point without a workspace
         if size_entry is not None:
             n = ctypes.c_size_t()
@@ -114,10 +115,10 @@ def _launch(plan, tensors, stream):
         with torch.cuda.device(plan.index):
             return _launch(plan, tensors, stream)
     if stream is None:
-        status = _run(plan.fn, plan.address, tensors, plan.nbytes, _raw_stream(plan.index))
+        status = _run(plan.fn, plan.address, tensors, plan.written, plan.nbytes, _raw_stream(plan.index))
     else:
         with torch.cuda.stream(stream):  # the workspace belongs to its pool
-            status = _run(plan.fn, plan.address, tensors, plan.nbytes, stream.cuda_stream)
+            status = _run(plan.fn, plan.address, tensors, plan.written, plan.nbytes, stream.cuda_stream)
     if status:
         _check(status, plan.entry)
 
@@ -179,7 +180,7 @@ def gated_scan_fwd(x, gate_a, gate_x, A, bias_a=None, bias_x=None, z=None, h0=No
                  (SSM_WANT_CKPT if ckpt is not None else 0))
         plan = _keep(key, _Plan("ssm_gated_scan_fwd", GatedDesc, _GATED_T,
                                 (("batch", batch), ("seqlen", L), ("dim", dim)), flags, tensors,
-                                "ssm_gated_scan_workspace_size"))
+                                ("y", "h_last", "ckpt"), "ssm_gated_scan_workspace_size"))
     _launch(plan, tensors, stream)
     return y, h_last
 
@@ -221,7 +222,7 @@ def gated_scan_bwd(dy, x, gate_a, gate_x, A, bias_a=None, bias_x=None, z=None, h
                  (SSM_HAS_LENS if lens is not None else 0) | (SSM_HAS_CKPT if ckpt is not None else 0) |
                  (SSM_HAS_DHLAST if dh_last is not None else 0))
         plan = _keep(key, _Plan("ssm_gated_scan_bwd", GatedBwdDesc, _GATED_BWD_T,
-                                (("batch", batch), ("seqlen", L), ("dim", dim)), flags, tensors,
+                                (("batch", batch), ("seqlen", L), ("dim", dim)), flags, tensors, tuple(out),
                                 "ssm_gated_scan_bwd_workspace_size"))
     _launch(plan, tensors, stream)
     return {k: v for k, v in out.items() if v is not None}
@@ -242,7 +243,8 @@ def gated_state_update(state, x, gate_a, gate_x, A, bias_a=None, bias_x=None, z=
         batch, dim = x.shape
         flags = _gated_flags(bias_a, bias_x, z) | (SSM_HAS_STATE_OUT if state_out is not None else 0)
         plan = _keep(key, _Plan("ssm_gated_state_update", GatedUpdateDesc, _GATED_UPD_T,
-                                (("batch", batch), ("dim", dim)), flags, tensors))
+                                (("batch", batch), ("dim", dim)), flags, tensors,
+                                ("y", "state" if state_out is None else "state_out")))
     _launch(plan, tensors, stream)
     return y
 
@@ -287,7 +289,8 @@ def rms_norm(x, weight, eps=1e-5, residual=None, residual_dtype=None, residual_o
                                 (("batch", x3.shape[0]), ("seqlen", x3.shape[1]), ("dim", x3.shape[2]),
                                  ("group", group), ("eps", float(eps))),
                                 SSM_HAS_RESIDUAL if residual is not None else 0,
-                                (x3, _rows(residual), weight, _rows(y), _rows(residual_out), _rows(scale))))
+                                (x3, _rows(residual), weight, _rows(y), _rows(residual_out), _rows(scale)),
+                                ("y", "residual_out", "scale")))
     _launch(plan, tensors, stream)
     return y, residual_out, scale
 
@@ -313,7 +316,7 @@ def rms_norm_bwd(dy, row, weight, eps=1e-5, dres=None, grad_dtype=None, stream=N
         plan = _keep(key, _Plan("ssm_rms_norm_bwd", NormBwdDesc, _NORM_BWD_T,
                                 (("batch", r3.shape[0]), ("seqlen", r3.shape[1]), ("dim", r3.shape[2]),
                                  ("eps", float(eps))), SSM_HAS_RESIDUAL if dres is not None else 0,
-                                (_rows(dy), r3, weight, _rows(dres), _rows(dx), dweight),
+                                (_rows(dy), r3, weight, _rows(dres), _rows(dx), dweight), ("dx", "dweight"),
                                 "ssm_rms_norm_bwd_workspace_size"))
     _launch(plan, tensors, stream)
     return {"dx": dx, "dweight": dweight}
@@ -357,6 +360,6 @@ def w4_matvec(x, weight, scale, zero=None, bias=None, y_dtype=None, y=None, stre
                                 (("rows", rows), ("ins", ins), ("outs", weight.shape[0]),
                                  ("group", ins // scale.shape[1])),
                                 (SSM_HAS_ZERO if zero is not None else 0) |
-                                (SSM_HAS_BIAS if bias is not None else 0), tensors))
+                                (SSM_HAS_BIAS if bias is not None else 0), tensors, ("y",)))
     _launch(plan, tensors, stream)
     return y
