@@ -7,6 +7,7 @@
 
 #include <ATen/ATen.h>
 #include <torch/csrc/Dtype.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
@@ -29,12 +30,14 @@ bool tensor_of(PyObject* o, const at::Tensor** t) {
   return true;
 }
 
+// Exceptions become the Python errors that torch makes of its own (an
+// allocation that fails is torch.OutOfMemoryError).
 template <class F>
 PyObject* guarded(F f) {
   try {
     return f();
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {
+    torch::translate_exception_to_python(std::current_exception());
     return nullptr;
   }
 }

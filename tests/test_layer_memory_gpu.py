@@ -1,5 +1,5 @@
 """What the layer's binding does with memory: operands that are only read stay
-shared, and what is written is written alone."""
+shared, what is written is written alone, and an allocation that fails says so."""
 import pytest
 
 from _gpu import banner
@@ -65,3 +65,19 @@ def test_lazily_copied_outputs_are_written_alone():
     ssm.rms_norm(x, w, y=buf)
     torch.cuda.synchronize()
     assert torch.equal(first, keep) and torch.equal(buf, ssm.rms_norm(x, w)[0])
+
+
+def test_out_of_memory_is_torchs_own_error():
+    """An output that does not fit what the process may use: the error that a
+    caller catches for torch's own allocations."""
+    banner("out of memory")
+    x = torch.zeros(1, 1024, device="cuda", dtype=BF16).expand(1 << 23, 1024)  # 16 GiB of y
+    w = torch.ones(1024, device="cuda")
+    torch.cuda.empty_cache()
+    torch.cuda.set_per_process_memory_fraction(0.02)
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            ssm.rms_norm(x, w)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert ssm.rms_norm(x[:3], w)[0].shape == (3, 1024)
