@@ -204,12 +204,12 @@ def gated_scan_bwd(dy, x, gate_a, gate_x, A, bias_a=None, bias_x=None, z=None, h
         given = tuple([out.get(k) for k in _GATED_OUT])
         if not out.keys() <= set(_GATED_OUT):
             raise ValueError("gated_scan_bwd: out takes " + ", ".join(_GATED_OUT))
+        if z is None and given[3] is not None:
+            raise ValueError("gated_scan_bwd: out holds dz, but there is no z")
     key = ("gated_scan_bwd", _sig(ins), _sig(given) if out else None)
     plan = _plans.get(key)
     dx, dga, dgx, dz = [_like(stream, dy) if t is None else t for t in given[:3]] + [given[3]]
-    if z is None:
-        dz = None
-    elif dz is None:
+    if z is not None and dz is None:
         dz = _like(stream, dy)
     out = {"dx": dx, "dgate_a": dga, "dgate_x": dgx, "dz": dz, "dA": _like(stream, A),
            "dbias_a": None if bias_a is None else _like(stream, bias_a),

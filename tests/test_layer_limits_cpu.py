@@ -35,3 +35,14 @@ def test_one_step_has_no_span(io):
             d, _ = gated_bwd(L=L, io=io, g=io, flags=BWD_ALL)
             setattr(d, name, far)
             assert size_of("ssm_gated_scan_bwd", d) == status, (L, stride, name)
+
+
+def test_dz_without_z_is_refused():
+    """Memory for a gradient that the call does not have would stay as it was."""
+    x, v = torch.zeros(2, 4, 8), torch.zeros(8)
+    with pytest.raises(ValueError, match="dz"):
+        S.gated_scan_bwd(x, x, x, x, v, out={"dz": torch.empty_like(x)})
+    with pytest.raises(ValueError, match="GPU"):
+        S.gated_scan_bwd(x, x, x, x, v, out={"dz": None})
+    with pytest.raises(ValueError, match="GPU"):
+        S.gated_scan_bwd(x, x, x, x, v, z=x, out={"dz": torch.empty_like(x)})
