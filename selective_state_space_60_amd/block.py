@@ -89,12 +89,27 @@ class GatedLayerWeights:
         return proj.split(self.E, -1)
 
 
+def _behind(lens, L):
+    """(batch, L, 1): the steps behind each row's length."""
+    return (torch.arange(L, device=lens.device) >= lens[:, None]).unsqueeze(-1)
+
+
 def gated_layer_fwd(u, residual, w: GatedLayerWeights, h0=None, lens=None, train=False):
     """u: (batch, L, M) bf16; residual: (batch, L, M) bf16 or fp32; h0, lens as
     in gated_scan_fwd.  Returns (output (batch, L, M) bf16, new residual, final
-    state (batch, E) fp32), and with train what gated_layer_bwd takes."""
+    state (batch, E) fp32), and with train what gated_layer_bwd takes.
+
+    Behind a row's length u and residual may hold anything: the output is zeros
+    there, the new residual is their sum, and nothing reaches a gradient of a
+    weight (products of the padding with zeros would, where it is infinite or
+    NaN, so what the backward takes does not hold it)."""
     batch, L, M = u.shape
     y, residual, _ = rms_norm(u, w.norm, eps=w.eps, residual=residual)
+    row = residual
+    if train and lens is not None:
+        behind = _behind(lens, L)
+        y.masked_fill_(behind, 0)
+        row = residual.masked_fill(behind, 1)  # a row of zeros has no norm with eps 0
     proj = torch.mm(y.reshape(batch * L, M), w.w_in_t).view(batch, L, 4 * w.E)
     x, ga, gx, z = w.split(proj)
     ckpt = gated_scan_ckpt(batch, L, w.E, u.device) if train else None
@@ -102,7 +117,7 @@ def gated_layer_fwd(u, residual, w: GatedLayerWeights, h0=None, lens=None, train
     out = torch.mm(h.reshape(batch * L, w.E), w.w_out_t).view(batch, L, M)
     if not train:
         return out, residual, state
-    return out, residual, state, {"row": residual, "y": y, "proj": proj, "h": h, "h0": h0, "lens": lens, "ckpt": ckpt}
+    return out, residual, state, {"row": row, "y": y, "proj": proj, "h": h, "h0": h0, "lens": lens, "ckpt": ckpt}
 
 
 def gated_layer_bwd(dout, dresidual, w: GatedLayerWeights, saved: dict, dstate=None) -> dict:
@@ -110,9 +125,12 @@ def gated_layer_bwd(dout, dresidual, w: GatedLayerWeights, saved: dict, dstate=N
     and dresidual (the residual's type) reach its outputs, dstate (batch, E)
     its final state.  Returns du (of the layer input and of the residual alike,
     the residual's type), dh0, and the weights' gradients dnorm, dA, dbias_a,
-    dbias_x (fp32), dw_in_t, dw_out_t (bf16, as the GEMMs hold the weights)."""
+    dbias_x (fp32), dw_in_t, dw_out_t (bf16, as the GEMMs hold the weights).
+    Behind a row's length dout may hold anything, and du is dresidual."""
     batch, L, M = dout.shape
     T = batch * L
+    if saved["lens"] is not None:
+        dout = dout.masked_fill(_behind(saved["lens"], L), 0)
     dout2 = dout.reshape(T, M)
     dh = torch.mm(dout2, w.w_out_t.t().contiguous()).view(batch, L, w.E)
     dw_out_t = torch.mm(saved["h"].reshape(T, w.E).t().contiguous(), dout2)
