@@ -199,12 +199,9 @@ __global__ __launch_bounds__(TPR > NT ? TPR : NT) void norm_fwd_kernel(NormParam
     load8(x, p.x_type, col, D - col, f[k]);
   }
   // the weights come along with the row: asked for behind the reduction they
-  // would be a second wait (a wide row has too many to hold)
-  constexpr bool kEarly = CH <= 4;
-  if constexpr (kEarly) {
+  // would be a second wait
 #pragma unroll
-    for (int k = 0; k < CH; ++k) load8(p.weight, kNormF32, (k * TPR + lane) * V, D - (k * TPR + lane) * V, w[k]);
-  }
+  for (int k = 0; k < CH; ++k) load8(p.weight, kNormF32, (k * TPR + lane) * V, D - (k * TPR + lane) * V, w[k]);
   if (p.residual) {
     const void* res = (const char*)p.residual + (b * p.rs_b + t * p.rs_t) * re;
     void* out = (char*)p.residual_out + (b * p.ros_b + t * p.ros_t) * oe;
@@ -239,8 +236,6 @@ __global__ __launch_bounds__(TPR > NT ? TPR : NT) void norm_fwd_kernel(NormParam
   float amax = 0.f;
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
-    const int col = (k * TPR + lane) * V;
-    if constexpr (!kEarly) load8(p.weight, kNormF32, col, D - col, w[k]);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       f[k][i] = f[k][i] * rstd * w[k][i];
