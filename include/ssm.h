@@ -447,8 +447,10 @@ typedef struct {
  * the state that enters its segment from the start of the sequence, by the
  * same operations.  SSM_NO_WAIT makes every workgroup do so: the same bits,
  * at a cost that grows with the square of the length.
- * Limit: 128 rows of any (batch, seqlen, dim) tensor of more than one step
- * must span less than 1 GiB (SSM_ERR_UNSUPPORTED otherwise). */
+ * Limits (SSM_ERR_UNSUPPORTED otherwise): 128 rows of any (batch, seqlen,
+ * dim) tensor of more than one step span less than 1 GiB; batch
+ * ceil(dim/32) < 2^24 - 7, ceil(dim/32) < 2^22; the segments' words at 64
+ * steps each, 12 batch dim ceil(seqlen/64) bytes, are less than 32 GiB. */
 #define SSM_GATED_CKPT_STEPS 64
 
 typedef struct {
@@ -494,7 +496,7 @@ typedef struct {
  * The sums over batch and time are fp32 partial sums added in a fixed order,
  * so the results are deterministic.  SSM_NO_WAIT as in the forward.  Outputs
  * may not overlap inputs or each other.  Workspace: ssm_gated_scan_bwd_workspace_size bytes, 256-byte
- * aligned.  Limit: the forward's span limit. */
+ * aligned.  Limits: the forward's. */
 typedef struct {
   int64_t batch, seqlen, dim;
   uint32_t flags;
@@ -533,7 +535,8 @@ typedef struct {
  *   state     : (batch, dim) F32 contiguous, read and overwritten; with
  *               SSM_HAS_STATE_OUT only read, and
  *   state_out : (batch, dim) F32 contiguous takes the new state
- * Outputs may not overlap inputs (but state, in place) or each other. */
+ * Outputs may not overlap inputs (but state, in place) or each other.
+ * Limit: batch ceil(dim/256) < 2^24 (SSM_ERR_UNSUPPORTED otherwise). */
 typedef struct {
   int64_t batch, dim;
   uint32_t flags;
@@ -560,8 +563,10 @@ typedef struct {
  *      row = x + residual                (rounded to residual_out's type; x
  *                                         itself without SSM_HAS_RESIDUAL)
  *      y   = weight * row / sqrt(mean(row^2) + eps)
- * The mean and the scaling are fp32.  The norm is taken of the row as
- * residual_out stores it, so that the backward sees the same row.
+ * The mean and the scaling are fp32: a row whose sum of squares passes the
+ * largest fp32 (values around 1e19) gives zeros, and one whose mean of squares
+ * comes to 0 with eps 0 gives no finite values.  The norm is taken of the row
+ * as residual_out stores it, so that the backward sees the same row.
  * An E4M3 output is quantised by `group` consecutive columns (0: the whole
  * row; the last group of a row may be shorter):
  *      scale = max(amax(|y|) / 448, 2^-126),   y8 = y / scale (nearest even)
@@ -576,8 +581,9 @@ typedef struct {
  *   scale    : (batch, seqlen, ceil(dim/group)) F32 contiguous ((batch, seqlen, 1) with
  *              group 0)                               if y is E4M3
  * io is SSM_F32 or SSM_BF16.  group: 0, 32, 64 or 128 (0 unless y is E4M3).
- * dim <= SSM_NORM_MAX_DIM.  eps >= 0.  Outputs may not overlap inputs (but
- * residual_out, above) or each other. */
+ * dim <= SSM_NORM_MAX_DIM, batch seqlen < 2^24 (SSM_ERR_UNSUPPORTED
+ * otherwise).  eps >= 0.  Outputs may not overlap inputs (but residual_out,
+ * above) or each other. */
 #define SSM_NORM_MAX_DIM 16384
 
 typedef struct {
@@ -610,8 +616,8 @@ typedef struct {
  *   dweight : (dim) F32 contiguous
  * dweight is a fixed-order sum of per-workgroup fp32 partial sums
  * (deterministic).  Workspace: ssm_rms_norm_bwd_workspace_size bytes,
- * 256-byte aligned.  dim and eps as in the forward; outputs may not overlap
- * inputs or each other. */
+ * 256-byte aligned.  dim, rows and eps as in the forward; outputs may not
+ * overlap inputs or each other. */
 typedef struct {
   int64_t batch, seqlen, dim;
   float eps;
@@ -635,8 +641,10 @@ typedef struct {
  * q[n,k] is the low (k even) or high (k odd) half of byte weight[n, k/2], 0..15;
  * zero is 8 without SSM_HAS_ZERO.  Products are bf16 matrix-core products of
  * x with q + 16 (exact in bf16), summed in fp32 by groups; 16 + zero times the
- * group's sum of x is taken off before the group's scale.  A row of x that
- * holds an infinity or a NaN has NaN in its whole row of y; with |x| below
+ * group's sum of x is taken off before the group's scale, so that the fp32
+ * sums round relative to sum |x| (32 + q + zero) scale (far below bf16's
+ * rounding; a few times a direct fp32 product's where y is F32).  A row of x
+ * that holds an infinity or a NaN has NaN in its whole row of y; with |x| below
  * 2^112 no group's sum overflows.
  *   x      : (rows, ins) BF16               rows contiguous and 16-byte aligned
  *   weight : (outs, ins/2) U8 contiguous, 16-byte aligned
@@ -644,8 +652,9 @@ typedef struct {
  *   zero   : (outs, ins/group) U8 contiguous   if SSM_HAS_ZERO (values to 255 count as they are)
  *   bias   : (outs) F32, any stride         if SSM_HAS_BIAS
  *   y      : (rows, outs) BF16 or F32       innermost stride 1
- * group: 32, 64 or 128; ins a multiple of group; rows <= SSM_W4_MAX_ROWS.
- * y may not overlap an input. */
+ * group: 32, 64 or 128; ins a multiple of group; rows <= SSM_W4_MAX_ROWS; ins
+ * < 2^26, outs <= 2^27 - 16, the rows of x span less than 1 GiB
+ * (SSM_ERR_UNSUPPORTED otherwise).  y may not overlap an input. */
 #define SSM_W4_MAX_ROWS 64
 
 typedef struct {

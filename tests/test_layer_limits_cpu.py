@@ -10,7 +10,7 @@ torch = pytest.importorskip("torch")
 if torch.cuda.is_available():  # pragma: no cover
     pytest.skip("host-validation tests run without a GPU", allow_module_level=True)
 
-from test_layer_abi_cpu import GATED_ALL, BWD_ALL, gated, gated_bwd, td  # noqa: E402
+from test_layer_abi_cpu import BWD_ALL, GATED_ALL, gated, gated_bwd, gated_update, norm, norm_bwd, td, w4  # noqa: E402
 
 S = ssm
 BLD = ("x", "gate_a", "gate_x", "z")
@@ -46,3 +46,52 @@ def test_dz_without_z_is_refused():
         S.gated_scan_bwd(x, x, x, x, v, out={"dz": None})
     with pytest.raises(ValueError, match="GPU"):
         S.gated_scan_bwd(x, x, x, x, v, z=x, out={"dz": torch.empty_like(x)})
+
+
+@pytest.mark.parametrize("sizes,ok", [
+    # batch ceil(dim / 32) < 2^24 - 7
+    ((1 << 23, 1, 33), False), (((1 << 23) - 4, 1, 33), True), (((1 << 23) - 3, 1, 33), False),
+    # ceil(dim / 32) < 2^22
+    ((1, 1, 32 * ((1 << 22) - 1)), True), ((1, 1, 32 * ((1 << 22) - 1) + 1), False),
+    # 12 batch dim ceil(seqlen / 64) < 2^35
+    ((1, 64 * (1 << 20), 2730), True), ((1, 64 * (1 << 20), 2731), False),
+])
+def test_scan_sizes(sizes, ok):
+    status = S.SSM_OK if ok else S.SSM_ERR_UNSUPPORTED
+    d, _ = gated(*sizes, flags=GATED_ALL)
+    assert size_of("ssm_gated_scan", d) == status
+    d, _ = gated_bwd(*sizes, flags=BWD_ALL)
+    assert size_of("ssm_gated_scan_bwd", d) == status
+
+
+# Without a GPU a call that passes every check ends at the launch.
+def taken(status):
+    assert status in (S.SSM_ERR_HIP, S.SSM_ERR_UNSUPPORTED)
+    return status == S.SSM_ERR_HIP
+
+
+@pytest.mark.parametrize("batch,dim,ok", [((1 << 24) - 1, 256, True), (1 << 24, 1, False), (1 << 23, 257, False),
+                                          ((1 << 23) - 1, 512, True)])
+def test_step_sizes(batch, dim, ok):
+    d, p = gated_update(batch, dim)
+    assert taken(S.lib().ssm_gated_state_update(ctypes.byref(d), ctypes.byref(p), None)) == ok
+
+
+@pytest.mark.parametrize("batch,L,ok", [(1, (1 << 24) - 1, True), (1 << 12, 1 << 12, False), (1 << 24, 1, False)])
+def test_norm_rows(batch, L, ok):
+    d, p = norm(batch, L, 8)
+    assert taken(S.lib().ssm_rms_norm_fwd(ctypes.byref(d), ctypes.byref(p), None)) == ok
+    d, _ = norm_bwd(batch, L, 8)
+    assert (size_of("ssm_rms_norm_bwd", d) == S.SSM_OK) == ok
+
+
+@pytest.mark.parametrize("rows,ins,outs,stride,ok", [
+    (1, (1 << 26) - 128, 1, None, True), (1, 1 << 26, 1, None, False),
+    (1, 128, (1 << 27) - 16, None, True), (1, 128, (1 << 27) - 15, None, False),
+    (2, 128, 1, (1 << 29) - 136, True), (2, 128, 1, (1 << 29) - 128, False), (1, 128, 1, 1 << 40, True),
+])
+def test_w4_sizes(rows, ins, outs, stride, ok):
+    d, p = w4(rows, ins, outs)
+    if stride is not None:
+        d.x = td((rows, ins), "bf16", (stride, 1))
+    assert taken(S.lib().ssm_w4_matvec(ctypes.byref(d), ctypes.byref(p), None)) == ok
