@@ -34,9 +34,12 @@
 // is affine in the carry m as well, with the same product P, and its carry is
 // found among the later segments in the same way.
 //
-// Measured: forward 4 x 4096 x 5120 bf16 with z 191 us (4.4 TB/s; VALU 55 %
-// busy; 243 us with 16 chunks a segment and fewer waves), 1 x 131072 x 1536 fp32
-// 622 us (5.2 TB/s); backward 8 x 2048 x 1536 bf16 with z 112 us (4.0 TB/s).
+// Times here and below are of calls in a captured graph, replayed over sets of
+// inputs that together exceed the last-level cache; a call is its fill, its
+// kernel and, backward, its sums.  Forward 4 x 4096 x 5120 bf16 with z 196 us (4.3
+// TB/s; VALU 55 % busy; 243 us with 16 chunks a segment and fewer waves), 1 x
+// 131072 x 1536 fp32 634 us (5.1 TB/s); backward 8 x 2048 x 1536 bf16 with z 121 us
+// (3.7 TB/s).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -712,7 +715,7 @@ struct Bwd : Place<V> {
       for (uint32_t& x : xr[j].w) asm volatile("" : "+v"(x));
     }
     // bf16 with z: four outputs' addresses on top of the inputs' spill (8 x 2048 x
-    // 1536 127 us, read anew 124; but fp32 203 against 237, bf16 without z 106
+    // 1536 127 us, read anew 124; but held fp32 203 against 237, bf16 without z 106
     // against 109)
     constexpr bool kAnew = BF16 && Z;
     const GatedBwdParams& q = kAnew ? args_anew<GatedBwdParams>() : this->q;

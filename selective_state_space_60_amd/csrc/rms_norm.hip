@@ -4,14 +4,19 @@
 //   row = x + residual (rounded to the type it is stored in)
 //   y   = weight row rstd,  rstd = rsqrt(mean(row^2) + eps)
 //
+// Times here and below are of calls in a captured graph, replayed over sets of
+// inputs that together exceed the last-level cache; a backward is its kernel
+// and its sums.
+//
 // Bound by HBM: a row is read once, kept in registers across the reduction
 // and written once (16384 x 2560, bf16 in, fp32 residual in and out, bf16 out:
-// 95 us, 5.3 TB/s; a large copy runs at 4.7).  A workgroup of four or eight waves
+// 94 us, 5.3 TB/s; a large copy runs at 4.7).  A workgroup of four or eight waves
 // owns a row, or a wave each of four narrow rows (no barrier).  A lane holds
 // groups of 8 consecutive columns: 16-byte loads of bf16, and an e4m3 group of
 // 32, 64 or 128 columns is 4, 8 or 16 neighbouring lanes, whose largest value is
-// found with DPP.  Few rows take one pass of latencies (1 x 2560 2.8 us, 333 x 5120 to
-// e4m3 6.8, of which a launch is 2.3).
+// found with DPP.  Few rows take one pass of latencies (1 x 2560 2.8 us, of which a
+// launch is 2.3; 333 x 5120 with a bf16 residual to e4m3 6.8, without it 5.3,
+// without it to bf16 4.5).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -287,8 +292,9 @@ __global__ __launch_bounds__(TPR > NT ? TPR : NT) void norm_fwd_kernel(NormParam
 // Workgroups walk the rows with a stride and keep dweight's sums of their rows
 // in registers; the four waves' sums are added in order through LDS.  AHEAD, for
 // bf16 rows and gradients: the next row's, 8 registers for 8 columns, are asked
-// for before this row's sums (16384 x 768 36.9 -> 32.0 us, 16384 x 2560 111 -> 85,
-// 4096 x 16384 145 -> 102).  Not where they would cost a wave a SIMD (256 threads
+// for before this row's sums (16384 x 768 36.9 -> 32.0 us, 16384 x 2560 111 -> 86,
+// 4096 x 16384 145 -> 102).  fp32 rows, as an fp32 residual stream has them, take
+// no part in it (16384 x 768 36.4 us, 16384 x 2560 107, 4.7 TB/s).  Not where they would cost a wave a SIMD (256 threads
 // with three column groups: 173 us at 16384 x 5120 against 203; 512 with two: 106
 // at 8192 x 8192 either way).
 template <int TPR, int CH>

@@ -34,8 +34,10 @@
 // (64 x 2560 -> 10240: 25.7 us against 16.8) leave a compute unit two of them
 // and its neighbour one.
 //
-// Measured: 1 x 2560 -> 10240 6.5 us, 16 x 5120 -> 2560 6.0 (a launch is 2.3),
-// 4 x 5120 -> 20480 16.4 (3.3 TB/s of weights).  A lane's step is some 110
+// Times here and below are of calls in a captured graph, replayed over matrices
+// that together exceed the last-level cache: 1 x 2560 -> 10240 6.5 us, 16 x 5120
+// -> 2560 6.1 (a launch is 2.3), 4 x 5120 -> 20480 16.4 (3.3 TB/s of weights), 64 x
+// 2560 -> 10240 16.9 (the weights widened again for each 16 rows).  A lane's step is some 110
 // VALU operations for 64 weights, 64 of them bringing weights into bf16.  Two
 // steps of loads in flight are no better (16 x 5120 -> 2560: 6.6), for their registers.
 #include <hip/hip_runtime.h>

@@ -4,6 +4,10 @@ linear recurrence (``gated_scan_fwd``, ``gated_scan_bwd``,
 product with 4-bit weights (``w4_matvec``).  Argument marshalling only, as in
 the package; definitions stand in include/ssm.h.
 
+``stream`` is where a call runs (default: the current stream of its tensors'
+device).  What the call allocates belongs to that stream; the tensors that are
+passed in are the caller's to keep until the stream is past the call.
+
 The descriptor of a call (shapes, strides, types, flags) and the workspace
 size it asks for are kept by exactly these values, so that a call that repeats
 a shape costs a lookup; pointers and values are never kept.
