@@ -13,7 +13,8 @@ LIB = os.path.join(HERE, "libssm.so")
 MARSHAL = os.path.join(HERE, "_marshal.so")
 SOURCES = ["ssm_abi.cpp", "scan_fwd.hip", "scan_bwd.hip", "ssd_fwd.hip", "ssd_bwd.hip", "update_fwd.hip",
            "conv_fwd.hip", "layer_abi.cpp", "gated_scan.hip", "rms_norm.hip", "w4_matvec.hip"]
-HEADERS = ["ssm_internal.h", "abi_checks.h", "column_sums.h", "w4_loads.h", os.path.join("..", "..", "include", "ssm.h")]
+HEADERS = ["ssm_internal.h", "layer_internal.h", "abi_checks.h", "column_sums.h", "w4_loads.h",
+           os.path.join("..", "..", "include", "ssm.h")]
 
 # Packed fp32 VALU ops are kept out of all device code.
 HIPCC_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared", "-Wall",

@@ -45,7 +45,7 @@
 #include <algorithm>
 
 #include "column_sums.h"
-#include "ssm_internal.h"
+#include "layer_internal.h"
 
 // A segment's pair comes out the same from every variant of a kernel: products
 // and sums are contracted where an fma is written, nowhere else.

@@ -9,7 +9,7 @@
 
 #include "../../include/ssm.h"
 #include "abi_checks.h"
-#include "ssm_internal.h"
+#include "layer_internal.h"
 
 using namespace ssm::abi;
 

@@ -22,7 +22,7 @@
 #include <algorithm>
 
 #include "column_sums.h"
-#include "ssm_internal.h"
+#include "layer_internal.h"
 
 namespace ssm {
 namespace {

@@ -42,7 +42,7 @@
 // steps of loads in flight are no better (16 x 5120 -> 2560: 6.6), for their registers.
 #include <hip/hip_runtime.h>
 
-#include "ssm_internal.h"
+#include "layer_internal.h"
 #include "w4_loads.h"
 
 namespace ssm {
