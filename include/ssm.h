@@ -74,7 +74,7 @@ typedef enum {
   SSM_BF16 = 1,
   SSM_F16 = 2, /* reserved */
   SSM_E4M3 = 3, /* 8-bit float, 4 exponent bits, largest 448, no infinities (norm output) */
-  SSM_I32 = 4,  /* sequence lengths (gated scan) */
+  SSM_I32 = 4,  /* sequence lengths (gated scan), starts and slots of packed sequences */
   SSM_U8 = 5    /* packed 4-bit weights and their zero points */
 } ssm_dtype;
 
@@ -106,6 +106,10 @@ typedef struct {
 #define SSM_HAS_ZERO 131072u   /* 4-bit weights: zero points                          */
 #define SSM_HAS_STATE_OUT 262144u /* gated decode: write the state to state_out       */
 #define SSM_NO_WAIT 524288u    /* gated scan: no workgroup waits for another          */
+#define SSM_HAS_STATES 1048576u /* packed sequences: a pool of states (or windows)    */
+#define SSM_HAS_STARTS 2097152u /* packed sequences: starts; without it each row is one */
+#define SSM_HAS_SRC 4194304u    /* packed sequences: the slot each starts from        */
+#define SSM_HAS_DST 8388608u    /* packed sequences, moves: the slot each ends in     */
 
 /* ------------------------------------------------------------------ scan */
 
@@ -672,6 +676,208 @@ typedef struct {
   void* y;
 } ssm_w4_ptrs;
 
+/* ------------------------------------------------------ packed sequences */
+
+/* Sequences of different lengths, packed row behind row without padding, each
+ * started from and ended in a slot of a pool that outlives the call: what a
+ * server keeps of a request is one window of the convolution and one state of
+ * the scan, of a size that never grows.  Common to ssm_causal_conv1d_packed
+ * and ssm_selective_scan_packed:
+ *   starts : (seqs + 1) I32 contiguous, if SSM_HAS_STARTS: sequence s is rows
+ *            [starts[s], starts[s+1]), ascending (empty sequences are allowed).
+ *            Rows in front of starts[0] and from starts[seqs] on belong to
+ *            none: nothing of them is used and their rows of y stay as they
+ *            are.  Without the flag every row is a sequence of one token
+ *            (seqs == tokens): the decode step
+ *   pool   : (slots, ...), if SSM_HAS_STATES; read and written
+ *   src    : (seqs) I32 contiguous, if SSM_HAS_SRC (default: slot s for
+ *            sequence s, seqs <= slots): the slot that the sequence starts from;
+ *            outside [0, slots) it starts from zeros.  Several sequences may
+ *            start from one slot (a shared prefix)
+ *   dst    : (seqs) I32 contiguous, if SSM_HAS_DST (default: src): the slot
+ *            that its end is written to, also where the sequence is empty;
+ *            outside [0, slots) the end is not kept
+ * A sequence may end in the slot it starts from.  Otherwise no slot that one
+ * sequence of a call ends in may be another's start or end: what such slots
+ * and sequences hold afterwards is not defined (nothing else is affected).
+ * starts, src and dst are read on the device and values that do not follow
+ * these rules never lead out of the tensors: starts are taken into [0, tokens],
+ * an end in front of its start is an empty sequence. */
+
+/* Causal depthwise convolution of packed sequences: ssm_causal_conv1d_fwd's
+ * definition for each, with the width - 1 inputs in front of the sequence taken
+ * from its window (the last row is the latest input) in place of zeros; its
+ * slot dst then holds the last width - 1 of window and sequence.
+ *   x       : (tokens, dim) io (F32 or BF16)    innermost stride 1
+ *   y       : (tokens, dim) io or F32           innermost stride 1
+ *   weight  : (dim, width) F32                  any strides
+ *   bias    : (dim) F32       if SSM_HAS_BIAS,  any stride
+ *   windows : (slots, width - 1, dim) io        if SSM_HAS_STATES, innermost stride 1
+ * Flags: SSM_HAS_BIAS, SSM_SILU, SSM_HAS_STARTS, SSM_HAS_STATES and, with it,
+ * SSM_HAS_SRC, SSM_HAS_DST.  1 <= width <= 8; width 1 has no window (pool).
+ * Limits (SSM_ERR_UNSUPPORTED otherwise): tokens < 2^30; 64 rows of x, y
+ * or windows span less than 1 GiB; (seqs + ceil(tokens/32)) ceil(dim/256) < 2^24. */
+typedef struct {
+  int64_t tokens, seqs, dim, width, slots;
+  uint32_t flags;
+  ssm_tensor_desc x, weight, bias, y, windows, starts, src, dst;
+} ssm_conv_packed_desc;
+
+typedef struct {
+  const void* x;
+  const float* weight;
+  const float* bias;     /* NULL unless SSM_HAS_BIAS   */
+  void* y;
+  void* windows;         /* NULL unless SSM_HAS_STATES */
+  const int32_t* starts; /* NULL unless SSM_HAS_STARTS */
+  const int32_t* src;    /* NULL unless SSM_HAS_SRC    */
+  const int32_t* dst;    /* NULL unless SSM_HAS_DST    */
+} ssm_conv_packed_ptrs;
+
+/* Selective scan of packed sequences (definition at the top of this file).
+ *   x, delta : (tokens, dim) io               innermost stride 1
+ *   z        : (tokens, dim) io               if SSM_HAS_Z, innermost stride 1
+ *   y        : (tokens, dim) io or F32        innermost stride 1
+ *   B, C     : (tokens, dstate) io            any strides
+ *   A        : (dim, dstate) F32              any strides (0 = shared)
+ *   D        : (dim) F32                      if SSM_HAS_D, any stride
+ *   delta_bias: (dim) F32                     if SSM_HAS_DELTA_BIAS, any stride
+ *   states   : (slots, dim, dstate) F32       if SSM_HAS_STATES; (dim, dstate) contiguous
+ * io is SSM_F32 or SSM_BF16.  Flags: SSM_HAS_Z, SSM_HAS_D, SSM_DISC_EULER,
+ * SSM_DELTA_SOFTPLUS, SSM_HAS_DELTA_BIAS, SSM_HAS_STARTS, SSM_HAS_STATES and,
+ * with it, SSM_HAS_SRC, SSM_HAS_DST.  dstate <= SSM_SCAN_MAX_DSTATE.
+ * (exp(delta A) - 1) / A keeps its relative accuracy for small delta A where io
+ * is F32; where it is BF16, so it does as long as delta A of 16 steps and the
+ * channels next to it stay below 1/8, and is off by 2^-23 / |A| at most
+ * otherwise.
+ * Workspace: ssm_selective_scan_packed_workspace_size bytes (may be 0), 256-byte
+ * aligned, contents undefined; calls that may overlap in time need workspaces
+ * of their own.
+ * Limits (SSM_ERR_UNSUPPORTED otherwise): tokens < 2^30; 64 rows of x,
+ * delta, z, y, B or C span less than 1 GiB; (seqs + 256) ceil(dim/64) < 2^24,
+ * dim dstate < 2^28. */
+typedef struct {
+  int64_t tokens, seqs, dim, dstate, slots;
+  uint32_t flags;
+  ssm_tensor_desc x, delta, A, B, C, D, z, y, delta_bias, states, starts, src, dst;
+} ssm_scan_packed_desc;
+
+typedef struct {
+  const void* x;
+  const void* delta;
+  const float* A;
+  const void* B;
+  const void* C;
+  const float* D;          /* NULL unless SSM_HAS_D          */
+  const void* z;           /* NULL unless SSM_HAS_Z          */
+  void* y;
+  const float* delta_bias; /* NULL unless SSM_HAS_DELTA_BIAS */
+  float* states;           /* NULL unless SSM_HAS_STATES     */
+  const int32_t* starts;   /* NULL unless SSM_HAS_STARTS     */
+  const int32_t* src;      /* NULL unless SSM_HAS_SRC        */
+  const int32_t* dst;      /* NULL unless SSM_HAS_DST        */
+} ssm_scan_packed_ptrs;
+
+/* --------------------------------------------------------- conv backward */
+
+/* Backward of ssm_causal_conv1d_fwd: with a[b,t,d] the convolution's output in
+ * front of the SiLU (recomputed) and dy = dLoss/dy,
+ *      g[b,t,d]     = dy[b,t,d] silu'(a[b,t,d])   (dy without SSM_SILU)
+ *      dx[b,t,d]    = sum_k weight[d,k] g[b, t+width-1-k, d]   (g = 0 past the end)
+ *      dweight[d,k] = sum_{b,t} g[b,t,d] x[b, t-width+1+k, d],   dbias[d] = sum_{b,t} g[b,t,d]
+ *   x       : (batch, seqlen, dim) io (F32 or BF16)   innermost stride 1
+ *   dy, dx  : (batch, seqlen, dim) io or F32          innermost stride 1
+ *   weight  : (dim, width) F32                        any strides
+ *   bias    : (dim) F32         if SSM_HAS_BIAS,      any stride
+ *   dweight : (dim, width) F32 contiguous
+ *   dbias   : (dim) F32 contiguous                    if SSM_HAS_BIAS
+ * Flags: SSM_HAS_BIAS, SSM_SILU.  1 <= width <= 8.  The sums are fp32 partial
+ * sums added in a fixed order (deterministic).  Outputs may not overlap inputs
+ * or each other.  Workspace: ssm_causal_conv1d_bwd_workspace_size bytes, 256-byte
+ * aligned.  Limits (SSM_ERR_UNSUPPORTED otherwise): 128 rows of x, dy or dx span
+ * less than 1 GiB; batch ceil(seqlen/64) ceil(dim/64) < 2^24; dim < 2^28. */
+typedef struct {
+  int64_t batch, seqlen, dim, width;
+  uint32_t flags;
+  ssm_tensor_desc dy, x, weight, bias, dx, dweight, dbias;
+} ssm_conv_bwd_desc;
+
+typedef struct {
+  const void* dy;
+  const void* x;
+  const float* weight;
+  const float* bias; /* NULL unless SSM_HAS_BIAS */
+  void* dx;
+  float* dweight;
+  float* dbias;      /* NULL unless SSM_HAS_BIAS */
+} ssm_conv_bwd_ptrs;
+
+/* -------------------------------------------------------- beam selection */
+
+/* One selection of a beam search: of every batch element's beams x vocab
+ * continuations the k of the highest score,
+ *      s[n,v] = scores[n] + logits[n,v] - log(sum_w exp(logits[n,w])),
+ * in falling order, the lower index n vocab + v first where scores are equal.
+ * A beam's own continuations are ordered by their logits; the normaliser is an
+ * fp32 sum, scores are formed and compared in fp64 and rounded to fp32 once.
+ * Banned tokens have the logit -inf.  A beam whose score or normaliser is not a
+ * finite number (all tokens banned, a NaN or +inf among the logits, a score of
+ * -inf for a beam that is not in use) scores -inf throughout; continuations of
+ * -inf are chosen only where nothing else is left, by their index.
+ *   logits     : (batch, beams, vocab) F32 or BF16   innermost stride 1
+ *   scores     : (batch, beams) F32                  any strides
+ *   out_scores : (batch, k) F32 contiguous
+ *   tokens     : (batch, k) I32 contiguous           v of the chosen
+ *   parents    : (batch, k) I32 contiguous           n of the chosen
+ * k <= SSM_BEAM_MAX_K, k <= beams vocab.  beams 1 and scores 0: the k most
+ * likely tokens.  Workspace: ssm_beam_select_workspace_size bytes, 256-byte
+ * aligned.  Limits (SSM_ERR_UNSUPPORTED otherwise): beams vocab < 2^31,
+ * batch beams ceil(vocab/4096) < 2^24, batch < 2^24,
+ * beams <= 1024, beams ceil(vocab/4096) <= 4096.  Outputs may not overlap
+ * inputs or each other. */
+#define SSM_BEAM_MAX_K 64
+
+typedef struct {
+  int64_t batch, beams, vocab, k;
+  uint32_t flags;
+  ssm_tensor_desc logits, scores, out_scores, tokens, parents;
+} ssm_beam_desc;
+
+typedef struct {
+  const void* logits;
+  const float* scores;
+  float* out_scores;
+  int32_t* tokens;
+  int32_t* parents;
+} ssm_beam_ptrs;
+
+/* ------------------------------------------------------------ slot moves */
+
+/* Moves between the slots of a pool, in place and all at once: for every i
+ *      pool[dst[i]] <- what pool[src[i]] held before the call.
+ * This forks (one src, several dst), reorders (a permutation, or the parents
+ * of a beam search), compacts and frees: a negative src clears the slot.  A src
+ * >= slots, a dst outside [0, slots), and src == dst move nothing (and cost no
+ * traffic).  Where one slot is the dst of two moves, one of them wins in each
+ * element.
+ *   pool : (slots, row) F32 or BF16   innermost stride 1
+ *   src  : (moves) I32 contiguous
+ *   dst  : (moves) I32 contiguous     if SSM_HAS_DST (default: dst[i] = i, moves <= slots)
+ * moves <= SSM_MOVE_MAX_MOVES, row < 2^27 (SSM_ERR_UNSUPPORTED otherwise). */
+#define SSM_MOVE_MAX_MOVES 2048
+
+typedef struct {
+  int64_t slots, row, moves;
+  uint32_t flags;
+  ssm_tensor_desc pool, src, dst;
+} ssm_move_desc;
+
+typedef struct {
+  void* pool;
+  const int32_t* src;
+  const int32_t* dst; /* NULL unless SSM_HAS_DST */
+} ssm_move_ptrs;
+
 /* --------------------------------------------------------------- entries */
 
 /* SSM_ABI_VERSION of the library that is loaded. */
@@ -794,6 +1000,28 @@ ssm_status ssm_rms_norm_bwd(const ssm_norm_bwd_desc* d, const ssm_norm_bwd_ptrs*
 
 /* Rows times 4-bit weights (definition above ssm_w4_desc).  No workspace. */
 ssm_status ssm_w4_matvec(const ssm_w4_desc* d, const ssm_w4_ptrs* p, void* hip_stream);
+
+/* Causal convolution of packed sequences (definition above
+ * ssm_conv_packed_desc).  No workspace. */
+ssm_status ssm_causal_conv1d_packed(const ssm_conv_packed_desc* d, const ssm_conv_packed_ptrs* p, void* hip_stream);
+
+/* Backward of the causal convolution (definition above ssm_conv_bwd_desc). */
+ssm_status ssm_causal_conv1d_bwd_workspace_size(const ssm_conv_bwd_desc* d, size_t* bytes);
+ssm_status ssm_causal_conv1d_bwd(const ssm_conv_bwd_desc* d, const ssm_conv_bwd_ptrs* p, void* workspace,
+                                 size_t workspace_bytes, void* hip_stream);
+
+/* Selective scan of packed sequences (definition above ssm_scan_packed_desc). */
+ssm_status ssm_selective_scan_packed_workspace_size(const ssm_scan_packed_desc* d, size_t* bytes);
+ssm_status ssm_selective_scan_packed(const ssm_scan_packed_desc* d, const ssm_scan_packed_ptrs* p, void* workspace,
+                                     size_t workspace_bytes, void* hip_stream);
+
+/* Beam search's selection (definition above ssm_beam_desc). */
+ssm_status ssm_beam_select_workspace_size(const ssm_beam_desc* d, size_t* bytes);
+ssm_status ssm_beam_select(const ssm_beam_desc* d, const ssm_beam_ptrs* p, void* workspace, size_t workspace_bytes,
+                           void* hip_stream);
+
+/* Moves between a pool's slots (definition above ssm_move_desc).  No workspace. */
+ssm_status ssm_state_move(const ssm_move_desc* d, const ssm_move_ptrs* p, void* hip_stream);
 
 #ifdef __cplusplus
 }

@@ -25,6 +25,7 @@ SSM_DELTA_SOFTPLUS, SSM_HAS_DELTA_BIAS, SSM_HAS_BIAS, SSM_SILU = 32, 64, 128, 25
 SSM_WANT_CKPT, SSM_HAS_CKPT, SSM_HAS_SSD_FWD = 512, 1024, 2048
 SSM_HAS_BIAS_A, SSM_HAS_BIAS_X, SSM_HAS_LENS, SSM_HAS_DHLAST = 4096, 8192, 16384, 32768
 SSM_HAS_RESIDUAL, SSM_HAS_ZERO, SSM_HAS_STATE_OUT, SSM_NO_WAIT = 65536, 131072, 262144, 524288
+SSM_HAS_STATES, SSM_HAS_STARTS, SSM_HAS_SRC, SSM_HAS_DST = 1 << 20, 1 << 21, 1 << 22, 1 << 23
 ABI_VERSION = 5
 MAX_DIMS = 5
 
@@ -36,7 +37,9 @@ EXPORTS = ("ssm_abi_version", "ssm_status_string", "ssm_last_hip_error", "ssm_se
            "ssm_ssd_bwd_workspace_size", "ssm_ssd_bwd", "ssm_selective_scan_fwd_noalloc",
            "ssm_gated_scan_workspace_size", "ssm_gated_scan_fwd", "ssm_gated_scan_bwd_workspace_size",
            "ssm_gated_scan_bwd", "ssm_gated_state_update", "ssm_rms_norm_fwd", "ssm_rms_norm_bwd_workspace_size",
-           "ssm_rms_norm_bwd", "ssm_w4_matvec")
+           "ssm_rms_norm_bwd", "ssm_w4_matvec", "ssm_causal_conv1d_packed", "ssm_causal_conv1d_bwd_workspace_size",
+           "ssm_causal_conv1d_bwd", "ssm_selective_scan_packed_workspace_size", "ssm_selective_scan_packed",
+           "ssm_beam_select_workspace_size", "ssm_beam_select", "ssm_state_move")
 
 
 class TensorDesc(ctypes.Structure):
@@ -61,6 +64,11 @@ _GATED_UPD_T = _GATED_IN + ("y", "state", "state_out")
 _NORM_T = ("x", "residual", "weight", "y", "residual_out", "scale")
 _NORM_BWD_T = ("dy", "row", "weight", "dres", "dx", "dweight")
 _W4_T = ("x", "weight", "scale", "zero", "bias", "y")
+_CONV_PACKED_T = ("x", "weight", "bias", "y", "windows", "starts", "src", "dst")
+_SCAN_PACKED_T = ("x", "delta", "A", "B", "C", "D", "z", "y", "delta_bias", "states", "starts", "src", "dst")
+_CONV_BWD_T = ("dy", "x", "weight", "bias", "dx", "dweight", "dbias")
+_BEAM_T = ("logits", "scores", "out_scores", "tokens", "parents")
+_MOVE_T = ("pool", "src", "dst")
 
 
 class ScanDesc(ctypes.Structure):
@@ -183,6 +191,48 @@ class W4Ptrs(ctypes.Structure):
     _fields_ = _pointers(_W4_T)
 
 
+class ConvPackedDesc(ctypes.Structure):
+    _fields_ = _sizes(("tokens", "seqs", "dim", "width", "slots")) + [("flags", ctypes.c_uint32)] + \
+        _descs(_CONV_PACKED_T)
+
+
+class ConvPackedPtrs(ctypes.Structure):
+    _fields_ = _pointers(_CONV_PACKED_T)
+
+
+class ScanPackedDesc(ctypes.Structure):
+    _fields_ = _sizes(("tokens", "seqs", "dim", "dstate", "slots")) + [("flags", ctypes.c_uint32)] + \
+        _descs(_SCAN_PACKED_T)
+
+
+class ScanPackedPtrs(ctypes.Structure):
+    _fields_ = _pointers(_SCAN_PACKED_T)
+
+
+class ConvBwdDesc(ctypes.Structure):
+    _fields_ = _sizes(("batch", "seqlen", "dim", "width")) + [("flags", ctypes.c_uint32)] + _descs(_CONV_BWD_T)
+
+
+class ConvBwdPtrs(ctypes.Structure):
+    _fields_ = _pointers(_CONV_BWD_T)
+
+
+class BeamDesc(ctypes.Structure):
+    _fields_ = _sizes(("batch", "beams", "vocab", "k")) + [("flags", ctypes.c_uint32)] + _descs(_BEAM_T)
+
+
+class BeamPtrs(ctypes.Structure):
+    _fields_ = _pointers(_BEAM_T)
+
+
+class MoveDesc(ctypes.Structure):
+    _fields_ = _sizes(("slots", "row", "moves")) + [("flags", ctypes.c_uint32)] + _descs(_MOVE_T)
+
+
+class MovePtrs(ctypes.Structure):
+    _fields_ = _pointers(_MOVE_T)
+
+
 class SSMError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -223,11 +273,14 @@ def lib() -> ctypes.CDLL:
         L.ssm_ssd_bwd_workspace_size.argtypes = [P(SSDBwdDesc), P(sz)]
         L.ssm_ssd_bwd.argtypes = [P(SSDBwdDesc), P(SSDBwdPtrs), vp, sz, vp]
         # descriptors and pointer structs of these go by address (or as packed bytes)
-        for name in ("ssm_gated_scan", "ssm_gated_scan_bwd", "ssm_rms_norm_bwd"):
+        for name in ("ssm_gated_scan", "ssm_gated_scan_bwd", "ssm_rms_norm_bwd", "ssm_causal_conv1d_bwd",
+                     "ssm_selective_scan_packed", "ssm_beam_select"):
             getattr(L, name + "_workspace_size").argtypes = [vp, P(sz)]
-        for name in ("ssm_gated_scan_fwd", "ssm_gated_scan_bwd", "ssm_rms_norm_bwd"):
+        for name in ("ssm_gated_scan_fwd", "ssm_gated_scan_bwd", "ssm_rms_norm_bwd", "ssm_causal_conv1d_bwd",
+                     "ssm_selective_scan_packed", "ssm_beam_select"):
             getattr(L, name).argtypes = [vp, vp, vp, sz, vp]
-        for name in ("ssm_gated_state_update", "ssm_rms_norm_fwd", "ssm_w4_matvec"):
+        for name in ("ssm_gated_state_update", "ssm_rms_norm_fwd", "ssm_w4_matvec", "ssm_causal_conv1d_packed",
+                     "ssm_state_move"):
             getattr(L, name).argtypes = [vp, vp, vp]
         for name in EXPORTS[3:]:
             getattr(L, name).restype = ctypes.c_int
@@ -649,3 +702,5 @@ def ssd_bwd(dy, x, delta, A, B, C, chunk, D=None, h0=None, euler=False, dx_dtype
 
 from .layer import (GATED_CKPT_STEPS, NORM_MAX_DIM, W4_MAX_ROWS, gated_scan_bwd, gated_scan_ckpt,  # noqa: E402
                     gated_scan_fwd, gated_state_update, rms_norm, rms_norm_bwd, w4_matvec, w4_quantize)
+from .serve import (BEAM_MAX_K, MOVE_MAX_MOVES, beam_select, causal_conv1d_bwd, causal_conv1d_packed,  # noqa: E402
+                    selective_scan_packed, state_move)

@@ -12,8 +12,10 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libssm.so")
 MARSHAL = os.path.join(HERE, "_marshal.so")
 SOURCES = ["ssm_abi.cpp", "scan_fwd.hip", "scan_bwd.hip", "ssd_fwd.hip", "ssd_bwd.hip", "update_fwd.hip",
-           "conv_fwd.hip", "layer_abi.cpp", "gated_scan.hip", "rms_norm.hip", "w4_matvec.hip"]
+           "conv_fwd.hip", "layer_abi.cpp", "gated_scan.hip", "rms_norm.hip", "w4_matvec.hip",
+           "serve_abi.cpp", "conv_packed.hip", "conv_bwd.hip", "scan_packed.hip", "beam_select.hip", "state_move.hip"]
 HEADERS = ["ssm_internal.h", "layer_internal.h", "abi_checks.h", "column_sums.h", "w4_loads.h",
+           "layer_checks.h", "packed_pieces.h", "serve_internal.h", "serve_device.h",
            os.path.join("..", "..", "include", "ssm.h")]
 
 # Packed fp32 VALU ops are kept out of all device code.

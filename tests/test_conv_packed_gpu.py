@@ -1,0 +1,168 @@
+"""The convolution of packed sequences over a pool of windows, against the fp64
+definition sequence by sequence."""
+import pytest
+import torch
+
+import selective_state_space_60_amd as ssm
+import _serve_ref as ref
+from _gpu import banner
+from _layer_ref import check
+
+pytestmark = pytest.mark.gpu
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def make(seed, T, D, W, slots, dt, x_cols=None):
+    g = torch.Generator().manual_seed(seed)
+    n = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    x = n(T, x_cols or D).to(dt)[:, :D]
+    return x, n(D, W) / W ** 0.5, 0.1 * n(D), n(slots, max(W - 1, 1), D).to(dt)[:, :W - 1]
+
+
+def run(x, w, b, win, starts, src, dst, silu=True, y=None, **kw):
+    i32 = lambda v: None if v is None else torch.tensor(v, dtype=torch.int32).cuda()  # noqa: E731
+    gw = None if win is None else win.cuda()
+    out = ssm.causal_conv1d_packed(x.cuda(), w.cuda(), gw, starts=i32(starts), src=i32(src), dst=i32(dst),
+                                   bias=None if b is None else b.cuda(), silu=silu, y=y, **kw)
+    torch.cuda.synchronize()
+    return out, gw
+
+
+def compare(out, gw, x, w, b, win, starts, src, dst, silu=True):
+    W = w.shape[1]
+    slots = 0 if win is None else win.shape[0]
+    kept = None if win is None else win.clone()
+    for begin, end, f, t in ref.packed(starts, src, dst, slots, x.shape[0]):
+        y, mag, last = ref.conv(x[begin:end], w, b, silu, None if f is None else win[f])
+        if end > begin:
+            check(out[begin:end], y, mag, ref.rel_conv(W, mag), "rows %d:%d" % (begin, end))
+        if t is not None and W > 1:
+            kept[t] = last.to(kept.dtype)
+    if kept is not None:
+        assert torch.equal(gw.cpu(), kept)
+
+
+# sequences shorter than the window, as long as it, ending at, before and behind the 32-row lines, empty ones
+STARTS = [0, 1, 3, 3, 6, 31, 32, 33, 64, 66, 66, 131, 132, 134, 260]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D,W", [(64, 4), (1028, 4), (37, 4), (260, 2), (129, 8), (64, 8), (5, 3), (12, 5), (40, 6),
+                                 (36, 7)])
+def test_ragged(dtype, D, W):
+    banner("packed conv D %d W %d %s" % (D, W, dtype))
+    S = len(STARTS) - 1
+    x, w, b, win = make(D + W, STARTS[-1], D, W, 2 * S + 1, TYPES[dtype])
+    src = [(7 * s) % S if s % 3 else -1 for s in range(S)]
+    src[4] = 2 * S + 9  # outside the pool
+    src[5] = src[7]     # a shared window
+    dst = [S + s for s in range(S)]
+    dst[6] = -3
+    out, gw = run(x, w, b, win, STARTS, src, dst)
+    compare(out, gw, x, w, b, win, STARTS, src, dst)
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("f32", 33)])
+def test_in_place(dtype, D):
+    """Each sequence ends in the slot that it starts from: by default, and named."""
+    S = len(STARTS) - 1
+    x, w, b, win = make(3, STARTS[-1], D, 4, S, TYPES[dtype])
+    for src in (None, [S - 1 - s for s in range(S)]):
+        out, gw = run(x, w, b, win, STARTS, src, None, silu=False)
+        compare(out, gw, x, w, b, win, STARTS, src, None, silu=False)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("S,D,W", [(1, 16, 4), (64, 1028, 4), (5, 7, 2), (33, 260, 8), (3, 1024, 3)])
+def test_single_tokens(dtype, S, D, W):
+    banner("packed conv tokens S %d D %d W %d" % (S, D, W))
+    x, w, b, win = make(S + D, S, D, W, S + 2, TYPES[dtype])
+    src = [s + 2 for s in range(S)]
+    src[0] = -1
+    for s, d in ((None, None), (src, None), (src, [(s + 3) % (S + 2) if s % 2 else -1 for s in range(S)])):
+        if d is not None:  # what one ends in no other may start from
+            s = [v if v not in d else -1 for v in s]
+        out, gw = run(x, w, b, win, None, s, d)
+        compare(out, gw, x, w, b, win, None, s, d)
+
+
+def test_step_by_step_is_the_whole():
+    """A sequence in parts of any length, down to single tokens, gives the bits of the whole."""
+    D, W = 72, 4
+    x, w, b, win = make(11, 150, D, W, 2, torch.bfloat16)
+    whole, _ = run(x, w, b, None, [0, 150], None, None)
+    pool = torch.full((2, W - 1, D), 5.0).to(torch.bfloat16).cuda()
+    parts, at, first = [], 0, True
+    for n in (1, 1, 2, 3, 40, 1, 64, 1, 37):
+        i = lambda v: torch.tensor(v, dtype=torch.int32).cuda()  # noqa: E731
+        starts = None if n == 1 else i([0, n])
+        parts.append(ssm.causal_conv1d_packed(x[at:at + n].cuda(), w.cuda(), pool, starts=starts,
+                                              src=i([-1 if first else 1]), dst=i([1]), bias=b.cuda(), silu=True))
+        at, first = at + n, False
+    assert at == 150 and torch.equal(torch.cat(parts), whole)
+    assert torch.equal(pool[1].cpu(), x[-3:]) and bool((pool[0] == 5).all())
+
+
+def test_rows_outside_stay():
+    """Rows in front of the first and behind the last sequence: not read, their y untouched."""
+    D = 48
+    x, w, b, win = make(2, 100, D, 4, 3, torch.bfloat16)
+    x = x.clone()
+    x[:5], x[70:] = float("nan"), float("inf")
+    starts, src, dst = [5, 40, 70], [-1, 2], [0, 1]
+    y = torch.full((100, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    out, gw = run(x, w, b, win, starts, src, dst, y=y)
+    compare(out, gw, x, w, b, win, starts, src, dst)
+    assert bool((y[:5] == 7).all()) and bool((y[70:] == 7).all())
+
+
+def test_starts_out_of_order_stay_inside():
+    """Starts that break the rules: nothing outside y and the pool changes, and no access leaves the tensors."""
+    D = 32
+    x, w, b, win = make(4, 64, D, 4, 4, torch.float32)
+    buf = torch.full((96, D), 3.0, device="cuda")
+    run(x, w, b, win, [40, 10, -5, 2 ** 30, 64], [0, 1, 2, 3], None, y=buf[16:80])
+    assert bool((buf[:16] == 3).all()) and bool((buf[80:] == 3).all())
+
+
+def test_strides_types_and_none():
+    """x and y as columns of wider rows, a pool inside a larger one, transposed weights, fp32 output, no bias."""
+    D, W, S = 40, 4, 3
+    g = torch.Generator().manual_seed(8)
+    wide = torch.randn(90, 3 * D + 1, generator=g).to(torch.bfloat16)
+    x = wide[:, D + 1:2 * D + 1]
+    w = torch.randn(W, D, generator=g).t()
+    pool = torch.randn(S, 2, W - 1, D, generator=g).to(torch.bfloat16)
+    starts = [0, 2, 50, 90]
+    gp = pool.cuda()
+    y = torch.zeros(90, 2 * D, device="cuda")
+    ssm.causal_conv1d_packed(wide.cuda()[:, D + 1:2 * D + 1], w.cuda(), gp[:, 1], silu=False, y=y[:, D:],
+                             starts=torch.tensor(starts, dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    compare(y[:, D:], gp[:, 1], x, w, None, pool[:, 1], starts, None, None, silu=False)
+    assert torch.equal(gp[:, 0].cpu(), pool[:, 0]) and bool((y[:, :D] == 0).all())
+
+
+def test_width_one():
+    x, w, b, _ = make(9, 70, 20, 1, 1, torch.float32)
+    out, _ = run(x, w, b, None, [0, 33, 70], None, None)
+    compare(out, None, x, w, b, None, [0, 33, 70], None, None)
+
+
+def test_far_rows():
+    """Rows and slots past 2^32 bytes."""
+    banner("packed conv far rows")
+    D, T, st, slot = 8, 600, 4_000_000, 1_500_000_000
+    x, w, b, win = make(5, T, D, 4, 3, torch.bfloat16)
+    big = torch.empty(T * st, dtype=torch.bfloat16, device="cuda")
+    gx = big.as_strided((T, D), (st, 1))
+    gx.copy_(x)
+    pool = torch.empty(2 * slot + 64, dtype=torch.bfloat16, device="cuda").as_strided((3, 3, D), (slot, D, 1))
+    pool.copy_(win)
+    starts, src, dst = [0, 290, 600], [2, -1], [1, 2]
+    i = lambda v: torch.tensor(v, dtype=torch.int32).cuda()  # noqa: E731
+    src = [0, 2]
+    dst = [1, 2]
+    out = ssm.causal_conv1d_packed(gx, w.cuda(), pool, starts=i(starts), src=i(src), dst=i(dst), bias=b.cuda(), silu=True)
+    torch.cuda.synchronize()
+    compare(out, pool, x, w, b, win, starts, src, dst)
