@@ -746,10 +746,11 @@ typedef struct {
  * io is SSM_F32 or SSM_BF16.  Flags: SSM_HAS_Z, SSM_HAS_D, SSM_DISC_EULER,
  * SSM_DELTA_SOFTPLUS, SSM_HAS_DELTA_BIAS, SSM_HAS_STARTS, SSM_HAS_STATES and,
  * with it, SSM_HAS_SRC, SSM_HAS_DST.  dstate <= SSM_SCAN_MAX_DSTATE.
- * (exp(delta A) - 1) / A keeps its relative accuracy for small delta A where io
- * is F32; where it is BF16, so it does as long as delta A of 16 steps and the
- * channels next to it stay below 1/8, and is off by 2^-23 / |A| at most
- * otherwise.
+ * (exp(delta A) - 1) / A keeps its relative accuracy for single tokens, and for
+ * sequences as long as |delta A| of 16 steps and 16 neighbouring channels stays
+ * below 1/8 or an A among these channels is 0; elsewhere an input's part is off by
+ * a few 2^-24 |B x / A|.  y of a sequence that is walked in pieces is off by up to
+ * 2^-16 (BF16 y) or 2^-20 (F32) of sum |C h| besides; the states are not.
  * Workspace: ssm_selective_scan_packed_workspace_size bytes (may be 0), 256-byte
  * aligned, contents undefined; calls that may overlap in time need workspaces
  * of their own.

@@ -21,18 +21,24 @@
 //
 // Pieces (packed_pieces.h).  A sequence is cut at grid lines, so that a long one
 // does not walk alone.  The first pass walks every piece, the later ones of a
-// sequence from zeros, and keeps each piece's end state and sum of delta.  The
-// second pass walks the later pieces again from their true states -- chained
-// from the kept ones by each wave for itself -- next to a twin from zeros, and
-// stops at the end of the tile where every state equals its twin bit for bit:
-// what follows is what the first pass wrote.  States that decay are walked again
-// over a short stretch only.
+// sequence from zeros, and keeps each piece's end state and sum of delta; true end
+// states follow from those without another walk.  The second pass corrects y: it
+// walks a later piece again from its true state -- chained from the kept ones by
+// each wave for itself -- and carries along what is left of that state, its product
+// with the decays so far, which is what the first pass's states lack.  It stops at
+// the end of the tile where that has come down to 2^-16 of every state where y is
+// bf16 (half a step is 2^-9), 2^-20 where it is fp32 (about what the arithmetic of
+// the walk is good for); it decays on from there.  States that decay are walked
+// again over a short stretch only.  (Walked on until the states equal the first
+// pass's bit for bit, the second pass of 16384 x 5120 in 24 sequences takes 126 us,
+// the slowest of a wave's 256 states counts; so 85 us.)
 //
 // Forms, chosen for each tile of a wave (delta A of its steps and channels):
 //   small   all |delta A| < 1/8: expm1(u)/u by its Taylor polynomial; right for A = 0
-//   fast    bf16 input, no A = 0: h <- Abar (h + q) - q, q = B x / A (the update
-//           multiplied out): 8 issue slots a state and step
-//   any     otherwise: (Abar - 1) / A, or the polynomial where |u| < 1/4
+//   fast    no A = 0: h <- Abar (h + q) - q, q = B x / A (the update multiplied
+//           out), 8 issue slots a state and step with the readout; a term is off
+//           by the roundings of q, so `small` takes the small steps
+//   any     otherwise: (Abar - 1) / A, or the polynomial where |delta A| < 1/4
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -61,14 +67,16 @@ __device__ __forceinline__ float other(float v) {
                                                            true));
 }
 
-// expm1(u) / u for |u| < 1/4 (through u^5; the next term is u^6 / 5040 < 5e-8).
-__device__ __forceinline__ float phi(float u) {
-  float q = 1.f / 720.f;
-  q = __builtin_fmaf(q, u, 1.f / 120.f);
-  q = __builtin_fmaf(q, u, 1.f / 24.f);
-  q = __builtin_fmaf(q, u, 1.f / 6.f);
-  q = __builtin_fmaf(q, u, 0.5f);
-  return __builtin_fmaf(q, u, 1.f);
+// (2^t - 1) / t for |t| < 1/4 log2(e): the Taylor series of expm1(u) / u, u = t ln 2,
+// times ln 2, through u^5 (the next term is u^6 / 5040 < 5e-8).
+__device__ __forceinline__ float ratio(float t) {
+  constexpr float l1 = kLn2, l2 = l1 * kLn2, l3 = l2 * kLn2, l4 = l3 * kLn2, l5 = l4 * kLn2, l6 = l5 * kLn2;
+  float q = l6 / 720.f;
+  q = __builtin_fmaf(q, t, l5 / 120.f);
+  q = __builtin_fmaf(q, t, l4 / 24.f);
+  q = __builtin_fmaf(q, t, l3 / 6.f);
+  q = __builtin_fmaf(q, t, l2 / 2.f);
+  return __builtin_fmaf(q, t, l1);
 }
 
 enum Form : int { kSmall = 0, kFast = 1, kAny = 2, kEuler = 3 };
@@ -76,67 +84,73 @@ enum Form : int { kSmall = 0, kFast = 1, kAny = 2, kEuler = 3 };
 // A lane's constants of its states.
 template <int NS>
 struct Lane {
-  float A[NS], A2[NS], iA[NS];  // A, A log2(e), 1/A (0 where A is 0)
+  float A[NS], iA[NS];  // A, 1/A (0 where A is 0)
 };
 
-// The state, its input and its decay of one step: h <- the next state; with a
-// twin, it takes the same factors through the same operations.  No implicit
-// fusing: the broadcast multiplies have to stay multiplies (an fma takes no DPP).
-template <int NS, int FORM, bool TWIN, int J>
-__device__ __forceinline__ float step(float (&h)[NS], float (&h2)[NS], const Lane<NS>& ln, float dt, float x,
-                                      const float (&B)[NS], const float (&C)[NS]) {
+// One step of a lane's states; returns its part of the readout.  dt: delta
+// log2(e); x: x, or delta x (kEuler).  AGAIN (the second pass): `old`, what is
+// left of the states that the piece started from, decays along.  No implicit fusing: the broadcast multiplies have
+// to stay multiplies (an fma takes no DPP), and side by side (the compiler looks
+// for a broadcast's uses over some twenty instructions only).
+template <int NS, int FORM, bool AGAIN, int J>
+__device__ __forceinline__ float step(float (&h)[NS], float (&old)[NS], const Lane<NS>& ln, float dt, float x,
+                                      const float* bc) {
 #pragma clang fp contract(off)
-  float yp = 0.f;
+  constexpr int NP = 4 * NS;
+  float t[NS], q[NS], B[NS], yp = 0.f;
+#pragma unroll
+  for (int k = 0; k < NS; ++k) t[k] = quad<J>(dt) * ln.A[k];
+#pragma unroll
+  for (int k = 0; k < NS; ++k) B[k] = bc[2 * J * NP + k];
+#pragma unroll
+  for (int k = 0; k < NS; ++k) q[k] = quad<J>(x) * (FORM == kFast ? ln.iA[k] : B[k]);
 #pragma unroll
   for (int k = 0; k < NS; ++k) {
     if constexpr (FORM == kFast) {
-      const float Ab = __builtin_amdgcn_exp2f(quad<J>(dt) * ln.A2[k]);
-      const float q = (quad<J>(x) * ln.iA[k]) * B[k];
-      h[k] = __builtin_fmaf(Ab, h[k] + q, -q);
-      if constexpr (TWIN) h2[k] = __builtin_fmaf(Ab, h2[k] + q, -q);
-    } else if constexpr (FORM == kEuler) {
-      const float Ab = __builtin_amdgcn_exp2f(quad<J>(dt) * ln.A2[k]);
-      const float q = quad<J>(x) * B[k];  // x is delta x here
-      h[k] = __builtin_fmaf(Ab, h[k], q);
-      if constexpr (TWIN) h2[k] = __builtin_fmaf(Ab, h2[k], q);
+      // (as h + (Ab - 1)(h + q) a state that a large delta wipes out would leave its rounding behind)
+      const float Ab = __builtin_amdgcn_exp2f(t[k]);
+      q[k] *= B[k];
+      h[k] = __builtin_fmaf(Ab, h[k] + q[k], -q[k]);
+      if constexpr (AGAIN) old[k] *= Ab;
     } else {
-      const float u = quad<J>(dt) * ln.A[k];
-      float c = quad<J>(dt) * phi(u), Ab;
-      if constexpr (FORM == kSmall) {
-        Ab = __builtin_fmaf(c, ln.A[k], 1.f);
+      float Ab;
+      if constexpr (FORM == kEuler) {
+        Ab = __builtin_amdgcn_exp2f(t[k]);
       } else {
-        Ab = __builtin_amdgcn_exp2f(quad<J>(dt) * ln.A2[k]);
-        const float far = (Ab - 1.f) * ln.iA[k];
-        c = fabsf(u) < 0.25f ? c : far;
+        const float r = ratio(t[k]);
+        float c = quad<J>(dt) * r;  // expm1(delta A) / A
+        if constexpr (FORM == kSmall) {
+          Ab = __builtin_fmaf(t[k], r, 1.f);
+        } else {
+          Ab = __builtin_amdgcn_exp2f(t[k]);
+          const float far = (Ab - 1.f) * ln.iA[k];
+          c = fabsf(t[k]) < 0.25f * kLog2e ? c : far;
+        }
+        q[k] *= c;
       }
-      const float q = c * (quad<J>(x) * B[k]);
-      h[k] = __builtin_fmaf(Ab, h[k], q);
-      if constexpr (TWIN) h2[k] = __builtin_fmaf(Ab, h2[k], q);
+      h[k] = __builtin_fmaf(Ab, h[k], q[k]);
+      if constexpr (AGAIN) old[k] *= Ab;
     }
-    yp = k == 0 ? C[k] * h[k] : __builtin_fmaf(C[k], h[k], yp);
+  }
+#pragma unroll
+  for (int k = 0; k < NS; ++k) {
+    const float C = bc[(2 * J + 1) * NP + k];
+    yp = k == 0 ? C * h[k] : __builtin_fmaf(C, h[k], yp);
   }
   return yp;
 }
 
 // Steps 4i .. 4i+3 of a tile; returns the readout of step 4i + (lane % 4).
 // bc: the tile's B and C in LDS from this lane's first state on.
-template <int NS, int FORM, bool TWIN>
-__device__ __forceinline__ float four_steps(float (&h)[NS], float (&h2)[NS], const Lane<NS>& ln, float dt, float x,
+template <int NS, int FORM, bool AGAIN>
+__device__ __forceinline__ float four_steps(float (&h)[NS], float (&old)[NS], const Lane<NS>& ln, float dt, float x,
                                             const float* bc) {
-  constexpr int NP = 4 * NS;
-  float B[4][NS], C[4][NS];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-#pragma unroll
-    for (int k = 0; k < NS; ++k) {
-      B[j][k] = bc[(2 * j) * NP + k];
-      C[j][k] = bc[(2 * j + 1) * NP + k];
-    }
-  }
-  const float y0 = step<NS, FORM, TWIN, 0>(h, h2, ln, dt, x, B[0], C[0]);
-  const float y1 = step<NS, FORM, TWIN, 1>(h, h2, ln, dt, x, B[1], C[1]);
-  const float y2 = step<NS, FORM, TWIN, 2>(h, h2, ln, dt, x, B[2], C[2]);
-  const float y3 = step<NS, FORM, TWIN, 3>(h, h2, ln, dt, x, B[3], C[3]);
+  // operands of later steps are not read ahead of these: that costs registers
+  __builtin_amdgcn_sched_barrier(0);
+  const float y0 = step<NS, FORM, AGAIN, 0>(h, old, ln, dt, x, bc);
+  const float y1 = step<NS, FORM, AGAIN, 1>(h, old, ln, dt, x, bc);
+  const float y2 = step<NS, FORM, AGAIN, 2>(h, old, ln, dt, x, bc);
+  const float y3 = step<NS, FORM, AGAIN, 3>(h, old, ln, dt, x, bc);
   // lane j: the sum of step j over the four lanes, by exchanging what the other needs
   const bool odd = threadIdx.x & 1, up = threadIdx.x & 2;
   const float a = (odd ? y1 : y0) + other<1>(odd ? y0 : y1);
@@ -165,64 +179,133 @@ __device__ __forceinline__ uint32_t load_raw(__amdgpu_buffer_rsrc_t r, uint32_t 
   else return __builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0);
 }
 
+// One stream of a wave: the address of the current tile's first row at the wave's
+// first channel (or state), the bytes of four rows, and this lane's place in a tile.
+// That place is fixed and the rows 4i are scalar offsets, so a whole tile's loads
+// and stores cost no vector arithmetic, and the walk few scalar registers.  What
+// does not exist -- channels, states, rows behind the piece -- goes out of range by
+// the lane's offset.
+struct Stream {
+  const char* at;
+  uint32_t four;
+  uint32_t off;
+
+  __device__ __forceinline__ void set(const void* base, int64_t st, int row, int64_t first, int e, uint32_t lane_off) {
+    at = (const char*)base + ((int64_t)row * st + first) * e;
+    four = 4 * (uint32_t)st * (uint32_t)e;
+    off = lane_off;
+  }
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer() const { return rsrc(at, kFar); }
+  __device__ __forceinline__ void advance() { at += 4 * (int64_t)four; }
+};
+
 // A wave's streams over one piece.
 template <bool BF16, int NS, bool VEC>
 struct Streams {
   static constexpr int E = BF16 ? 2 : 4;
   using T = Tile<BF16, NS, VEC>;
-  const ScanPackedParams& p;
-  int64_t d0;     // first channel of the wave
-  uint32_t lch;   // this lane's channel within the wave's
-  bool ch_ok;
-  int j, r, n0;   // lane % 4, lane / 4, first state
-  int end;        // of the piece
+  Stream x, dt, z, y, B, C;
+  uint32_t nB, nC;   // bytes from state to state
+  int j, r, kn;      // lane % 4, lane / 4, states of the lane that exist
+  bool has_z, y_f32;
 
-  // Rows t .. t + left - 1 from the wave's first channel on.
-  __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows(const void* base, int64_t st, int t, int left) const {
-    return rsrc((const char*)base + ((int64_t)t * st + d0) * E, row_range(left, st, p.D - d0, E));
+  __device__ __forceinline__ Streams(const ScanPackedParams& p, int64_t d0, int lane, int t)
+      : j(lane % 4), r(lane / 4), has_z(p.z != nullptr), y_f32(p.y_f32) {
+    const int64_t ch = lane / 4, n0 = NS * j;
+    const bool ok = d0 + ch < p.D, in = n0 < p.N;
+    kn = in ? (int)(p.N - n0) : 0;
+    auto place = [&](int64_t st, uint32_t e) { return ok ? ((uint32_t)j * (uint32_t)st + (uint32_t)ch) * e : kFar; };
+    auto states = [&](int64_t st, int64_t sn) {
+      return in ? ((uint32_t)r * (uint32_t)st + (uint32_t)n0 * (uint32_t)sn) * E : kFar;
+    };
+    x.set(p.x, p.xs_t, t, d0, E, place(p.xs_t, E));
+    dt.set(p.delta, p.ds_t, t, d0, E, place(p.ds_t, E));
+    z.set(has_z ? p.z : p.x, p.zs_t, t, d0, E, place(p.zs_t, E));
+    const int ye = 2 << p.y_f32;  // y_f32 is 0 or 1 (a select would move the address to vector registers)
+    y.set(p.y, p.ys_t, t, d0, ye, place(p.ys_t, (uint32_t)ye));
+    B.set(p.B, p.Bs_t, t, 0, E, states(p.Bs_t, p.Bs_n));
+    C.set(p.C, p.Cs_t, t, 0, E, states(p.Cs_t, p.Cs_n));
+    nB = (uint32_t)p.Bs_n * E;
+    nC = (uint32_t)p.Cs_n * E;
   }
 
-  // The tile at row t; rows past the piece and channels and states that do not exist read zeros.
-  __device__ __forceinline__ void load(int t, T& o) const {
-    const int left = end - t < kTile ? end - t : kTile;
-    const auto rx = rows(p.x, p.xs_t, t, left), rd = rows(p.delta, p.ds_t, t, left);
-    const auto rz = rows(p.z ? p.z : p.x, p.zs_t, t, p.z ? left : 0);
+  template <bool FULL>
+  __device__ __forceinline__ void load_rows(const Stream& s, int left, uint32_t (&v)[4]) const {
+    const auto b = s.buffer();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int row = 4 * i + j;
-      const bool ok = ch_ok && row < left;
-      o.x[i] = load_raw<BF16>(rx, ok ? ((uint32_t)row * (uint32_t)p.xs_t + lch) * E : kFar);
-      o.dt[i] = load_raw<BF16>(rd, ok ? ((uint32_t)row * (uint32_t)p.ds_t + lch) * E : kFar);
-      o.z[i] = load_raw<BF16>(rz, ok ? ((uint32_t)row * (uint32_t)p.zs_t + lch) * E : kFar);
+      const uint32_t off = FULL ? s.off : 4 * i + j < left ? s.off + i * s.four : kFar;
+      const int so = FULL ? (int)(i * s.four) : 0;
+      if constexpr (BF16) v[i] = __builtin_amdgcn_raw_buffer_load_b16(b, (int)off, so, 0);
+      else v[i] = __builtin_amdgcn_raw_buffer_load_b32(b, (int)off, so, 0);
     }
-    load_states(p.B, p.Bs_t, p.Bs_n, t, left, o.B);
-    load_states(p.C, p.Cs_t, p.Cs_n, t, left, o.C);
   }
 
-  __device__ __forceinline__ void load_states(const void* base, int64_t st, int64_t sn, int t, int left,
-                                              uint32_t (&o)[T::kWords]) const {
-    const auto rb = rsrc((const char*)base + (int64_t)t * st * E, row_range(left, st, (p.N - 1) * sn + 1, E));
-    const uint32_t row = (uint32_t)r * (uint32_t)st;
+  // Row r of B or C.
+  __device__ __forceinline__ void load_states(const Stream& s, uint32_t sn, uint32_t off, uint32_t (&o)[T::kWords]) const {
+    const auto b = s.buffer();
     if constexpr (VEC) {  // this lane's NS states lie side by side, all in or all out
-      const uint32_t off = r < left && n0 < p.N ? (row + (uint32_t)n0) * E : kFar;
       if constexpr (T::kWords == 1) {
-        if constexpr (BF16 && NS == 1) o[0] = load_raw<true>(rb, off);
-        else o[0] = __builtin_amdgcn_raw_buffer_load_b32(rb, (int)off, 0, 0);
+        if constexpr (BF16 && NS == 1) o[0] = load_raw<true>(b, off);
+        else o[0] = __builtin_amdgcn_raw_buffer_load_b32(b, (int)off, 0, 0);
       } else if constexpr (T::kWords == 2) {
-        const auto v = __builtin_amdgcn_raw_buffer_load_b64(rb, (int)off, 0, 0);
+        const auto v = __builtin_amdgcn_raw_buffer_load_b64(b, (int)off, 0, 0);
         o[0] = v[0]; o[1] = v[1];
       } else {
 #pragma unroll
         for (int i = 0; i < T::kWords / 4; ++i) {
-          const auto v = __builtin_amdgcn_raw_buffer_load_b128(rb, (int)(off + 16u * i), 0, 0);
+          const auto v = __builtin_amdgcn_raw_buffer_load_b128(b, (int)(off + 16u * i), 0, 0);
           o[4 * i] = v[0]; o[4 * i + 1] = v[1]; o[4 * i + 2] = v[2]; o[4 * i + 3] = v[3];
         }
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < NS; ++k)
-        o[k] = load_raw<BF16>(rb, r < left && n0 + k < p.N ? (row + (uint32_t)(n0 + k) * (uint32_t)sn) * E : kFar);
+      for (int k = 0; k < NS; ++k) o[k] = load_raw<BF16>(b, k < kn ? off + (uint32_t)k * sn : kFar);
     }
+  }
+
+  template <bool FULL>
+  __device__ __forceinline__ void load_tile(int left, T& o) const {
+    load_rows<FULL>(x, left, o.x);
+    load_rows<FULL>(dt, left, o.dt);
+    if (has_z) load_rows<FULL>(z, left, o.z);
+    load_states(B, nB, FULL || r < left ? B.off : kFar, o.B);
+    load_states(C, nC, FULL || r < left ? C.off : kFar, o.C);
+  }
+
+  // The next tile, `left` of whose rows belong to the piece (<= 0: none); what does not exist reads zeros.
+  __device__ __forceinline__ void load(int left, T& o) {
+    if (left >= kTile) load_tile<true>(kTile, o);
+    else load_tile<false>(left, o);
+    x.advance();
+    dt.advance();
+    z.advance();
+    B.advance();
+    C.advance();
+  }
+
+  template <bool FULL, bool F32>
+  __device__ __forceinline__ void store_rows(int left, const float (&v)[4]) const {
+    const auto b = y.buffer();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t off = FULL ? y.off : 4 * i + j < left ? y.off + i * y.four : kFar;
+      const int so = FULL ? (int)(i * y.four) : 0;
+      if constexpr (F32) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[i]), b, (int)off, so, 0);
+      else __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (__bf16)v[i]), b, (int)off, so, 0);
+    }
+  }
+
+  // y of the next tile.
+  __device__ __forceinline__ void store(int left, const float (&v)[4]) {
+    if (left >= kTile) {
+      if (!BF16 || y_f32) store_rows<true, true>(left, v);
+      else store_rows<true, false>(left, v);
+    } else {
+      if (!BF16 || y_f32) store_rows<false, true>(left, v);
+      else store_rows<false, false>(left, v);
+    }
+    y.advance();
   }
 };
 
@@ -264,24 +347,49 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// One piece of one sequence for 16 channels.  TWIN: the second pass over a later
+// The state at grid line `line` of a sequence that crosses line `first` first:
+// from that line's state on, each piece's end state and the decay over the piece
+// applied to the state before it.  Four lines are asked for at a time.
+template <int NS>
+__device__ __forceinline__ void enter(const ScanPackedParams& p, const Lane<NS>& ln, int first, int line, int64_t own,
+                                      int64_t d, int nk, bool vec, float (&h)[NS]) {
+  const int64_t words = p.D * p.N;
+  load_block<NS>(p.H + (int64_t)(first - 1) * words + own, nk, vec, h);
+  for (int l0 = first + 1; l0 <= line; l0 += 4) {
+    float e[4][NS], sum[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t l = (l0 + i < line ? l0 + i : line) - 1;
+      load_block<NS>(p.H + l * words + own, nk, vec, e[i]);
+      sum[i] = p.dsum[l * p.D + d];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (l0 + i <= line)
+#pragma unroll
+        for (int k = 0; k < NS; ++k) h[k] = __builtin_fmaf(__builtin_amdgcn_exp2f(ln.A[k] * sum[i]), h[k], e[i][k]);
+  }
+}
+
+// One piece of one sequence for 16 channels.  AGAIN: the second pass over a later
 // piece (packed_pieces.h).
-template <bool BF16, int NS, bool EULER, bool TWIN, bool VEC>
-__global__ __launch_bounds__(64 * kWaves) void scan_packed_kernel(ScanPackedParams p, unsigned nblk, int vec_state) {
+template <bool BF16, int NS, bool EULER, bool AGAIN, bool VEC>
+__global__ __launch_bounds__(64 * kWaves, NS <= 4 ? 4 : NS == 8 ? 2 : 1) void scan_packed_kernel(ScanPackedParams p, unsigned nblk, int vec_state) {
   constexpr int NP = 4 * NS;
   __shared__ __align__(16) float lds[kWaves][2][kTile][2][NP];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
-  const int piece = (int)(blockIdx.x / nblk);
   const int64_t d0 = ((int64_t)(blockIdx.x % nblk) * kWaves + wave) * kCh;
   if (d0 >= p.D) return;
   // the piece: rows [begin, end) of sequence s; `line` > 0: from that grid line on
-  int s = piece, line = 0;
+  int piece = (int)(blockIdx.x / nblk);
+  if (!AGAIN && p.order) piece = p.order[piece];
+  int s = piece - p.lines, line = 0;
   packed::Run seq, run;
-  if (!TWIN && piece < p.q.seqs) {
+  if (!AGAIN && s >= 0) {
     seq = sequence_of(p.q, s);
     run = p.lines ? packed::first_piece(seq, p.step) : seq;
   } else {
-    line = TWIN ? piece + 1 : piece - p.q.seqs + 1;
+    line = piece + 1;
     s = find_sequence(p.q, line * p.step);
     if (s < 0) return;
     seq = sequence_of(p.q, s);
@@ -296,43 +404,33 @@ __global__ __launch_bounds__(64 * kWaves) void scan_packed_kernel(ScanPackedPara
   const int64_t own = dd * p.N + (n0 < p.N ? n0 : 0);  // of the lane's first state in a (D, N) block
 
   Lane<NS> ln;
-  float h[NS], h2[NS];
+  float h[NS], old[NS];
   float amax = 0.f;
   bool zero = false;
 #pragma unroll
   for (int k = 0; k < NS; ++k) {
     const float a = k < nk ? p.A[dd * p.As_d + (n0 + k) * p.As_n] : -1.f;
     ln.A[k] = a;
-    ln.A2[k] = a * kLog2e;
     ln.iA[k] = a != 0.f ? 1.f / a : 0.f;
     zero = zero || a == 0.f;
     amax = k < nk ? fmaxf(amax, fabsf(a)) : amax;
-    h[k] = h2[k] = 0.f;
+    h[k] = old[k] = 0.f;
   }
   const bool any_zero = __ballot(zero) != 0;
   const float Dk = p.Dskip && ch_ok ? p.Dskip[dd * p.Ds_d] : 0.f;
   const float bias = p.dbias && ch_ok ? p.dbias[dd * p.dbs_d] : 0.f;
-  const int64_t block = p.D * p.N;
   const bool vec = vec_state != 0;
-  if constexpr (TWIN) {
-    // the state at the line: from the sequence's first line on, each piece's end state, the decay over
-    // it applied to the state before it
-    const int first = seq.begin / p.step + 1;
-    load_block<NS>(p.H + (int64_t)(first - 1) * block + own, nk, vec, h);
-    for (int l = first + 1; l <= line; ++l) {
-      float e[NS];
-      load_block<NS>(p.H + (int64_t)(l - 1) * block + own, nk, vec, e);
-      const float sum = p.dsum[(int64_t)(l - 1) * p.D + dd];
+  if constexpr (AGAIN) {
+    enter<NS>(p, ln, seq.begin / p.step + 1, line, own, dd, nk, vec, h);
 #pragma unroll
-      for (int k = 0; k < NS; ++k) h[k] = __builtin_fmaf(__builtin_amdgcn_exp2f(ln.A2[k] * sum), h[k], e[k]);
-    }
+    for (int k = 0; k < NS; ++k) old[k] = h[k];
   } else if (line == 0) {
     const int64_t from = src_slot(p.q, s);
     if (from >= 0) load_block<NS>(p.states + from * p.sts_s + own, nk, vec, h);
   }
 
-  Streams<BF16, NS, VEC> st = {p, d0, (uint32_t)(lane / 4), ch_ok, j, lane / 4, n0, run.end};
-  const int YE = p.y_f32 ? 4 : 2;
+  Streams<BF16, NS, VEC> st(p, d0, lane, run.begin);
+  const bool has_z = st.has_z, dsoftplus = p.dsoftplus;
   Tile<BF16, NS, VEC> tile;
   auto stage = [&](int buf) {
     float* row = lds[wave][buf][lane / 4][0] + n0;
@@ -344,96 +442,188 @@ __global__ __launch_bounds__(64 * kWaves) void scan_packed_kernel(ScanPackedPara
   };
   float sum_dt = 0.f;
   bool met = false;
-  st.load(run.begin, tile);
+  const float close = p.y_f32 ? 0x1p-20f : 0x1p-16f;
+  int left = run.end - run.begin;
+  st.load(left, tile);
   stage(0);
   int buf = 0;
-  for (int t = run.begin; t < run.end; t += kTile, buf ^= 1) {
-    const int left = run.end - t < kTile ? run.end - t : kTile;
-    float x[4], dt[4], z[4], xs[4];
-    float umax = 0.f;
+  for (; left > 0; left -= kTile, buf ^= 1) {
+    float x[4], dt[4], xs[4], gate[4];
+    float tmax = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       x[i] = raw2f<BF16>(tile.x[i]);
-      z[i] = raw2f<BF16>(tile.z[i]);
-      float v = raw2f<BF16>(tile.dt[i]);
-      if (p.dsoftplus) v = 4 * i + j < left ? softplus(v + bias) : 0.f;  // past the piece nothing changes
-      dt[i] = v;
-      umax = fmaxf(umax, fabsf(v));
-      if constexpr (!TWIN) sum_dt += v;
-      xs[i] = EULER ? v * x[i] : x[i];
+      dt[i] = raw2f<BF16>(tile.dt[i]);
     }
-    st.load(t + kTile, tile);
+    if (dsoftplus) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float v = softplus(dt[i] + bias);
+        dt[i] = 4 * i + j < left ? v : 0.f;  // past the piece nothing changes
+      }
+    }
+    if (has_z) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float z = raw2f<BF16>(tile.z[i]);
+        gate[i] = z * sigmoid(z);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      xs[i] = EULER ? dt[i] * x[i] : x[i];
+      dt[i] *= kLog2e;
+      tmax = fmaxf(tmax, fabsf(dt[i]));
+      if constexpr (!AGAIN) sum_dt += dt[i];
+    }
+    st.load(left - kTile, tile);
     wave_sync();
     const float* bc = lds[wave][buf][0][0] + n0;
     float y[4];
     // the four lanes hold different steps and states: each one's largest delta and |A|
-    umax = fmaxf(umax, other<1>(umax));
-    umax = fmaxf(umax, other<2>(umax));
-    const int form = EULER ? kEuler : __ballot(!(umax * amax < 0.125f)) == 0 ? kSmall : BF16 && !any_zero ? kFast : kAny;
+    tmax = fmaxf(tmax, other<1>(tmax));
+    tmax = fmaxf(tmax, other<2>(tmax));
+    const int form = EULER ? kEuler
+                     : __ballot(!(tmax * amax < 0.125f * kLog2e)) == 0 ? kSmall
+                     : any_zero                                         ? kAny
+                                                                       : kFast;
     if constexpr (EULER) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = four_steps<NS, kEuler, TWIN>(h, h2, ln, dt[i], xs[i], bc + i * 8 * NP);
+      for (int i = 0; i < 4; ++i) {
+        y[i] = four_steps<NS, kEuler, AGAIN>(h, old, ln, dt[i], xs[i], bc + i * 8 * NP);
+        // a tile is one block of code here, and all its factors would be formed first, and spilled
+        if (AGAIN && i < 3) asm volatile("" : "+v"(h[0]), "+v"(dt[i + 1]), "+v"(xs[i + 1]));
+      }
     } else if (form == kSmall) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = four_steps<NS, kSmall, TWIN>(h, h2, ln, dt[i], xs[i], bc + i * 8 * NP);
+      for (int i = 0; i < 4; ++i) y[i] = four_steps<NS, kSmall, AGAIN>(h, old, ln, dt[i], xs[i], bc + i * 8 * NP);
     } else if (form == kFast) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = four_steps<NS, kFast, TWIN>(h, h2, ln, dt[i], xs[i], bc + i * 8 * NP);
+      for (int i = 0; i < 4; ++i) y[i] = four_steps<NS, kFast, AGAIN>(h, old, ln, dt[i], xs[i], bc + i * 8 * NP);
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = four_steps<NS, kAny, TWIN>(h, h2, ln, dt[i], xs[i], bc + i * 8 * NP);
+      for (int i = 0; i < 4; ++i) y[i] = four_steps<NS, kAny, AGAIN>(h, old, ln, dt[i], xs[i], bc + i * 8 * NP);
     }
-    const auto ry = rsrc((char*)p.y + ((int64_t)t * p.ys_t + d0) * YE, row_range(left, p.ys_t, p.D - d0, YE));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float v = __builtin_fmaf(Dk, x[i], y[i]);
-      if (p.z) v *= z[i] * sigmoid(z[i]);
-      const int row = 4 * i + j;
-      store1(ry, ch_ok && row < left ? ((uint32_t)row * (uint32_t)p.ys_t + st.lch) * (uint32_t)YE : kFar, v, p.y_f32);
+    for (int i = 0; i < 4; ++i) y[i] = __builtin_fmaf(Dk, x[i], y[i]);
+    if (has_z) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] *= gate[i];
     }
+    st.store(left, y);
     stage(buf ^ 1);
-    if constexpr (TWIN) {
+    if constexpr (AGAIN) {
       bool same = true;
 #pragma unroll
-      for (int k = 0; k < NS; ++k) same = same && __float_as_uint(h[k]) == __float_as_uint(h2[k]);
+      for (int k = 0; k < NS; ++k) same = same && fabsf(old[k]) <= close * fabsf(h[k]);
       if (__ballot(!same) == 0) {
-        met = t + kTile < run.end;
+        met = left > kTile;
         break;
       }
     }
   }
 
-  if (run.end < seq.end) {  // the piece ends at a line inside the sequence
-    if constexpr (!TWIN) {
-      const int64_t l = run.end / p.step - 1;
-      store_block<NS>(p.H + l * block + own, nk, vec, h);
+  const ScanPackedParams& q = args_anew<ScanPackedParams>();
+  const int64_t words = q.D * q.N;
+  const bool inside = run.end < seq.end;  // the piece ends at a line inside the sequence
+  if constexpr (!AGAIN) {
+    if (inside || line > 0) {
+      // the sequence's end after a line is not the true one yet, and another workgroup may not have read the slot
+      const int64_t at = inside ? run.end / q.step - 1 : line - 1;
+      store_block<NS>((inside ? q.H : q.E) + at * words + own, nk, vec, h);
       sum_dt += other<1>(sum_dt);
       sum_dt += other<2>(sum_dt);
-      if (j == 0 && ch_ok) p.dsum[l * p.D + d] = sum_dt;
+      if (j == 0 && ch_ok) (inside ? q.dsum : q.esum)[at * q.D + d] = sum_dt;
+      return;
     }
-    return;
   }
-  // the sequence's end: the first pass keeps that of a later piece aside (another workgroup may not have read
-  // the slot yet, and it is not the true state)
-  if (!TWIN && line > 0) {
-    store_block<NS>(p.E + (int64_t)(line - 1) * block + own, nk, vec, h);
-    return;
-  }
-  const int64_t to = dst_slot(p.q, s);
+  const int64_t to = inside ? -1 : dst_slot(q.q, s);
   if (to < 0) return;
-  if (TWIN && met) load_block<NS>(p.E + (int64_t)(line - 1) * block + own, nk, vec, h);
-  store_block<NS>(p.states + to * p.sts_s + own, nk, vec, h);
+  if (AGAIN && met) {
+    float e[NS];
+    load_block<NS>(q.E + (int64_t)(line - 1) * words + own, nk, vec, e);
+    const float sum = q.esum[(int64_t)(line - 1) * q.D + dd];
+    enter<NS>(q, ln, seq.begin / q.step + 1, line, own, dd, nk, vec, h);
+#pragma unroll
+    for (int k = 0; k < NS; ++k) h[k] = __builtin_fmaf(__builtin_amdgcn_exp2f(ln.A[k] * sum), h[k], e[k]);
+  }
+  store_block<NS>(q.states + to * q.sts_s + own, nk, vec, h);
+}
+
+// The pieces of the first pass by their length, the longest first: one workgroup,
+// a piece for each thread.
+__global__ __launch_bounds__(kScanOrdered) void order_kernel(ScanPackedParams p) {
+  __shared__ int len[kScanOrdered], starts[kScanOrdered + 1];
+  const int i = (int)threadIdx.x, n = p.lines + p.q.seqs;
+  for (int k = i; k <= p.q.seqs; k += kScanOrdered) starts[k] = p.q.starts[k];
+  __syncthreads();
+  int mine = -1;
+  auto rows = [&](int s) { return packed::sequence(starts[s], starts[s + 1], p.q.tokens); };
+  if (i < n) {
+    packed::Run r;
+    if (i < p.lines) {
+      const int at = (i + 1) * p.step;
+      const int s = packed::last_start(p.q.seqs, [&](int lo, int stride, int count) {
+        int c = 0;
+        for (int k = 0; k < count; ++k) c += starts[lo + k * stride] <= at;
+        return c;
+      });
+      r = s < 0 ? packed::Run{0, 0} : packed::later_piece(rows(s), at, p.step);
+    } else {
+      r = packed::first_piece(rows(i - p.lines), p.step);
+    }
+    mine = r.end - r.begin;
+  }
+  len[i] = mine;
+  __syncthreads();
+  int rank = 0;
+  for (int k = 0; k < n; ++k) rank += len[k] > mine || (len[k] == mine && k < i);
+  if (i < n) p.order[rank] = i;
 }
 
 // ------------------------------------------------------------ single tokens
 
-// One token of each sequence: a wave has 16 channels of it, a lane NS states of
-// one channel, read and written 16 bytes at a time.  Bound by that traffic, so
-// every state takes the accurate form.
-template <bool BF16, int NS, bool EULER>
-__global__ __launch_bounds__(64 * kWaves) void step_packed_kernel(ScanPackedParams p, unsigned nblk, int vec_state) {
+// A lane's NS states of a row: by words where `vec` says that they lie side by
+// side and aligned (all of them in or all out), else one by one.
+template <bool BF16, int NS>
+__device__ __forceinline__ void load_row(const void* base, int64_t at, int64_t sn, int n0, int nk, bool vec,
+                                         float (&o)[NS]) {
+  constexpr int E = BF16 ? 2 : 4;
+  const char* const p = (const char*)base + (at + (nk > 0 ? n0 : 0) * sn) * E;
+  if (NS > 1 && vec) {
+    uint32_t w[NS * E / 4 > 0 ? NS * E / 4 : 1];
+    if constexpr (NS * E % 16 == 0) {
+#pragma unroll
+      for (int i = 0; i < NS * E / 16; ++i) {
+        const uint4 v = ((const uint4*)p)[i];
+        w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+      }
+    } else if constexpr (NS * E == 8) {
+      const uint2 v = *(const uint2*)p;
+      w[0] = v.x; w[1] = v.y;
+    } else {
+      w[0] = *(const uint32_t*)p;
+    }
+#pragma unroll
+    for (int k = 0; k < NS; ++k)
+      o[k] = BF16 ? __uint_as_float((k & 1) ? (w[k >> 1] & 0xFFFF0000u) : (w[k >> 1] << 16)) : __uint_as_float(w[BF16 ? 0 : k]);
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < NS; ++k) {
+    const char* const q = p + (k < nk ? k : 0) * sn * E;
+    o[k] = BF16 ? raw2f<true>(*(const uint16_t*)q) : *(const float*)q;
+  }
+}
+
+// One token of each sequence.  A wave has 16 channels of U sequences, a lane NS
+// states of one channel of each, read and written 16 bytes at a time, all U asked
+// for at once.  Bound by that traffic, so every state takes the accurate form.
+template <bool BF16, int NS, bool EULER, int U>
+__global__ __launch_bounds__(64 * kWaves) void step_packed_kernel(ScanPackedParams p, unsigned nblk, int vec_state,
+                                                                  int vec_bc, int vec_a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
-  const int s = (int)(blockIdx.x / nblk);
+  const int s0 = (int)(blockIdx.x / nblk) * U;
   const int64_t d0 = ((int64_t)(blockIdx.x % nblk) * kWaves + wave) * kCh;
   if (d0 >= p.D) return;
   const int j = lane % 4, n0 = j * NS;
@@ -443,43 +633,54 @@ __global__ __launch_bounds__(64 * kWaves) void step_packed_kernel(ScanPackedPara
   const int nk = !ch_ok || n0 >= p.N ? 0 : (p.N - n0 < NS ? (int)(p.N - n0) : NS);
   const int64_t own = dd * p.N + (n0 < p.N ? n0 : 0);
   const bool vec = vec_state != 0;
-  const int64_t from = src_slot(p.q, s), to = dst_slot(p.q, s);
-  float h[NS], A[NS], B[NS], C[NS];
-#pragma unroll
-  for (int k = 0; k < NS; ++k) h[k] = 0.f;
-  if (from >= 0) load_block<NS>(p.states + from * p.sts_s + own, nk, vec, h);
   auto at = [&](const void* base, int64_t i) {
     if constexpr (BF16) return raw2f<true>(((const uint16_t*)base)[i]);
     else return ((const float*)base)[i];
   };
-  const float x = at(p.x, s * p.xs_t + dd);
-  float dt = at(p.delta, s * p.ds_t + dd);
-  const float z = p.z ? at(p.z, s * p.zs_t + dd) : 0.f;
+  float h[U][NS], B[U][NS], C[U][NS], x[U], dt[U], z[U], A[NS];
+  int64_t to[U];
 #pragma unroll
-  for (int k = 0; k < NS; ++k) {
-    const int64_t n = k < nk ? n0 + k : 0;
-    A[k] = p.A[dd * p.As_d + n * p.As_n];
-    B[k] = at(p.B, s * p.Bs_t + n * p.Bs_n);
-    C[k] = at(p.C, s * p.Cs_t + n * p.Cs_n);
+  for (int u = 0; u < U; ++u) {
+    // the last sequence again where there are no U left: its results are not stored twice
+    const int s = s0 + u < p.q.seqs ? s0 + u : p.q.seqs - 1;
+    const int64_t from = src_slot(p.q, s);
+    to[u] = s0 + u < p.q.seqs ? dst_slot(p.q, s) : -1;
+#pragma unroll
+    for (int k = 0; k < NS; ++k) h[u][k] = 0.f;
+    if (from >= 0) load_block<NS>(p.states + from * p.sts_s + own, nk, vec, h[u]);
+    x[u] = at(p.x, s * p.xs_t + dd);
+    dt[u] = at(p.delta, s * p.ds_t + dd);
+    z[u] = p.z ? at(p.z, s * p.zs_t + dd) : 0.f;
+    load_row<BF16, NS>(p.B, s * p.Bs_t, p.Bs_n, n0, nk, vec_bc, B[u]);
+    load_row<BF16, NS>(p.C, s * p.Cs_t, p.Cs_n, n0, nk, vec_bc, C[u]);
   }
+  load_row<false, NS>(p.A, dd * p.As_d, p.As_n, n0, nk, vec_a, A);
   const float Dk = p.Dskip ? p.Dskip[dd * p.Ds_d] : 0.f;
-  if (p.dsoftplus) dt = softplus(dt + (p.dbias ? p.dbias[dd * p.dbs_d] : 0.f));
-  float y = 0.f;
+  const float bias = p.dbias ? p.dbias[dd * p.dbs_d] : 0.f;
 #pragma unroll
-  for (int k = 0; k < NS; ++k) {
-    const float u = dt * A[k], Ab = __builtin_amdgcn_exp2f(u * kLog2e);
-    const float c = EULER ? dt : fabsf(u) < 0.25f ? dt * phi(u) : (Ab - 1.f) / A[k];
-    h[k] = __builtin_fmaf(Ab, h[k], c * (x * B[k]));
-    if (k < nk) y = __builtin_fmaf(C[k], h[k], y);
-  }
-  if (to >= 0) store_block<NS>(p.states + to * p.sts_s + own, nk, vec, h);
-  y += other<1>(y);
-  y += other<2>(y);
-  if (j == 0 && ch_ok) {
-    float v = __builtin_fmaf(Dk, x, y);
-    if (p.z) v *= z * sigmoid(z);
-    if (p.y_f32) ((float*)p.y)[s * p.ys_t + d] = v;
-    else ((__bf16*)p.y)[s * p.ys_t + d] = (__bf16)v;
+  for (int u = 0; u < U; ++u) {
+    float v = dt[u];
+    if (p.dsoftplus) v = softplus(v + bias);
+    const float dte = v * kLog2e;
+    float y = 0.f;
+#pragma unroll
+    for (int k = 0; k < NS; ++k) {
+      const float t = dte * A[k], Ab = __builtin_amdgcn_exp2f(t);
+      const float far = (Ab - 1.f) * __builtin_amdgcn_rcpf(A[k]), near = dte * ratio(t);
+      const float c = EULER ? v : fabsf(t) < 0.25f * kLog2e ? near : far;
+      h[u][k] = __builtin_fmaf(Ab, h[u][k], c * (x[u] * B[u][k]));
+      y = __builtin_fmaf(k < nk ? C[u][k] : 0.f, k < nk ? h[u][k] : 0.f, y);
+    }
+    if (to[u] >= 0) store_block<NS>(p.states + to[u] * p.sts_s + own, nk, vec, h[u]);
+    y += other<1>(y);
+    y += other<2>(y);
+    if (j == 0 && ch_ok && s0 + u < p.q.seqs) {
+      float o = __builtin_fmaf(Dk, x[u], y);
+      if (p.z) o *= z[u] * sigmoid(z[u]);
+      const int64_t i = (int64_t)(s0 + u) * p.ys_t + d;
+      if (p.y_f32) ((float*)p.y)[i] = o;
+      else ((__bf16*)p.y)[i] = (__bf16)o;
+    }
   }
 }
 
@@ -489,17 +690,26 @@ void launch_ns(const ScanPackedParams& p, hipStream_t stream) {
   auto al = [](const void* ptr, int64_t bytes) { return ((uintptr_t)ptr % (uintptr_t)bytes) == 0; };
   // whole 16-byte words of a lane's states (the workspace's blocks are aligned and follow (D, N))
   const int vec_state = NS >= 4 && p.N % NS == 0 && al(p.states, 16) && p.sts_s % 4 == 0;
-  if (!p.q.starts) {
-    hipLaunchKernelGGL((step_packed_kernel<BF16, NS, EULER>), dim3(nblk * (unsigned)p.q.seqs), dim3(64 * kWaves), 0,
-                       stream, p, nblk, vec_state);
-    return;
-  }
   // B and C: a lane's NS states by 16-byte words (or one smaller)
   const int64_t word = std::min<int64_t>(16, NS * (BF16 ? 2 : 4)), e = BF16 ? 2 : 4;
   const bool vec = p.N % NS == 0 && p.Bs_n == 1 && p.Cs_n == 1 && al(p.B, word) && al(p.C, word) &&
                    p.Bs_t * e % word == 0 && p.Cs_t * e % word == 0;
+  if (!p.q.starts) {
+    const int vec_a = p.N % NS == 0 && p.As_n == 1 && al(p.A, std::min(16, 4 * NS)) && p.As_d % std::min(4, NS) == 0;
+    // four sequences a wave where that leaves two workgroups a compute unit
+    constexpr int U = NS <= 4 ? 4 : 1;
+    const unsigned groups = ((unsigned)p.q.seqs + U - 1) / U;
+    if (U > 1 && nblk * groups >= 512)
+      hipLaunchKernelGGL((step_packed_kernel<BF16, NS, EULER, U>), dim3(nblk * groups), dim3(64 * kWaves), 0, stream, p,
+                         nblk, vec_state, vec, vec_a);
+    else
+      hipLaunchKernelGGL((step_packed_kernel<BF16, NS, EULER, 1>), dim3(nblk * (unsigned)p.q.seqs), dim3(64 * kWaves), 0,
+                         stream, p, nblk, vec_state, vec, vec_a);
+    return;
+  }
   const unsigned n = (unsigned)p.q.seqs + (unsigned)p.lines;
   const dim3 block(64 * kWaves);
+  if (p.order) hipLaunchKernelGGL(order_kernel, dim3(1), dim3(kScanOrdered), 0, stream, p);
   if (vec) {
     hipLaunchKernelGGL((scan_packed_kernel<BF16, NS, EULER, false, true>), dim3(nblk * n), block, 0, stream, p, nblk,
                        vec_state);
@@ -527,20 +737,26 @@ void launch_n(const ScanPackedParams& p, hipStream_t stream) {
 }  // namespace
 
 ScanPackedPlan plan_scan_packed(int64_t tokens, int64_t seqs, int64_t dim, int64_t dstate, bool single) {
-  ScanPackedPlan pl = {0, 0, 0, 0, 0, 0};
-  (void)seqs;
+  ScanPackedPlan pl = {};
   if (single) return pl;
   auto round256 = [](int64_t n) { return (n + 255) / 256 * 256; };
-  // pieces of 16 channels that fill the card
+  // Three waves for each SIMD (four are resident).  Fewer, longer pieces leave them
+  // idle at the end, more are walked again: 16384 x 5120 bf16 at 2048 waves 646 us,
+  // 2560 492, 3072 495, 4096 498; 1111 x 1536 fp32 at 64 rows a piece 40 us, 128 46,
+  // 256 54 (a wave walks 16 rows in 2 to 3 us).
   const int64_t waves = (dim + kCh - 1) / kCh;
-  int64_t step = (tokens * waves / 4096 + kTile - 1) / kTile * kTile;
-  step = std::max<int64_t>(step, 256);
+  int64_t step = (tokens * waves / 3072 + kTile - 1) / kTile * kTile;
+  step = std::max<int64_t>(step, 64);
   step = std::max<int64_t>(step, ((tokens + 254) / 255 + kTile - 1) / kTile * kTile);  // at most 255 lines
   pl.step = step;
   pl.lines = (tokens - 1) / step;
+  const int64_t n = pl.lines + seqs;
   pl.ws_H = pl.ws_E = round256(pl.lines * dim * dstate * 4);
-  pl.ws_S = round256(pl.lines * dim * 4);
-  pl.ws_total = pl.ws_H + pl.ws_E + pl.ws_S;
+  pl.ws_S = round256(2 * pl.lines * dim * 4);
+  // The longest first where they do not run all at once (16384 x 5120 in 24
+  // sequences: 740 -> 590 us), unless the 4 us that this takes are too many.
+  pl.ws_order = n <= kScanOrdered && n * waves > 4096 && tokens * waves >= (1 << 20) ? round256(n * 4) : 0;
+  pl.ws_total = pl.ws_H + pl.ws_E + pl.ws_S + pl.ws_order;
   return pl;
 }
 

@@ -363,11 +363,13 @@ ssm_status ssm_selective_scan_packed(const ssm_scan_packed_desc* d, const ssm_sc
   q.dsoftplus = (f & SSM_DELTA_SOFTPLUS) != 0;
   q.step = (int)pl.step;
   q.lines = (int)pl.lines;
+  char* const w = (char*)workspace;
+  if (pl.ws_order) q.order = (int*)(w + pl.ws_H + pl.ws_E + pl.ws_S);
   if (pl.lines) {
-    char* w = (char*)workspace;
     q.H = (float*)w;
     q.E = (float*)(w + pl.ws_H);
     q.dsum = (float*)(w + pl.ws_H + pl.ws_E);
+    q.esum = q.dsum + pl.lines * d->dim;
   }
   return hip_status(ssm::launch_scan_packed(q, (hipStream_t)hip_stream));
 }

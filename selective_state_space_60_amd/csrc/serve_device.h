@@ -96,5 +96,14 @@ static __device__ __forceinline__ int64_t dst_slot(const PackedSeqs& q, int s) {
   return v >= 0 && v < q.slots ? v : -1;
 }
 
+// The kernel's first argument read anew: what only a late part needs is loaded
+// there, not held in (or spilled from) scalar registers until then.
+template <class P>
+static __device__ __forceinline__ const P& args_anew() {
+  auto at = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(at));
+  return *(const P*)(const __attribute__((address_space(4))) P*)at;
+}
+
 }  // namespace dev
 }  // namespace ssm

@@ -82,12 +82,16 @@ struct ScanPackedParams {
   // words of the grid lines, for the sequences that cross them
   float* H;           // (lines, D, N): state at the line, from zeros at the line before (or the sequence's start)
   float* E;           // (lines, D, N): state at the end of a sequence that ends behind the line, from zeros there
-  float* dsum;        // (lines, D): sum of delta over the piece that ends at the line
+  int* order;         // (lines + seqs): the pieces, the longest first, or null: in their order
+  float* dsum;        // (lines, D): log2(e) times the sum of delta over the piece that ends at the line
+  float* esum;        // (lines, D): the same over the piece from the line to its sequence's end
 };
+
+constexpr int kScanOrdered = 256;  // pieces that are put in order, at most
 
 // The plan of a packed scan: rows of a piece, grid lines and workspace bytes.
 struct ScanPackedPlan {
-  int64_t step, lines, ws_H, ws_E, ws_S, ws_total;
+  int64_t step, lines, ws_H, ws_E, ws_S, ws_order, ws_total;
 };
 ScanPackedPlan plan_scan_packed(int64_t tokens, int64_t seqs, int64_t dim, int64_t dstate, bool single);
 
