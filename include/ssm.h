@@ -819,8 +819,8 @@ typedef struct {
  * continuations the k of the highest score,
  *      s[n,v] = scores[n] + logits[n,v] - log(sum_w exp(logits[n,w])),
  * in falling order, the lower index n vocab + v first where scores are equal.
- * A beam's own continuations are ordered by their logits; the normaliser is an
- * fp32 sum, scores are formed and compared in fp64 and rounded to fp32 once.
+ * The normaliser is an fp32 sum of up to 4096 tokens at a time, added up in fp64;
+ * scores are formed and compared in fp64 and rounded to fp32 once.
  * Banned tokens have the logit -inf.  A beam whose score or normaliser is not a
  * finite number (all tokens banned, a NaN or +inf among the logits, a score of
  * -inf for a beam that is not in use) scores -inf throughout; continuations of

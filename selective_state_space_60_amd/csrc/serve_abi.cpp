@@ -208,13 +208,14 @@ ssm_status validate_beam(const ssm_beam_desc* d) {
 }
 
 struct BeamPlan {
-  int64_t parts, ws_cand, ws_total;
+  ssm::BeamPieces cut;
+  int64_t ws_cand, ws_total;
 };
 
 BeamPlan plan_beam(const ssm_beam_desc& d) {
   BeamPlan pl;
-  pl.parts = ssm::beam_parts(d.batch * d.beams, d.vocab);
-  const int64_t n = d.batch * d.beams * pl.parts;
+  pl.cut = ssm::beam_pieces(d.batch * d.beams, d.vocab);
+  const int64_t n = d.batch * d.beams * pl.cut.parts;
   pl.ws_cand = round256(n * d.k * 8);
   pl.ws_total = pl.ws_cand + round256(n * 8);
   return pl;
@@ -403,7 +404,8 @@ ssm_status ssm_beam_select(const ssm_beam_desc* d, const ssm_beam_ptrs* p, void*
   q.ls_b = d->logits.stride[0]; q.ls_n = d->logits.stride[1];
   q.ss_b = d->scores.stride[0]; q.ss_n = d->scores.stride[1];
   q.f32 = d->logits.dtype == SSM_F32;
-  q.parts = (int)pl.parts;
+  q.values = pl.cut.values;
+  q.parts = (int)pl.cut.parts;
   q.cand = (uint64_t*)workspace;
   q.stat = (float2*)((char*)workspace + pl.ws_cand);
   return hip_status(ssm::launch_beam_select(q, (hipStream_t)hip_stream));

@@ -108,13 +108,17 @@ struct BeamParams {
   int k;
   int64_t ls_b, ls_n, ss_b, ss_n;
   int f32;              // logits are fp32 (1) or bf16 (0)
-  int parts;            // pieces of a row
+  int values, parts;    // values of a thread, pieces of a row
   float2* stat;         // (batch, beams, parts): largest logit, sum of exp(logit - largest)
   uint64_t* cand;       // (batch, beams, parts, k): the best of a piece in falling order; 0: none
 };
 
-// Pieces that a row of logits is cut into.
-int64_t beam_parts(int64_t rows, int64_t vocab);
+// Values of a thread, and pieces that a row of logits is cut into.
+struct BeamPieces {
+  int values;
+  int64_t parts;
+};
+BeamPieces beam_pieces(int64_t rows, int64_t vocab);
 
 hipError_t launch_beam_select(const BeamParams& p, hipStream_t stream);
 
