@@ -796,7 +796,7 @@ typedef struct {
  * sums added in a fixed order (deterministic).  Outputs may not overlap inputs
  * or each other.  Workspace: ssm_causal_conv1d_bwd_workspace_size bytes, 256-byte
  * aligned.  Limits (SSM_ERR_UNSUPPORTED otherwise): 128 rows of x, dy or dx span
- * less than 1 GiB; batch ceil(seqlen/64) ceil(dim/64) < 2^24; dim < 2^28. */
+ * less than 1 GiB; batch ceil(seqlen/128) ceil(dim/64) < 2^24; dim < 2^28. */
 typedef struct {
   int64_t batch, seqlen, dim, width;
   uint32_t flags;

@@ -165,7 +165,7 @@ ssm_status validate_conv_bwd(const ssm_conv_bwd_desc* d) {
   if (f & ~(SSM_HAS_BIAS | SSM_SILU)) return SSM_ERR_UNSUPPORTED;
   if (d->width > 8 || d->dim >= ((int64_t)1 << 28) || !sizes_ok({d->batch, d->seqlen, d->dim}))
     return SSM_ERR_UNSUPPORTED;
-  if ((__int128)d->batch * ((d->seqlen + 63) / 64) * ((d->dim + 63) / 64) >= kMaxBlocks256) return SSM_ERR_UNSUPPORTED;
+  if ((__int128)d->batch * ((d->seqlen + 127) / 128) * ((d->dim + 63) / 64) >= kMaxBlocks256) return SSM_ERR_UNSUPPORTED;
   const int32_t io = d->x.dtype;
   if (io == SSM_F16) return SSM_ERR_UNSUPPORTED;
   const int64_t bld[3] = {d->batch, d->seqlen, d->dim}, dw[2] = {d->dim, d->width}, dd[1] = {d->dim};
@@ -181,7 +181,7 @@ ssm_status validate_conv_bwd(const ssm_conv_bwd_desc* d) {
 }
 
 int64_t conv_bwd_bytes(const ssm_conv_bwd_desc& d) {
-  return round256(ssm::conv_bwd_parts(d.batch, d.seqlen, d.dim) * (d.width + 1) * d.dim * 4);
+  return round256(ssm::conv_bwd_parts(d.batch, d.seqlen) * (d.width + 1) * d.dim * 4);
 }
 
 // ----------------------------------------------------------- beam selection

@@ -51,11 +51,9 @@ struct ConvBwdParams {
   int io_bf16, dy_f32, dx_f32, silu;
 };
 
-// Steps of a workgroup, as many as give the card enough workgroups.
-int64_t conv_bwd_steps(int64_t batch, int64_t seqlen, int64_t dim);
-inline int64_t conv_bwd_parts(int64_t batch, int64_t seqlen, int64_t dim) {
-  const int64_t n = conv_bwd_steps(batch, seqlen, dim);
-  return batch * ((seqlen + n - 1) / n);
+constexpr int64_t kConvBwdSteps = 4 * 32;  // of a workgroup
+inline int64_t conv_bwd_parts(int64_t batch, int64_t seqlen) {
+  return batch * ((seqlen + kConvBwdSteps - 1) / kConvBwdSteps);
 }
 
 hipError_t launch_conv_bwd(const ConvBwdParams& p, hipStream_t stream);
