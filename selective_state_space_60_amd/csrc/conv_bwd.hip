@@ -201,10 +201,9 @@ __global__ __launch_bounds__(64 * NW) void conv_bwd_kernel(ConvBwdParams p, unsi
   constexpr int own = (int)kConvBwdSteps / NW;
   const int64_t t0 = (pt * NW + wave) * own;
   Stretch<BF16, DYF, V, W> q;
+  load_taps<V, W>(p.w, on ? d0 : c0, p.ws_d, p.ws_k, q.wk);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-#pragma unroll
-    for (int k = 0; k < W; ++k) q.wk[v][k] = on ? p.w[(d0 + v) * p.ws_d + k * p.ws_k] : 0.f;
     q.bv[v] = on && p.bias ? p.bias[(d0 + v) * p.bs_d] : 0.f;
 #pragma unroll
     for (int k = 0; k < W; ++k) q.dw[v][k] = 0.f;

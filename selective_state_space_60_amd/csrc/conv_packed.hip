@@ -174,15 +174,12 @@ __global__ __launch_bounds__(NT) void conv_packed_kernel(ConvPackedParams p, uns
     if (t0 >= end) return;
   }
   if (ch.c0 + ch.lane >= p.D) return;  // V divides D where it is 4, so a thread is all in or all out
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int64_t d = ch.c0 + ch.lane + v;
-#pragma unroll
-    for (int k = 0; k < W; ++k) ch.w[v][k] = p.w[d * p.ws_d + k * p.ws_k];
-    ch.b[v] = p.bias ? p.bias[d * p.bs_d] : 0.f;
-  }
   const bool pool = W > 1 && p.windows && first;
-  const int64_t from = pool ? src_slot(p.q, s) : -1, to = pool ? dst_slot(p.q, s) : -1;
+  const Slots slot = slots_of(p.q, s, p.w);  // no pool: no slots
+  const int64_t from = pool ? slot.from : -1, to = pool ? slot.to : -1;
+  load_taps<V, W>(p.w, ch.c0 + ch.lane, p.ws_d, p.ws_k, ch.w);
+#pragma unroll
+  for (int v = 0; v < V; ++v) ch.b[v] = p.bias ? p.bias[(ch.c0 + ch.lane + v) * p.bs_d] : 0.f;
   const __amdgpu_buffer_rsrc_t win = window_buffer<BF16, W>(p, from, ch.c0);
   // the new window: its row i is row n - (W - 1) + i of the sequence, or one of the old window
   Row<BF16, V> next[W > 1 ? W - 1 : 1];

@@ -425,7 +425,7 @@ __global__ __launch_bounds__(64 * kWaves, NS <= 4 ? 4 : NS == 8 ? 2 : 1) void sc
 #pragma unroll
     for (int k = 0; k < NS; ++k) old[k] = h[k];
   } else if (line == 0) {
-    const int64_t from = src_slot(p.q, s);
+    const int64_t from = slots_of(p.q, s, p.A).from;
     if (from >= 0) load_block<NS>(p.states + from * p.sts_s + own, nk, vec, h);
   }
 
@@ -537,7 +537,7 @@ __global__ __launch_bounds__(64 * kWaves, NS <= 4 ? 4 : NS == 8 ? 2 : 1) void sc
       return;
     }
   }
-  const int64_t to = inside ? -1 : dst_slot(q.q, s);
+  const int64_t to = inside ? -1 : slots_of(q.q, s, q.A).to;
   if (to < 0) return;
   if (AGAIN && met) {
     float e[NS];
@@ -643,8 +643,9 @@ __global__ __launch_bounds__(64 * kWaves) void step_packed_kernel(ScanPackedPara
   for (int u = 0; u < U; ++u) {
     // the last sequence again where there are no U left: its results are not stored twice
     const int s = s0 + u < p.q.seqs ? s0 + u : p.q.seqs - 1;
-    const int64_t from = src_slot(p.q, s);
-    to[u] = s0 + u < p.q.seqs ? dst_slot(p.q, s) : -1;
+    const Slots slot = slots_of(p.q, s, p.A);
+    const int64_t from = slot.from;
+    to[u] = s0 + u < p.q.seqs ? slot.to : -1;
 #pragma unroll
     for (int k = 0; k < NS; ++k) h[u][k] = 0.f;
     if (from >= 0) load_block<NS>(p.states + from * p.sts_s + own, nk, vec, h[u]);
@@ -697,7 +698,7 @@ void launch_ns(const ScanPackedParams& p, hipStream_t stream) {
   if (!p.q.starts) {
     const int vec_a = p.N % NS == 0 && p.As_n == 1 && al(p.A, std::min(16, 4 * NS)) && p.As_d % std::min(4, NS) == 0;
     // four sequences a wave where that leaves two workgroups a compute unit
-    constexpr int U = NS <= 4 ? 4 : 1;
+    constexpr int U = NS <= 4 ? 2 : 1;
     const unsigned groups = ((unsigned)p.q.seqs + U - 1) / U;
     if (U > 1 && nblk * groups >= 512)
       hipLaunchKernelGGL((step_packed_kernel<BF16, NS, EULER, U>), dim3(nblk * groups), dim3(64 * kWaves), 0, stream, p,

@@ -86,14 +86,53 @@ static __device__ __forceinline__ int find_sequence(const PackedSeqs& q, int at)
   });
 }
 
-// The slot that sequence s starts from and the one it ends in, or -1.
-static __device__ __forceinline__ int64_t src_slot(const PackedSeqs& q, int s) {
-  const int v = q.src ? q.src[s] : s;
-  return v >= 0 && v < q.slots ? v : -1;
+// The slot that a sequence starts from and the one it ends in, or -1.
+struct Slots {
+  int64_t from, to;
+};
+
+// Both asked for at once and without a branch: a list that is not there is read
+// from `any`, some memory of at least four bytes, and not used.
+static __device__ __forceinline__ Slots slots_of(const PackedSeqs& q, int s, const void* any) {
+  const int32_t* const ps = q.src ? q.src + s : (const int32_t*)any;
+  const int32_t* const pd = q.dst ? q.dst + s : (const int32_t*)any;
+  const int vs = *ps, vd = *pd;
+  const int from = q.src ? vs : s, to = q.dst ? vd : from;
+  return {from >= 0 && from < q.slots ? from : -1, to >= 0 && to < q.slots ? to : -1};
 }
-static __device__ __forceinline__ int64_t dst_slot(const PackedSeqs& q, int s) {
-  const int v = q.dst ? q.dst[s] : q.src ? q.src[s] : s;
-  return v >= 0 && v < q.slots ? v : -1;
+
+// The W taps of a thread's V channels from d0 on.  A dense (D, W) block is read by
+// 16-byte words (V 4) or 8-byte words (V 2): one by one they are V W loads with
+// every lane on another line.
+template <int V, int W>
+static __device__ __forceinline__ void load_taps(const float* w, int64_t d0, int64_t ws_d, int64_t ws_k,
+                                                 float (&o)[V][W]) {
+  if (V > 1 && ws_k == 1 && ws_d == W && ((uintptr_t)w & 15) == 0) {  // uniform
+    const float* const at = w + d0 * W;
+    float f[V * W];
+    if constexpr (V == 4) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        const float4 v = ((const float4*)at)[i];
+        f[4 * i] = v.x; f[4 * i + 1] = v.y; f[4 * i + 2] = v.z; f[4 * i + 3] = v.w;
+      }
+    } else if constexpr (V == 2) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        const float2 v = ((const float2*)at)[i];
+        f[2 * i] = v.x; f[2 * i + 1] = v.y;
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int k = 0; k < W; ++k) o[v][k] = f[v * W + k];
+    return;
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int k = 0; k < W; ++k) o[v][k] = w[(d0 + v) * ws_d + k * ws_k];
 }
 
 // The kernel's first argument read anew: what only a late part needs is loaded
