@@ -8,6 +8,11 @@ SelectiveSSM listing): in_proj to x and z; Conv1D + SiLU on x; x_proj to
 B | C | dt; dt_proj (with bias, softplus applied in the scan); the selective
 scan; y * SiLU(z); out_proj.
 
+``mamba_block_bwd`` is its backward.  ``mamba_block_packed`` runs the block over
+packed sequences that live in a pool of windows and states: prompts of different
+lengths, parts of prompts, or (without starts) one token each of many sequences;
+``beam_advance`` is a beam search's step over such a pool.
+
 ``mamba_layer_fwd`` puts the block behind an RMS norm on a residual stream.
 ``gated_layer_fwd`` / ``gated_layer_bwd`` are the same kind of layer around the
 gated linear recurrence, and ``gated_layer_step`` is its decode step, whose
@@ -17,8 +22,9 @@ from __future__ import annotations
 
 import torch
 
-from . import (causal_conv1d, gated_scan_bwd, gated_scan_ckpt, gated_scan_fwd, gated_state_update, rms_norm,
-               rms_norm_bwd, selective_scan_fwd, w4_matvec, w4_quantize)
+from . import (beam_select, causal_conv1d, causal_conv1d_bwd, causal_conv1d_packed, gated_scan_bwd, gated_scan_ckpt,
+               gated_scan_fwd, gated_state_update, rms_norm, rms_norm_bwd, scan_ckpt, selective_scan_bwd,
+               selective_scan_fwd, selective_scan_packed, state_move, w4_matvec, w4_quantize)
 
 
 class BlockWeights:
@@ -37,9 +43,10 @@ class BlockWeights:
         self.M = self.W_in_t.shape[0]
 
 
-def mamba_block_fwd(u: torch.Tensor, w: BlockWeights, mark=None) -> torch.Tensor:
+def mamba_block_fwd(u: torch.Tensor, w: BlockWeights, mark=None, train=False):
     """u: (batch, L, d_model) bf16 -> (batch, L, d_model) bf16.  `mark`, if
-    given, is called after each stage (for timing)."""
+    given, is called after each stage (for timing).  With train: (output, what
+    mamba_block_bwd takes)."""
     batch, L, M = u.shape
     E, N, R = w.E, w.N, w.R
     T = batch * L
@@ -52,12 +59,76 @@ def mamba_block_fwd(u: torch.Tensor, w: BlockWeights, mark=None) -> torch.Tensor
     delta = torch.mm(xd[:, 2 * N:2 * N + R], w.W_dt_t).view(batch, L, E)  # dt_proj (bias in the scan)
     if mark: mark("x_proj+dt_proj")
     xd = xd.view(batch, L, -1)
+    ckpt = scan_ckpt(batch, L, E, N, u.device) if train else None
     y, _ = selective_scan_fwd(xc, delta, w.A, xd[..., :N], xd[..., N:2 * N], D=w.D, z=z,
-                              delta_softplus=True, delta_bias=w.b_dt)
+                              delta_softplus=True, delta_bias=w.b_dt, ckpt=ckpt)
     if mark: mark("scan")
     out = torch.mm(y.view(T, E), w.W_out_t).view(batch, L, M)           # out_proj
     if mark: mark("out_proj")
+    if train:
+        return out, {"u": u, "xz": xz, "xc": xc, "xd": xd, "delta": delta, "y": y, "ckpt": ckpt}
     return out
+
+
+def mamba_block_bwd(dout: torch.Tensor, w: BlockWeights, saved: dict) -> dict:
+    """Gradients of mamba_block_fwd(..., train=True): dout (batch, L, d_model)
+    bf16 reaches its output.  Returns du (bf16) and the weights' gradients, the
+    projections' dW_in_t, dW_x_t, dW_dt_t, dW_out_t in bf16 as the GEMMs hold the
+    weights, dconv_w, dconv_b, db_dt, dA, dD in fp32."""
+    u, xz, xc, xd, delta = (saved[k] for k in ("u", "xz", "xc", "xd", "delta"))
+    batch, L, M = u.shape
+    E, N, R, T = w.E, w.N, w.R, batch * L
+    across = lambda t: t.t().contiguous()  # noqa: E731
+    x, z = xz[..., :E], xz[..., E:]
+    dout2 = dout.reshape(T, M)
+    dy = torch.mm(dout2, across(w.W_out_t)).view(batch, L, E)
+    g = selective_scan_bwd(dy, xc, delta, w.A, xd[..., :N], xd[..., N:2 * N], D=w.D, z=z, delta_softplus=True,
+                           delta_bias=w.b_dt, ckpt=saved["ckpt"])
+    ddelta = g["ddelta"].view(T, E)
+    dxd = torch.zeros_like(xd).view(T, -1)                              # B | C | dt | padding
+    dxd[:, :N], dxd[:, N:2 * N] = g["dB"].view(T, N), g["dC"].view(T, N)
+    dxd[:, 2 * N:2 * N + R] = torch.mm(ddelta, across(w.W_dt_t))
+    dxc = g["dx"].view(T, E) + torch.mm(dxd, across(w.W_x_t))
+    dxz = torch.empty_like(xz)
+    c = causal_conv1d_bwd(dxc.view(batch, L, E), x, w.conv_w, w.conv_b, silu=True, dx=dxz[..., :E])
+    dxz[..., E:] = g["dz"]
+    dxz2 = dxz.view(T, 2 * E)
+    return {"du": torch.mm(dxz2, across(w.W_in_t)).view(batch, L, M),
+            "dW_in_t": torch.mm(across(u.reshape(T, M)), dxz2), "dW_x_t": torch.mm(across(xc.view(T, E)), dxd),
+            "dW_dt_t": torch.mm(across(xd.view(T, -1)[:, 2 * N:2 * N + R]), ddelta),
+            "dW_out_t": torch.mm(across(saved["y"].view(T, E)), dout2), "dconv_w": c["dweight"], "dconv_b": c["dbias"],
+            "db_dt": g["ddelta_bias"], "dA": g["dA"], "dD": g["dD"]}
+
+
+def mamba_block_packed(u, w: BlockWeights, windows, states, starts=None, src=None, dst=None):
+    """The block over packed sequences: u (tokens, d_model) bf16, sequence s rows
+    starts[s] to starts[s + 1] (without starts each row is one token of a
+    sequence).  windows (slots, width - 1, E) bf16 and states (slots, E, N) fp32
+    are the pool that the sequences start from and end in (see
+    causal_conv1d_packed), updated in place.  Returns (tokens, d_model) bf16; rows
+    of no sequence hold anything."""
+    E, N, R = w.E, w.N, w.R
+    xz = torch.mm(u, w.W_in_t)
+    seqs = dict(starts=starts, src=src, dst=dst)
+    xc = causal_conv1d_packed(xz[:, :E], w.conv_w, windows, bias=w.conv_b, silu=True, **seqs)
+    xd = torch.mm(xc, w.W_x_t)
+    delta = torch.mm(xd[:, 2 * N:2 * N + R], w.W_dt_t)
+    y = selective_scan_packed(xc, delta, w.A, xd[:, :N], xd[:, N:2 * N], states, D=w.D, z=xz[:, E:],
+                              delta_softplus=True, delta_bias=w.b_dt, **seqs)
+    return torch.mm(y, w.W_out_t)
+
+
+def beam_advance(logits, scores, slots, pools):
+    """A beam search's step: from logits (batch, beams, vocab) and scores (batch,
+    beams) fp32 the `beams` best continuations of every batch element, and the
+    pools' slots moved so that beam n's slot slots[b, n] (int32) holds the state of
+    the beam it continues.  pools: the windows and states of every layer.  Returns
+    (scores, tokens, parents), each (batch, beams)."""
+    scores, tokens, parents = beam_select(logits, scores, slots.shape[1])
+    src = slots.gather(1, parents.long()).view(-1)
+    for pool in pools:
+        state_move(pool, src, slots.view(-1))
+    return scores, tokens, parents
 
 
 def mamba_layer_fwd(u: torch.Tensor, residual: torch.Tensor, w: BlockWeights, norm_weight: torch.Tensor,

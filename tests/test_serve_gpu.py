@@ -1,0 +1,258 @@
+"""The operators over packed sequences together, as a server and a training step
+use them: a Mamba block over a pool (prompts, parts, tokens), its training step,
+beam search, HIP graphs, streams."""
+import pytest
+
+import synth
+from _gpu import banner
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():  # pragma: no cover
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+import selective_state_space_60_amd as ssm  # noqa: E402
+from selective_state_space_60_amd import block  # noqa: E402
+
+# Every value between two operators is rounded to bf16 (2^-8 at most, 2^-9.5 in
+# the mean square).  A block's output passes five such roundings, a gradient about
+# ten, that enter independently, each at most a few times amplified: sqrt(10)
+# 2^-9.5 is 0.5 %, so 2 % and 3 % of the whole.
+BF16_BLOCK, BF16_GRAD = 2e-2, 3e-2
+
+
+def rel(got, want):
+    g, w = got.detach().double().cpu(), want.detach().double().cpu()
+    assert bool(torch.isfinite(g).all())
+    return float((g - w).norm() / w.norm())
+
+
+def weights(M=64, E=128, N=16, R=4, K=4, seed=1):
+    spec = synth.block_spec(synth.BLOCK2_8B, batch=1, seqlen=8, d_model=M, d_inner=E, dstate=N, dt_rank=R, d_conv=K)
+    host = synth.block_inputs(spec, seed)
+    return block.BlockWeights(host, N, R)
+
+
+def pools(w, slots, K=4):
+    return (torch.full((slots, K - 1, w.E), 3.0, device="cuda").bfloat16(),
+            torch.full((slots, w.E, w.N), 3.0, device="cuda"))
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def test_prompts_parts_and_tokens():
+    """Three requests: prompts in one call, the rest of one of them, then token by token, against the block over the
+    whole sequences."""
+    banner("block over a pool")
+    w = weights()
+    g = torch.Generator().manual_seed(2)
+    n, steps = [5, 170, 33], 4
+    seqs = [torch.randn(1, v + steps, w.M, generator=g).bfloat16().cuda() for v in n]
+    want = [block.mamba_block_fwd(s, w)[0] for s in seqs]
+    windows, states = pools(w, 6)
+    slots = [4, 0, 2]
+    first = [5, 100, 33]
+    u = torch.cat([s[0, :v] for s, v in zip(seqs, first)])
+    out = block.mamba_block_packed(u, w, windows, states, i32([0, 5, 105, 138]), i32([-1] * 3), i32(slots))
+    got = list(out.split(first))
+    more = block.mamba_block_packed(seqs[1][0, 100:170].contiguous(), w, windows, states, i32([0, 70]), i32([0]))
+    got[1] = torch.cat([got[1], more])
+    for t in range(steps):
+        u = torch.stack([s[0, v + t] for s, v in zip(seqs, n)])
+        out = block.mamba_block_packed(u, w, windows, states, src=i32(slots))
+        got = [torch.cat([a, out[k:k + 1]]) for k, a in enumerate(got)]
+    for k in range(3):
+        assert rel(got[k], want[k]) <= BF16_BLOCK, k
+    for s in (1, 3, 5):  # slots of no request
+        assert bool((windows[s] == 3).all()) and bool((states[s] == 3).all())
+
+
+def test_shared_prefix():
+    """Two requests go on from one prefix's slot and end in their own."""
+    w = weights(seed=3)
+    g = torch.Generator().manual_seed(4)
+    prefix = torch.randn(40, w.M, generator=g).bfloat16().cuda()
+    tails = [torch.randn(v, w.M, generator=g).bfloat16().cuda() for v in (9, 20)]
+    windows, states = pools(w, 4)
+    block.mamba_block_packed(prefix, w, windows, states, i32([0, 40]), i32([-1]), i32([3]))
+    kept = windows[3].clone(), states[3].clone()
+    out = block.mamba_block_packed(torch.cat(tails), w, windows, states, i32([0, 9, 29]), i32([3, 3]), i32([0, 1]))
+    assert torch.equal(windows[3], kept[0]) and torch.equal(states[3], kept[1])
+    for part, tail in zip(out.split([9, 20]), tails):
+        want = block.mamba_block_fwd(torch.cat([prefix, tail])[None], w)[0, 40:]
+        assert rel(part, want) <= BF16_BLOCK
+
+
+def reference_block(u, h, N, R):
+    """The block in fp64 (differentiable): u (b, L, M), h the weights."""
+    E = h["W_out_t"].shape[0]
+    xz = u @ h["W_in_t"]
+    x, z = xz[..., :E], xz[..., E:]
+    W = h["conv_w"].shape[1]
+    pad = torch.nn.functional.pad(x, (0, 0, W - 1, 0))
+    a = h["conv_b"] + sum(h["conv_w"][:, k] * pad[:, k:k + x.shape[1]] for k in range(W))
+    xc = a * torch.sigmoid(a)
+    xd = xc @ h["W_x_t"]
+    B, C = xd[..., :N], xd[..., N:2 * N]
+    dt = torch.nn.functional.softplus(xd[..., 2 * N:2 * N + R] @ h["W_dt_t"] + h["b_dt"])
+    s, ys = torch.zeros(u.shape[0], E, N, dtype=torch.float64), []
+    for t in range(u.shape[1]):
+        e = dt[:, t, :, None] * h["A"]
+        s = torch.exp(e) * s + torch.expm1(e) / h["A"] * B[:, t, None, :] * xc[:, t, :, None]
+        ys.append((s * C[:, t, None, :]).sum(-1))
+    y = (torch.stack(ys, 1) + h["D"] * xc) * z * torch.sigmoid(z)
+    return y @ h["W_out_t"]
+
+
+def test_training_step():
+    """The block's backward against fp64 autograd."""
+    banner("block training step")
+    w = weights(M=48, E=96, N=16, R=3, seed=5)
+    g = torch.Generator().manual_seed(6)
+    u = torch.randn(2, 70, w.M, generator=g).bfloat16()
+    dout = torch.randn(2, 70, w.M, generator=g).bfloat16()
+    plain = block.mamba_block_fwd(u.cuda(), w)
+    out, saved = block.mamba_block_fwd(u.cuda(), w, train=True)
+    assert torch.equal(out, plain)
+    got = block.mamba_block_bwd(dout.cuda(), w, saved)
+    names = {"dW_in_t": "W_in_t", "dW_x_t": "W_x_t", "dW_dt_t": "W_dt_t", "dW_out_t": "W_out_t", "dconv_w": "conv_w",
+             "dconv_b": "conv_b", "db_dt": "b_dt", "dA": "A", "dD": "D"}
+    h = {v: getattr(w, v).double().cpu().requires_grad_() for v in names.values()}
+    u64 = u.double().requires_grad_()
+    ref = reference_block(u64, h, w.N, w.R)
+    assert rel(out, ref) <= BF16_BLOCK
+    (ref * dout.double()).sum().backward()
+    assert rel(got["du"], u64.grad) <= BF16_GRAD
+    for k, v in names.items():
+        want = h[v].grad
+        if k == "dW_x_t":  # columns behind B, C and dt are padding
+            assert bool((got[k][:, 2 * w.N + w.R:] == 0).all())
+        assert rel(got[k], want) <= BF16_GRAD, k
+
+
+def test_beam_advance():
+    """Pools of two layers follow the beams: against indexing copies of them."""
+    g = torch.Generator().manual_seed(7)
+    batch, beams, V = 3, 4, 777
+    pool = [torch.randn(14, 3, 10, generator=g).bfloat16().cuda(), torch.randn(14, 2, 20, 16, generator=g).cuda()[:, 1]]
+    before = [p.clone() for p in pool]
+    slots = torch.randperm(14, generator=g)[:12].view(batch, beams).to(torch.int32).cuda()
+    logits, scores = torch.randn(batch, beams, V, generator=g).cuda(), -torch.rand(batch, beams, generator=g).cuda()
+    s, t, p = block.beam_advance(logits, scores, slots, pool)
+    all_scores = (scores[..., None].double() + torch.log_softmax(logits.double(), -1)).flatten(1)
+    want = all_scores.topk(beams, -1)
+    assert torch.equal(p.long() * V + t.long(), want.indices) and float((s - want.values).abs().max()) < 1e-5
+    for a, b in zip(pool, before):
+        ref = b.clone()
+        ref[slots.long().view(-1)] = b[slots.gather(1, p.long()).long().view(-1)]
+        assert torch.equal(a, ref)
+
+
+def test_decode_in_a_graph():
+    """A decode step with beam search, captured once and replayed between eager work: every replay gives the bits of
+    the eager step."""
+    banner("decode graph")
+    w = weights(seed=8)
+    g = torch.Generator().manual_seed(9)
+    batch, beams, V = 4, 3, 500
+    head = (torch.randn(w.M, V, generator=g) / w.M ** 0.5).bfloat16().cuda()
+    emb = torch.randn(V, w.M, generator=g).bfloat16().cuda()
+    slots = torch.arange(batch * beams, dtype=torch.int32).flip(0).view(batch, beams).cuda()
+
+    def fresh():
+        gen = torch.Generator().manual_seed(10)
+        win, st = pools(w, batch * beams)
+        win.copy_(torch.randn(win.shape, generator=gen))
+        st.copy_(torch.randn(st.shape, generator=gen))
+        return [torch.randn(batch * beams, w.M, generator=gen).bfloat16().cuda(),
+                -torch.rand(batch, beams, generator=gen).cuda(), win, st]
+
+    def step(v):
+        out = block.mamba_block_packed(v[0], w, v[2], v[3], src=slots.view(-1))
+        s, t, p = block.beam_advance(torch.mm(out, head).view(batch, beams, V), v[1], slots, (v[2], v[3]))
+        v[0].copy_(emb[t.long().view(-1)])
+        v[1].copy_(s)
+        return t, p
+
+    eager, held = fresh(), fresh()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        warm = fresh()
+        step(warm)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(held)
+    for v, f in zip(held, fresh()):
+        v.copy_(f)
+    for k in range(5):
+        graph.replay()
+        want = step(eager)
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1]), k
+        for a, b in zip(held, eager):
+            assert torch.equal(a, b), k
+
+
+def test_two_graphs_of_prompts_at_once():
+    """Two captured scans of prompts, each with the workspace of its own capture, replayed on two streams together."""
+    D, N, T = 320, 16, 1500
+    gen = torch.Generator().manual_seed(11)
+    rnd = lambda *s: torch.randn(s, generator=gen).cuda()  # noqa: E731
+    A = -torch.arange(1.0, N + 1).repeat(D, 1).cuda()
+    starts = i32([0, 20, 1100, 1500])
+    runs = []
+    for _ in range(2):
+        t = [rnd(T, D), 0.1 * rnd(T, D).abs(), rnd(T, N), rnd(T, N), torch.zeros(3, D, N, device="cuda")]
+        want = ssm.selective_scan_packed(t[0], t[1], A, t[2], t[3], t[4], starts=starts)
+        state = t[4].clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            t[4].zero_()
+            y = ssm.selective_scan_packed(t[0], t[1], A, t[2], t[3], t[4], starts=starts)
+        runs.append((graph, t, y, want, state, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for graph, t, y, want, state, stream in runs:
+            with torch.cuda.stream(stream):
+                y.zero_()
+                graph.replay()
+        torch.cuda.synchronize()
+        for graph, t, y, want, state, stream in runs:
+            assert torch.equal(y, want) and torch.equal(t[4], state)
+
+
+def test_streams():
+    """Calls on a given stream, and two of them under way at once."""
+    D, N, T = 128, 16, 900
+    gen = torch.Generator().manual_seed(12)
+    rnd = lambda *s: torch.randn(s, generator=gen).cuda()  # noqa: E731
+    A, w = -torch.rand(D, N, generator=gen).cuda() - 0.1, rnd(D, 4)
+    x, dt, B, C = rnd(T, D), 0.1 * rnd(T, D).abs(), rnd(T, N), rnd(T, N)
+    starts = i32([0, 300, 900])
+    logits, scores, pool = rnd(2, 3, 5000), rnd(2, 3), rnd(5, 1000)
+    order = i32([1, 2, 3, 4, 0])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+
+    def all_ops(s):
+        st, win, p = torch.zeros(2, D, N, device="cuda"), torch.zeros(2, 3, D, device="cuda"), pool.clone()
+        if s is not None:
+            s.wait_stream(torch.cuda.current_stream())
+        y = ssm.causal_conv1d_packed(x, w, win, starts=starts, silu=True, stream=s)
+        o = [y, ssm.selective_scan_packed(x, dt, A, B, C, st, starts=starts, stream=s)]
+        o += list(ssm.beam_select(logits, scores, 4, stream=s)) + [ssm.state_move(p, order, stream=s)]
+        o += list(ssm.causal_conv1d_bwd(x[None], x[None], w, silu=True, stream=s).values())
+        return o + [st, win]
+
+    want = all_ops(None)
+    torch.cuda.synchronize()
+    got = [all_ops(s) for s in streams]
+    torch.cuda.synchronize()
+    for g in got:
+        for a, b in zip(g, want):
+            assert torch.equal(a, b)
