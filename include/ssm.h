@@ -715,7 +715,8 @@ typedef struct {
  *   windows : (slots, width - 1, dim) io        if SSM_HAS_STATES, innermost stride 1
  * Flags: SSM_HAS_BIAS, SSM_SILU, SSM_HAS_STARTS, SSM_HAS_STATES and, with it,
  * SSM_HAS_SRC, SSM_HAS_DST.  1 <= width <= 8; width 1 has no window (pool).
- * Limits (SSM_ERR_UNSUPPORTED otherwise): tokens < 2^30; 64 rows of x, y
+ * y may not overlap an input, nor the pool any other tensor.
+ * Limits (SSM_ERR_UNSUPPORTED otherwise): tokens < 2^30; dim < 2^28; 64 rows of x, y
  * or windows span less than 1 GiB; (seqs + ceil(tokens/32)) ceil(dim/256) < 2^24. */
 typedef struct {
   int64_t tokens, seqs, dim, width, slots;
@@ -746,17 +747,18 @@ typedef struct {
  * io is SSM_F32 or SSM_BF16.  Flags: SSM_HAS_Z, SSM_HAS_D, SSM_DISC_EULER,
  * SSM_DELTA_SOFTPLUS, SSM_HAS_DELTA_BIAS, SSM_HAS_STARTS, SSM_HAS_STATES and,
  * with it, SSM_HAS_SRC, SSM_HAS_DST.  dstate <= SSM_SCAN_MAX_DSTATE.
- * (exp(delta A) - 1) / A keeps its relative accuracy for single tokens, and for
- * sequences as long as |delta A| of 16 steps and 16 neighbouring channels stays
- * below 1/8 or an A among these channels is 0; elsewhere an input's part is off by
- * a few 2^-24 |B x / A|.  y of a sequence that is walked in pieces is off by up to
- * 2^-16 (BF16 y) or 2^-20 (F32) of sum |C h| besides; the states are not.
+ * (exp(delta A) - 1) / A is good to a few fp32 roundings for single tokens; for
+ * sequences, with the largest delta of 16 steps, to 2^-14 of itself where io is F32
+ * and 2^-11 where it is BF16 (smaller deltas among larger ones: to that of the
+ * largest).  y of a sequence that is walked in pieces is off by up to 2^-16 (BF16 y)
+ * or 2^-20 (F32) of sum |C h| besides; the states are not.
  * Workspace: ssm_selective_scan_packed_workspace_size bytes (may be 0), 256-byte
  * aligned, contents undefined; calls that may overlap in time need workspaces
  * of their own.
- * Limits (SSM_ERR_UNSUPPORTED otherwise): tokens < 2^30; 64 rows of x,
- * delta, z, y, B or C span less than 1 GiB; (seqs + 256) ceil(dim/64) < 2^24,
- * dim dstate < 2^28. */
+ * y may not overlap an input, nor the pool any other tensor.
+ * Limits (SSM_ERR_UNSUPPORTED otherwise): tokens < 2^30; 64 rows of x, delta, z or
+ * y, and 64 rows and one row's extent of B or C, span less than 1 GiB; (seqs +
+ * 256) ceil(dim/64) < 2^24, dim dstate < 2^28. */
 typedef struct {
   int64_t tokens, seqs, dim, dstate, slots;
   uint32_t flags;

@@ -35,10 +35,13 @@
 //
 // Forms, chosen for each tile of a wave (delta A of its steps and channels):
 //   small   all |delta A| < 1/8: expm1(u)/u by its Taylor polynomial; right for A = 0
-//   fast    no A = 0: h <- Abar (h + q) - q, q = B x / A (the update multiplied
-//           out), 8 issue slots a state and step with the readout; a term is off
-//           by the roundings of q, so `small` takes the small steps
-//   any     otherwise: (Abar - 1) / A, or the polynomial where |delta A| < 1/4
+//   fast    h <- Abar (h + q) - q, q = B x / A (the update multiplied out), 8 issue
+//           slots a state and step with the readout.  A term u q is off by the
+//           roundings of q, 2^-22 |q|, so it takes that every channel's largest
+//           delta and smallest |A| give |u| >= 2^-11 (bf16: terms are good to
+//           2^-11) or 2^-8 (fp32: to 2^-14)
+//   any     otherwise, A = 0 among it: (Abar - 1) / A, or the polynomial where
+//           |delta A| < 1/4; 17 issue slots
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -405,18 +408,21 @@ __global__ __launch_bounds__(64 * kWaves, NS <= 4 ? 4 : NS == 8 ? 2 : 1) void sc
 
   Lane<NS> ln;
   float h[NS], old[NS];
-  float amax = 0.f;
-  bool zero = false;
+  float amax = 0.f, amin = __builtin_inff();  // of |A|
 #pragma unroll
   for (int k = 0; k < NS; ++k) {
     const float a = k < nk ? p.A[dd * p.As_d + (n0 + k) * p.As_n] : -1.f;
     ln.A[k] = a;
     ln.iA[k] = a != 0.f ? 1.f / a : 0.f;
-    zero = zero || a == 0.f;
     amax = k < nk ? fmaxf(amax, fabsf(a)) : amax;
+    amin = k < nk ? fminf(amin, fabsf(a)) : amin;
     h[k] = old[k] = 0.f;
   }
-  const bool any_zero = __ballot(zero) != 0;
+  // of the channel
+  amax = fmaxf(amax, other<1>(amax));
+  amax = fmaxf(amax, other<2>(amax));
+  amin = fminf(amin, other<1>(amin));
+  amin = fminf(amin, other<2>(amin));
   const float Dk = p.Dskip && ch_ok ? p.Dskip[dd * p.Ds_d] : 0.f;
   const float bias = p.dbias && ch_ok ? p.dbias[dd * p.dbs_d] : 0.f;
   const bool vec = vec_state != 0;
@@ -480,13 +486,14 @@ __global__ __launch_bounds__(64 * kWaves, NS <= 4 ? 4 : NS == 8 ? 2 : 1) void sc
     wave_sync();
     const float* bc = lds[wave][buf][0][0] + n0;
     float y[4];
-    // the four lanes hold different steps and states: each one's largest delta and |A|
+    // the four lanes hold different steps
     tmax = fmaxf(tmax, other<1>(tmax));
     tmax = fmaxf(tmax, other<2>(tmax));
-    const int form = EULER ? kEuler
-                     : __ballot(!(tmax * amax < 0.125f * kLog2e)) == 0 ? kSmall
-                     : any_zero                                         ? kAny
-                                                                       : kFast;
+    constexpr float kNear = (BF16 ? 0x1p-11f : 0x1p-8f) * kLog2e;
+    const int form = EULER                                                     ? kEuler
+                     : __ballot(!(tmax * amax < 0.125f * kLog2e)) == 0         ? kSmall
+                     : __ballot(tmax > 0.f && !(tmax * amin >= kNear)) == 0    ? kFast
+                                                                               : kAny;
     if constexpr (EULER) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -697,7 +704,8 @@ void launch_ns(const ScanPackedParams& p, hipStream_t stream) {
                    p.Bs_t * e % word == 0 && p.Cs_t * e % word == 0;
   if (!p.q.starts) {
     const int vec_a = p.N % NS == 0 && p.As_n == 1 && al(p.A, std::min(16, 4 * NS)) && p.As_d % std::min(4, NS) == 0;
-    // four sequences a wave where that leaves two workgroups a compute unit
+    // two sequences a wave where that leaves two workgroups a compute unit: 64 x 5120
+    // fp32 16.3 us one at a time, 13.2 with two, 13.6 with four
     constexpr int U = NS <= 4 ? 2 : 1;
     const unsigned groups = ((unsigned)p.q.seqs + U - 1) / U;
     if (U > 1 && nblk * groups >= 512)
@@ -742,11 +750,12 @@ ScanPackedPlan plan_scan_packed(int64_t tokens, int64_t seqs, int64_t dim, int64
   if (single) return pl;
   auto round256 = [](int64_t n) { return (n + 255) / 256 * 256; };
   // Three waves for each SIMD (four are resident).  Fewer, longer pieces leave them
-  // idle at the end, more are walked again: 16384 x 5120 bf16 at 2048 waves 646 us,
-  // 2560 492, 3072 495, 4096 498; 1111 x 1536 fp32 at 64 rows a piece 40 us, 128 46,
+  // idle at the end, more are walked again: 16384 x 5120 bf16 at 2 waves a SIMD
+  // 646 us, 2.5 492, 3 495, 4 498; 1111 x 1536 fp32 at 64 rows a piece 40 us, 128 46,
   // 256 54 (a wave walks 16 rows in 2 to 3 us).
+  constexpr int64_t kSimds = 256 * 4;
   const int64_t waves = (dim + kCh - 1) / kCh;
-  int64_t step = (tokens * waves / 3072 + kTile - 1) / kTile * kTile;
+  int64_t step = (tokens * waves / (3 * kSimds) + kTile - 1) / kTile * kTile;
   step = std::max<int64_t>(step, 64);
   step = std::max<int64_t>(step, ((tokens + 254) / 255 + kTile - 1) / kTile * kTile);  // at most 255 lines
   pl.step = step;

@@ -23,9 +23,10 @@ bool rows_fit(const ssm_tensor_desc& t, int dim, int64_t rows) {
   return (rows * (__int128)st + 64) * esize(t.dtype) < kMaxSpan;
 }
 
-// A row's own elements, addressed from the same base: `width` of them, `sn` apart.
-bool width_fits(int64_t width, int64_t sn, int32_t dtype) {
-  return ((__int128)width * sn + 64) * esize(dtype) < kMaxSpan;
+// The same for rows of `width` elements that lie `sn` apart.
+bool rows_fit(const ssm_tensor_desc& t, int dim, int64_t rows, int64_t width, int64_t sn) {
+  const int64_t st = t.shape[dim] > 1 ? t.stride[dim] : 0;
+  return (rows * (__int128)st + (__int128)width * sn + 64) * esize(t.dtype) < kMaxSpan;
 }
 
 // The row stride of an output that a kernel drops rows behind the last from.
@@ -96,7 +97,7 @@ ssm_status validate_conv_packed(const ssm_conv_packed_desc* d, const ssm_conv_pa
   SSM_TRY(check_out(true, d->y, 2, td, d->y.dtype == io || d->y.dtype == SSM_F32, true, false));
   SSM_TRY(check_out(pool, d->windows, 3, win, d->windows.dtype == io, true, false));
   if (!rows_fit(d->x, 0, 64) || !rows_fit(d->y, 0, 64) || (pool && !rows_fit(d->windows, 1, 64)) ||
-      !width_fits(d->dim, 1, SSM_F32))
+      d->dim >= ((int64_t)1 << 28))
     return SSM_ERR_UNSUPPORTED;
   Ptrs a;
   SSM_TRY(a.in(true, d->x, p->x));
@@ -147,11 +148,10 @@ ssm_status validate_scan_packed(const ssm_scan_packed_desc* d) {
   // a slot is one contiguous (dim, dstate) block
   if (pool && ((d->dstate > 1 && d->states.stride[2] != 1) || (d->dim > 1 && d->states.stride[1] != d->dstate)))
     return SSM_ERR_STRIDE;
-  for (const ssm_tensor_desc* t : {&d->x, &d->delta, &d->y, &d->B, &d->C})
+  for (const ssm_tensor_desc* t : {&d->x, &d->delta, &d->y})
     if (!rows_fit(*t, 0, 64)) return SSM_ERR_UNSUPPORTED;
   if ((f & SSM_HAS_Z) && !rows_fit(d->z, 0, 64)) return SSM_ERR_UNSUPPORTED;
-  if (!width_fits(d->dim, 1, SSM_F32) || !width_fits(d->dstate, d->B.stride[1], io) ||
-      !width_fits(d->dstate, d->C.stride[1], io))
+  if (!rows_fit(d->B, 0, 64, d->dstate, d->B.stride[1]) || !rows_fit(d->C, 0, 64, d->dstate, d->C.stride[1]))
     return SSM_ERR_UNSUPPORTED;
   return SSM_OK;
 }

@@ -120,6 +120,27 @@ def test_small_steps_keep_their_accuracy():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_wide_ranges_of_decay(dtype):
+    """Channels and states whose decays are orders of magnitude apart, side by side in a wave: each keeps its accuracy.
+    A term is good to 2^-14 (fp32) or 2^-11 (bf16) at the channel's largest step, and every step is the same here; 120
+    additions and decays add 240 roundings."""
+    T, D, N = 120, 32, 16
+    g = torch.Generator().manual_seed(61)
+    v = make(62, T, D, N, 2, TYPES[dtype], z=False, A=-(10 ** (torch.rand(D, N, generator=g) * 6 - 4)))
+    step = 10 ** (torch.rand(D, generator=g) * 4 - 4)
+    v["delta"] = step.expand(T, D).to(TYPES[dtype])
+    v["D"], v["states"] = torch.zeros(D), torch.zeros(2, D, N)
+    out, pool = run(v, [0, T], [-1], [1], softplus=False)
+    _, h, _, _ = ref.scan(v["x"], v["delta"], v["A"], v["B"], v["C"])
+    u = v["delta"][0].double()[:, None] * v["A"].double()
+    mag = torch.zeros(D, N, dtype=torch.float64)
+    for t in range(T):
+        mag = torch.exp(u) * mag + (torch.expm1(u) / v["A"].double() * v["B"][t].double() *
+                                    v["x"][t].double()[:, None]).abs()
+    check(pool[1], h, mag, (2.0 ** -11 if dtype == "bf16" else 2.0 ** -14) + 240 * ref.U, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("S,D,N", [(1, 16, 16), (64, 80, 16), (3, 33, 4), (7, 130, 1), (5, 20, 64), (9, 17, 13),
                                    (2, 64, 32), (4, 8, 8)])
 def test_single_tokens(dtype, S, D, N):
@@ -255,3 +276,36 @@ def test_far_rows_and_slots():
                                     dst=i([1, 0]), D=g["D"], z=g["z"][:2], delta_softplus=True,
                                     delta_bias=g["delta_bias"])
     compare(out, pool, v2, None, [2, 0], [1, 0])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_more_pieces_than_run_at_once(dtype):
+    """Sequences of very different lengths over many channels: the pieces are taken longest first.  Channels do not
+    meet, so a few of them show all."""
+    T, D, N = 16400, 1040, 16
+    banner("ordered pieces %s" % dtype)
+    g = torch.Generator().manual_seed(81)
+    starts = [0] + sorted(torch.randint(0, T + 1, (69,), generator=g).tolist()) + [T]
+    seqs = len(starts) - 1
+    v = make(82, T, D, N, seqs, TYPES[dtype])
+    v["states"] = torch.randn(seqs, D, N, generator=g)
+    src = [s if s % 3 else -1 for s in range(seqs)]
+    out, pool = run(v, starts, src, list(range(seqs)))
+    keep = torch.tensor(list(range(0, D, 97)) + [15, 16, 63, 64, D - 17, D - 16, D - 1])
+    cut = {k: None if t is None else t[keep] if k in ("A", "D", "delta_bias") else
+           t[:, keep] if k in ("x", "delta", "z", "states") else t for k, t in v.items()}
+    compare(out.cpu()[:, keep], pool.cpu()[:, keep], cut, starts, src, list(range(seqs)))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [16, 5, 1])
+@pytest.mark.parametrize("euler", [False, True])
+def test_many_single_tokens(dtype, N, euler):
+    """Enough of them that a wave takes two, and one too many for that."""
+    S, D = 65, 1100
+    banner("single tokens %d x %d x %d %s" % (S, D, N, dtype))
+    v = make(83, S, D, N, S + 3, TYPES[dtype])
+    src = [-1 if s == 64 else (s * 7) % S + 2 for s in range(S)]
+    dst = [(s * 7) % S + 2 if s % 9 else -1 for s in range(S)]
+    out, pool = run(v, None, src, dst, euler=euler)
+    compare(out, pool, v, None, src, dst, euler=euler)
