@@ -48,7 +48,7 @@ def compare(got, logits, scores, k):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("batch,beams,V,k", [(1, 1, 1, 1), (2, 3, 7, 5), (1, 1, 1000, 1), (3, 4, 1025, 8), (2, 2, 65, 64),
                                              (1, 16, 4097, 32), (5, 1, 9000, 64), (64, 5, 2100, 10), (2, 4, 50281, 8),
-                                             (1, 3, 131, 64), (300, 16, 1030, 3)])
+                                             (1, 3, 131, 64), (300, 16, 1030, 3), (40, 8, 20000, 6)])
 def test_random(dtype, batch, beams, V, k):
     banner("beam %s" % ((batch, beams, V, k, dtype),))
     g = torch.Generator().manual_seed(V + k)
