@@ -125,9 +125,9 @@ def beam_advance(logits, scores, slots, pools):
     the beam it continues.  pools: the windows and states of every layer.  Returns
     (scores, tokens, parents), each (batch, beams)."""
     scores, tokens, parents = beam_select(logits, scores, slots.shape[1])
-    src = slots.gather(1, parents.long()).view(-1)
+    src, dst = slots.gather(1, parents.long()).view(-1), slots.reshape(-1)
     for pool in pools:
-        state_move(pool, src, slots.view(-1))
+        state_move(pool, src, dst)
     return scores, tokens, parents
 
 

@@ -425,6 +425,7 @@ __global__ __launch_bounds__(64 * kWaves, NS <= 4 ? 4 : NS == 8 ? 2 : 1) void sc
   amin = fminf(amin, other<2>(amin));
   const float Dk = p.Dskip && ch_ok ? p.Dskip[dd * p.Ds_d] : 0.f;
   const float bias = p.dbias && ch_ok ? p.dbias[dd * p.dbs_d] : 0.f;
+  const uint64_t alive = __ballot(ch_ok);
   const bool vec = vec_state != 0;
   if constexpr (AGAIN) {
     enter<NS>(p, ln, seq.begin / p.step + 1, line, own, dd, nk, vec, h);
@@ -492,7 +493,7 @@ __global__ __launch_bounds__(64 * kWaves, NS <= 4 ? 4 : NS == 8 ? 2 : 1) void sc
     constexpr float kNear = (BF16 ? 0x1p-11f : 0x1p-8f) * kLog2e;
     const int form = EULER                                                     ? kEuler
                      : __ballot(!(tmax * amax < 0.125f * kLog2e)) == 0         ? kSmall
-                     : __ballot(tmax > 0.f && !(tmax * amin >= kNear)) == 0    ? kFast
+                     : (__ballot(!(tmax * amin >= kNear)) & alive) == 0        ? kFast
                                                                                : kAny;
     if constexpr (EULER) {
 #pragma unroll

@@ -151,8 +151,8 @@ def state_move(pool, src, dst=None, stream=None):
     plan = _l._plans.get(key)
     tensors = (pool, src, dst)
     if plan is None:
-        if pool.dim() < 2:
-            raise ValueError("state_move: pool is (slots, ...)")
+        if pool.dim() < 2 or pool.shape[0] == 0:
+            raise ValueError("state_move: pool is (slots, ...), at least one")
         row = pool.flatten(1) if pool[0].is_contiguous() else None
         if row is None or row.data_ptr() != pool.data_ptr():
             raise ValueError("state_move: a slot of the pool must be contiguous")

@@ -309,3 +309,28 @@ def test_many_single_tokens(dtype, N, euler):
     dst = [(s * 7) % S + 2 if s % 9 else -1 for s in range(S)]
     out, pool = run(v, None, src, dst, euler=euler)
     compare(out, pool, v, None, src, dst, euler=euler)
+
+
+def test_no_steps_and_a_hair_of_decay():
+    """A channel whose |A| is next to nothing and whose steps are zero keeps its state, next to channels that decay."""
+    T, D, N = 40, 16, 4
+    v = make(84, T, D, N, 1, torch.float32, z=False)
+    v["A"] = torch.full((D, N), -40.0)
+    v["A"][3] = -torch.tensor([1e-38, 1e-39, 2.0 ** -126, 1.0])
+    v["x"] = v["x"] + 9
+    v["delta"] = torch.full((T, D), 0.5)
+    v["delta"][:, 3] = 0
+    v["D"] = torch.zeros(D)
+    out, pool = run(v, [0, T], None, None, softplus=False)
+    assert torch.equal(pool[0, 3].cpu(), v["states"][0, 3])
+    compare(out, pool, v, [0, T], [0], [0], softplus=False, dt_min=0.5, a_min=1.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_smallest(dtype):
+    """One token, one channel, one state: as a sequence and as a token."""
+    for starts in ([0, 1], None):
+        for src in (None, [-1]):
+            v = make(85, 1, 1, 1, 1, TYPES[dtype])
+            out, pool = run(v, starts, src, [0])
+            compare(out, pool, v, starts, src, [0])
