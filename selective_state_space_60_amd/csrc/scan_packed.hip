@@ -45,6 +45,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "serve_device.h"
 
@@ -752,12 +753,17 @@ ScanPackedPlan plan_scan_packed(int64_t tokens, int64_t seqs, int64_t dim, int64
   auto round256 = [](int64_t n) { return (n + 255) / 256 * 256; };
   // Three waves for each SIMD (four are resident).  Fewer, longer pieces leave them
   // idle at the end, more are walked again: 16384 x 5120 bf16 at 2 waves a SIMD
-  // 646 us, 2.5 492, 3 495, 4 498; 1111 x 1536 fp32 at 64 rows a piece 40 us, 128 46,
-  // 256 54 (a wave walks 16 rows in 2 to 3 us).
+  // 646 us, 2.5 492, 3 495, 4 498.
   constexpr int64_t kSimds = 256 * 4;
   const int64_t waves = (dim + kCh - 1) / kCh;
   int64_t step = (tokens * waves / (3 * kSimds) + kTile - 1) / kTile * kTile;
-  step = std::max<int64_t>(step, 64);
+  // Where that many waves are not to be had, a wave walks 16 rows in 2.2 us in either
+  // pass, and a state is chained over four lines in 0.9 us: the least of 0.275 step +
+  // 0.22 tokens / step.  One sequence of 4000 x 128 fp32 takes 66 us at 16 rows a
+  // piece, 43 at 32, 38 at 64; 500 x 64 bf16 18, 19, 27; 1111 x 1536 fp32 in 37
+  // sequences 36 at 32, 40 at 64.
+  step = std::max(step, ((int64_t)std::sqrt(0.8 * (double)tokens) + kTile / 2) / kTile * kTile);
+  step = std::max<int64_t>(step, kTile);
   step = std::max<int64_t>(step, ((tokens + 254) / 255 + kTile - 1) / kTile * kTile);  // at most 255 lines
   pl.step = step;
   pl.lines = (tokens - 1) / step;
