@@ -2,10 +2,11 @@
 // (constexpr functions run on the device as well), so that the host can walk
 // every piece of a launch.
 //
-// The rows are cut by a grid of `step` rows.  A sequence's first piece runs to
-// the next grid line behind its start; every grid line inside a sequence starts
-// another.  So the host, which does not know the lengths, launches one piece
-// for each sequence and one for each grid line, whatever the sequences are.
+// The rows are cut by a grid of `step` rows.  A sequence of at most `step` rows
+// is one piece.  A longer one's first piece runs to the next grid line behind its
+// start, and every grid line inside it starts another.  So the host, which does
+// not know the lengths, launches one piece for each sequence and one for each grid
+// line, whatever the sequences are.
 #pragma once
 
 #include <stdint.h>
@@ -25,14 +26,15 @@ constexpr Run sequence(int start, int next, int tokens) {
 
 // The first piece of a sequence.
 constexpr Run first_piece(Run seq, int step) {
+  if (seq.end - seq.begin <= step) return seq;
   const int line = (seq.begin / step + 1) * step;
   return {seq.begin, seq.end < line ? seq.end : line};
 }
 
-// The piece from the grid line `at` on, for the sequence that has that row
-// inside (begin < at < end), else empty.
+// The piece from the grid line `at` on, for a sequence that is cut there (longer
+// than a step, begin < at < end), else empty.
 constexpr Run later_piece(Run seq, int at, int step) {
-  if (at <= seq.begin || at >= seq.end) return {at, at};
+  if (at <= seq.begin || at >= seq.end || seq.end - seq.begin <= step) return {at, at};
   return {at, seq.end < at + step ? seq.end : at + step};
 }
 
