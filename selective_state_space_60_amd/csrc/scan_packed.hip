@@ -465,9 +465,10 @@ __global__ __launch_bounds__(64 * kWaves, NS <= 4 ? 4 : NS == 8 ? 2 : 1) void sc
     }
     if (dsoftplus) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float v = softplus(dt[i] + bias);
-        dt[i] = 4 * i + j < left ? v : 0.f;  // past the piece nothing changes
+      for (int i = 0; i < 4; ++i) dt[i] = softplus(dt[i] + bias);
+      if (left < kTile) {  // uniform; past the piece nothing changes
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dt[i] = 4 * i + j < left ? dt[i] : 0.f;
       }
     }
     if (has_z) {
