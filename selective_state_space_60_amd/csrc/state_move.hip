@@ -1,6 +1,8 @@
 // Moves between the slots of a pool, in place and all at once, for gfx950:
 // pool[dst[i]] <- what pool[src[i]] held before.  Bound by HBM: a slot that
-// changes is read and written once.
+// changes is read and written once (the states of 64 x 4 beams of 5120 x 16 fp32, of
+// which half are other beams' copies: 15.3 us for 84 MB, 5.5 TB/s, part of it from the
+// last-level cache; forks of a window: 2.2 us, a launch).
 //
 // A workgroup owns a slice of every slot's row and all moves of it: it loads
 // every source's part into registers, waits for all of its threads, and then
