@@ -106,3 +106,20 @@ def test_deterministic_and_graph():
         torch.cuda.synchronize()
         for name in first:
             assert torch.equal(held[name], first[name]) and torch.equal(eager[name], first[name]), (k, name)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_expanded_gradient_and_neighbours(dtype):
+    """dy of a plain sum (one row for all), and a batch element of NaN next to others: their dx stays theirs."""
+    g = torch.Generator().manual_seed(31)
+    b, L, D, W = 3, 70, 48, 4
+    x = torch.randn(b, L, D, generator=g).to(dtype)
+    w, bias = torch.randn(D, W, generator=g), torch.randn(D, generator=g)
+    row = torch.randn(D, generator=g).to(dtype)
+    got = ssm.causal_conv1d_bwd(row.cuda().expand(b, L, D), x.cuda(), w.cuda(), bias.cuda(), silu=True)
+    want = ssm.causal_conv1d_bwd(row.expand(b, L, D).contiguous().cuda(), x.cuda(), w.cuda(), bias.cuda(), silu=True)
+    for k in want:
+        assert torch.equal(got[k], want[k]), k
+    x[1] = float("nan")
+    bad = ssm.causal_conv1d_bwd(row.cuda().expand(b, L, D), x.cuda(), w.cuda(), bias.cuda(), silu=True)
+    assert torch.equal(bad["dx"][0], want["dx"][0]) and torch.equal(bad["dx"][2], want["dx"][2])

@@ -166,3 +166,24 @@ def test_far_rows():
     out = ssm.causal_conv1d_packed(gx, w.cuda(), pool, starts=i(starts), src=i(src), dst=i(dst), bias=b.cuda(), silu=True)
     torch.cuda.synchronize()
     compare(out, pool, x, w, b, win, starts, src, dst)
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("f32", 33)])
+def test_neighbours_do_not_meet(dtype, D):
+    """NaN and infinities in other sequences, in rows of none and in other slots reach nothing."""
+    W, S = 4, len(STARTS) - 1
+    x, w, b, win = make(21, STARTS[-1] + 40, D, W, 2 * S, TYPES[dtype])
+    src, dst = [s if s % 2 else -1 for s in range(S)], [S + s for s in range(S)]
+    for bad in (0, 1):
+        clean, clean_win = run(x, w, b, win, STARTS, src, dst)
+        px, pwin = x.clone(), win.clone()
+        px[STARTS[-1]:] = float("nan")
+        for s in range(S):
+            if s % 2 == bad:
+                px[STARTS[s]:STARTS[s + 1]] = float("inf") if s % 3 else float("nan")
+                pwin[s] = float("nan")
+        out, gw = run(px, w, b, pwin, STARTS, src, dst)
+        for s in range(S):
+            if s % 2 != bad:
+                assert torch.equal(out[STARTS[s]:STARTS[s + 1]], clean[STARTS[s]:STARTS[s + 1]]), s
+                assert torch.equal(gw[S + s], clean_win[S + s]), s

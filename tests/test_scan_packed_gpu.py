@@ -334,3 +334,31 @@ def test_smallest(dtype):
             v = make(85, 1, 1, 1, 1, TYPES[dtype])
             out, pool = run(v, starts, src, [0])
             compare(out, pool, v, starts, src, [0])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("single", [False, True])
+def test_neighbours_do_not_meet(dtype, single):
+    """NaN and infinities in other sequences and other slots reach nothing."""
+    D, N = 40, 16
+    starts = None if single else STARTS
+    S = 33 if single else len(STARTS) - 1
+    at = list(range(S + 1)) if single else STARTS
+    v = make(86, at[-1], D, N, 2 * S, TYPES[dtype])
+    src, dst = [s if s % 4 < 2 else -1 for s in range(S)], [S + s for s in range(S)]
+    clean, clean_pool = run(v, starts, src, dst)
+    for bad in (0, 1):
+        p = dict(v)
+        for k in ("x", "delta", "z", "B", "C", "states"):
+            p[k] = v[k].clone()
+        for s in range(S):
+            if s % 2 == bad:
+                for k in ("x", "z", "B", "C"):
+                    p[k][at[s]:at[s + 1]] = float("inf") if s % 3 else float("nan")
+                p["delta"][at[s]:at[s + 1]] = float("nan") if s % 3 else 30.0
+                p["states"][s] = float("nan")
+        out, pool = run(p, starts, src, dst)
+        for s in range(S):
+            if s % 2 != bad:
+                assert torch.equal(out[at[s]:at[s + 1]], clean[at[s]:at[s + 1]]), s
+                assert torch.equal(pool[S + s], clean_pool[S + s]), s
