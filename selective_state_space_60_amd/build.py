@@ -6,6 +6,8 @@ import os
 import subprocess
 import sys
 import sysconfig
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -19,7 +21,7 @@ HEADERS = ["ssm_internal.h", "layer_internal.h", "abi_checks.h", "column_sums.h"
            os.path.join("..", "..", "include", "ssm.h")]
 
 # Packed fp32 VALU ops are kept out of all device code.
-HIPCC_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared", "-Wall",
+HIPCC_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",
                "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 
 
@@ -46,12 +48,8 @@ def build_marshal() -> str:
     return MARSHAL
 
 
-def build(verbose: bool = False) -> str:
-    """Compile every source into libssm.so and _marshal.so (always recompiles)."""
-    build_marshal()
-    srcs = [os.path.join(CSRC, s) for s in SOURCES]
-    tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [hipcc()] + HIPCC_FLAGS + ["-I", os.path.join(HERE, "..", "include")] + srcs + ["-o", tmp]
+def run(cmd: list, verbose: bool) -> None:
+    """One call of hipcc; RuntimeError with its output where it fails."""
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     res = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
@@ -61,6 +59,20 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError("hipcc failed:\n" + out)
     if verbose and out.strip():
         print(out, file=sys.stderr)
+
+
+def build(verbose: bool = False) -> str:
+    """Compile every source into libssm.so and _marshal.so (always recompiles)."""
+    build_marshal()
+    tmp = LIB + ".tmp%d" % os.getpid()
+    with tempfile.TemporaryDirectory() as objs, ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+        outs = [os.path.join(objs, os.path.splitext(s)[0] + ".o") for s in SOURCES]
+        flags = HIPCC_FLAGS + ["-I", os.path.join(HERE, "..", "include")]
+        # one compiler for each source, side by side (the longest takes two minutes)
+        for job in [pool.submit(run, [hipcc()] + flags + ["-c", os.path.join(CSRC, s), "-o", o], verbose)
+                    for s, o in zip(SOURCES, outs)]:
+            job.result()
+        run([hipcc(), "--offload-arch=gfx950", "-fPIC", "-shared"] + outs + ["-o", tmp], verbose)
     os.replace(tmp, LIB)
     return LIB
 

@@ -163,9 +163,10 @@ __global__ __launch_bounds__(64 * kWaves) void beam_piece_kernel(BeamParams p) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
   __shared__ float2 stat[kWaves];
   __shared__ int count[kWaves];
-  const int64_t job = blockIdx.x;
-  const int part = (int)(job % p.parts) * kWaves + wave;
-  const int64_t row = job / p.parts, b = row / p.beams, n = row % p.beams;
+  // (32-bit quotients: a 64-bit one is a hundred operations in front of the loads)
+  const uint32_t job = blockIdx.x, row = job / (uint32_t)p.parts;
+  const int part = (int)(job - row * (uint32_t)p.parts) * kWaves + wave;
+  const int64_t b = row / (uint32_t)p.beams, n = row - (uint32_t)b * (uint32_t)p.beams;
   constexpr int ES = F32 ? 4 : 2;
   const char* const at = (const char*)p.logits + (b * p.ls_b + n * p.ls_n) * ES;
   const int V = (int)p.V, base = part * (64 * E);
@@ -241,7 +242,7 @@ __global__ __launch_bounds__(64 * kWaves) void beam_piece_kernel(BeamParams p) {
 #pragma unroll 4
     for (int i = 0; i < m; ++i) rank += hi[w][i] > mh || (hi[w][i] == mh && lo[w][i] > ml);
   }
-  uint64_t* const cand = p.cand + job * p.k;
+  uint64_t* const cand = p.cand + (int64_t)job * p.k;
   if (lane < held.held && rank < p.k) cand[rank] = (uint64_t)mh << 32 | ml;
   if (threadIdx.x < 64) {
     int all = 0;
