@@ -5,9 +5,8 @@
 //   <- the last W - 1 rows of [window, sequence].
 // Bound by HBM: each x is read once, each y written once (16384 x 5120 bf16 in 24
 // sequences, W 4: 75 us, 4.5 TB/s).  One token of each of 64 sequences of 5120
-// channels takes 6.7 us, of which the launch is 2.2, the bytes 1.1 and the rest the
-// chain of loads: the slot, its window, the sum.  A workgroup takes one
-// piece (packed_pieces.h) of up to TS rows and NT * V channels; a thread owns V
+// channels takes 6.5 us, of which a launch is 2.2 and the bytes 1.1.  A workgroup
+// takes one piece (packed_pieces.h) of up to TS rows and NT * V channels; a thread owns V
 // consecutive channels, loads its rows and the W - 1 in front of them at once
 // and slides the window in registers.  Rows of other sequences and rows that do
 // not exist come back as zeros from the buffer's range, so no load sits behind
@@ -149,7 +148,7 @@ __device__ __forceinline__ void convolve(const ConvPackedParams& p, const Chan<V
   }
 }
 
-// TS rows of a piece at most; TS 1: every row is a sequence.
+// TS rows of a piece at most.
 template <bool BF16, int V, int W, int TS>
 __global__ __launch_bounds__(NT) void conv_packed_kernel(ConvPackedParams p, unsigned nchb) {
   constexpr int E = BF16 ? 2 : 4;
@@ -157,12 +156,12 @@ __global__ __launch_bounds__(NT) void conv_packed_kernel(ConvPackedParams p, uns
   Chan<V, W> ch;
   ch.c0 = (int64_t)(blockIdx.x % nchb) * (NT * V);
   ch.lane = (int)threadIdx.x * V;
-  const bool first = TS == 1 || piece < p.q.seqs;
+  const bool first = piece < p.q.seqs;
   int s = piece, t0, end;
   packed::Run seq;
   if (first) {
     seq = sequence_of(p.q, s);
-    const packed::Run r = TS == 1 ? seq : packed::first_piece(seq, TS);
+    const packed::Run r = packed::first_piece(seq, TS);
     t0 = r.begin;
     end = r.end;
   } else {
@@ -199,7 +198,7 @@ __global__ __launch_bounds__(NT) void conv_packed_kernel(ConvPackedParams p, uns
     }
   }
   if (end > t0) convolve<BF16, V, W, TS>(p, ch, seq.begin, t0, end, win);
-  if (TS > 1 && pool && end < seq.end && end - seq.begin < W - 1)
+  if (pool && end < seq.end && end - seq.begin < W - 1)
     convolve<BF16, V, W, TS>(p, ch, seq.begin, end, seq.end < end + TS ? seq.end : end + TS, win);
   if (to >= 0) {
     const __amdgpu_buffer_rsrc_t out = window_buffer<BF16, W>(p, to, ch.c0);
@@ -209,12 +208,48 @@ __global__ __launch_bounds__(NT) void conv_packed_kernel(ConvPackedParams p, uns
   }
 }
 
+// One token of each sequence.  The slot is asked for first, then all that does not
+// depend on it, so that the window is the only load that waits for another (64 x 5120
+// bf16: 6.5 us; as pieces of one row each, 6.7).
+template <bool BF16, int V, int W>
+__global__ __launch_bounds__(NT) void conv_token_kernel(ConvPackedParams p, unsigned nchb) {
+  constexpr int E = BF16 ? 2 : 4;
+  const int s = (int)(blockIdx.x / nchb);
+  Chan<V, W> ch;
+  ch.c0 = (int64_t)(blockIdx.x % nchb) * (NT * V);
+  ch.lane = (int)threadIdx.x * V;
+  if (ch.c0 + ch.lane >= p.D) return;
+  const Slots slot = slots_of(p.q, s, p.w);  // no pool: no slots
+  Row<BF16, V> rows[W];
+  rows[W - 1] = load_row<BF16, V>(rsrc((const char*)p.x + ((int64_t)s * p.xs_t + ch.c0) * E, kFar), (uint32_t)(ch.lane * E));
+  load_taps<V, W>(p.w, ch.c0 + ch.lane, p.ws_d, p.ws_k, ch.w);
+#pragma unroll
+  for (int v = 0; v < V; ++v) ch.b[v] = p.bias ? p.bias[(ch.c0 + ch.lane + v) * p.bs_d] : 0.f;
+  const uint32_t lane_w = (uint32_t)(ch.lane * E), row_w = (uint32_t)(p.wins_t * E);
+  const __amdgpu_buffer_rsrc_t win = window_buffer<BF16, W>(p, slot.from, ch.c0);
+#pragma unroll
+  for (int k = 0; k < W - 1; ++k) rows[k] = load_row<BF16, V>(win, lane_w + (uint32_t)k * row_w);
+  float o[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    float acc = ch.b[v];
+#pragma unroll
+    for (int k = 0; k < W; ++k) acc = __builtin_fmaf(ch.w[v][k], elem<BF16, V>(rows[k], v), acc);
+    o[v] = p.silu ? acc * sigmoid(acc) : acc;
+  }
+  const int YE = p.y_f32 ? 4 : 2;
+  store_y<V>(rsrc((char*)p.y + ((int64_t)s * p.ys_t + ch.c0) * YE, kFar), (uint32_t)(ch.lane * YE), o, p.y_f32);
+  // what has no slot goes out of the buffer's range
+  const __amdgpu_buffer_rsrc_t out = window_buffer<BF16, W>(p, slot.to, ch.c0);
+#pragma unroll
+  for (int k = 0; k < W - 1; ++k) store_raw<BF16, V>(out, lane_w + (uint32_t)k * row_w, rows[k + 1]);
+}
+
 template <bool BF16, int V, int W>
 void launch_w(const ConvPackedParams& p, hipStream_t stream) {
   const unsigned nchb = (unsigned)((p.D + (int64_t)NT * V - 1) / ((int64_t)NT * V));
   if (!p.q.starts) {
-    hipLaunchKernelGGL((conv_packed_kernel<BF16, V, W, 1>), dim3(nchb * (unsigned)p.q.seqs), dim3(NT), 0, stream, p,
-                       nchb);
+    hipLaunchKernelGGL((conv_token_kernel<BF16, V, W>), dim3(nchb * (unsigned)p.q.seqs), dim3(NT), 0, stream, p, nchb);
   } else {
     const unsigned n = (unsigned)packed::pieces(p.q.tokens, p.q.seqs, kTS);
     hipLaunchKernelGGL((conv_packed_kernel<BF16, V, W, kTS>), dim3(nchb * n), dim3(NT), 0, stream, p, nchb);

@@ -656,16 +656,13 @@ __global__ __launch_bounds__(64 * kWaves) void step_packed_kernel(ScanPackedPara
   };
   float h[U][NS], B[U][NS], C[U][NS], x[U], dt[U], z[U], A[NS];
   int64_t to[U];
+  Slots slot[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     // the last sequence again where there are no U left: its results are not stored twice
     const int s = s0 + u < p.q.seqs ? s0 + u : p.q.seqs - 1;
-    const Slots slot = slots_of(p.q, s, p.A);
-    const int64_t from = slot.from;
-    to[u] = s0 + u < p.q.seqs ? slot.to : -1;
-#pragma unroll
-    for (int k = 0; k < NS; ++k) h[u][k] = 0.f;
-    if (from >= 0) load_block<NS>(p.states + from * p.sts_s + own, nk, vec, h[u]);
+    slot[u] = slots_of(p.q, s, p.A);
+    to[u] = s0 + u < p.q.seqs ? slot[u].to : -1;
     x[u] = at(p.x, s * p.xs_t + dd);
     dt[u] = at(p.delta, s * p.ds_t + dd);
     z[u] = p.z ? at(p.z, s * p.zs_t + dd) : 0.f;
@@ -675,6 +672,13 @@ __global__ __launch_bounds__(64 * kWaves) void step_packed_kernel(ScanPackedPara
   load_row<false, NS>(p.A, dd * p.As_d, p.As_n, n0, nk, vec_a, A);
   const float Dk = p.Dskip ? p.Dskip[dd * p.Ds_d] : 0.f;
   const float bias = p.dbias ? p.dbias[dd * p.dbs_d] : 0.f;
+  // all that needs no slot is on its way by now
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+#pragma unroll
+    for (int k = 0; k < NS; ++k) h[u][k] = 0.f;
+    if (slot[u].from >= 0) load_block<NS>(p.states + slot[u].from * p.sts_s + own, nk, vec, h[u]);
+  }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     float v = dt[u];
