@@ -359,22 +359,25 @@ __device__ __forceinline__ void wave_sync() {
 
 // The state at grid line `line` of a sequence that crosses line `first` first:
 // from that line's state on, each piece's end state and the decay over the piece
-// applied to the state before it.  Four lines are asked for at a time.
+// applied to the state before it.  Latency is all there is: several lines are
+// asked for at a time.
 template <int NS>
 __device__ __forceinline__ void enter(const ScanPackedParams& p, const Lane<NS>& ln, int first, int line, int64_t own,
                                       int64_t d, int nk, bool vec, float (&h)[NS]) {
+  constexpr int kLines = NS <= 4 ? 12 : 8;
   const int64_t words = p.D * p.N;
   load_block<NS>(p.H + (int64_t)(first - 1) * words + own, nk, vec, h);
-  for (int l0 = first + 1; l0 <= line; l0 += 4) {
-    float e[4][NS], sum[4];
+#pragma unroll 1
+  for (int l0 = first + 1; l0 <= line; l0 += kLines) {
+    float e[kLines][NS], sum[kLines];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kLines; ++i) {
       const int64_t l = (l0 + i < line ? l0 + i : line) - 1;
       load_block<NS>(p.H + l * words + own, nk, vec, e[i]);
       sum[i] = p.dsum[l * p.D + d];
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kLines; ++i)
       if (l0 + i <= line)
 #pragma unroll
         for (int k = 0; k < NS; ++k) h[k] = __builtin_fmaf(__builtin_amdgcn_exp2f(ln.A[k] * sum[i]), h[k], e[i][k]);
@@ -769,11 +772,11 @@ ScanPackedPlan plan_scan_packed(int64_t tokens, int64_t seqs, int64_t dim, int64
   constexpr int64_t kSimds = 256 * 4;
   const int64_t waves = (dim + kCh - 1) / kCh;
   int64_t step = (tokens * waves / (3 * kSimds) + kTile - 1) / kTile * kTile;
-  // Where that many waves are not to be had, a wave walks 16 rows in 2.2 us in either
-  // pass, and a state is chained over four lines in 0.9 us: the least of 0.275 step +
-  // 0.22 tokens / step.  One sequence of 4000 x 128 fp32 takes 66 us at 16 rows a
-  // piece, 43 at 32, 38 at 64; 500 x 64 bf16 18, 19, 27; 1111 x 1536 fp32 in 37
-  // sequences 36 at 32, 40 at 64.
+  // Where that many waves are not to be had, the rows that a wave walks in either pass
+  // (16 in 2.2 us) stand against the lines that it chains a state over: about
+  // sqrt(0.8 tokens) rows a piece.  4000 x 128 fp32: 33.8 us at its 64 rows, 32.8 at 48;
+  // 2000 x 768 bf16: 35.3 at its 48, 38.0 at 32; 500 x 64 bf16: 16.3 at its 16, and 26.7
+  // at 64 (chained four lines at a time).
   step = std::max(step, ((int64_t)std::sqrt(0.8 * (double)tokens) + kTile / 2) / kTile * kTile);
   step = std::max<int64_t>(step, kTile);
   step = std::max<int64_t>(step, ((tokens + 254) / 255 + kTile - 1) / kTile * kTile);  // at most 255 lines
