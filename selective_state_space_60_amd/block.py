@@ -25,6 +25,7 @@ import torch
 from . import (beam_select, causal_conv1d, causal_conv1d_bwd, causal_conv1d_packed, gated_scan_bwd, gated_scan_ckpt,
                gated_scan_fwd, gated_state_update, rms_norm, rms_norm_bwd, scan_ckpt, selective_scan_bwd,
                selective_scan_fwd, selective_scan_packed, state_move, w4_matvec, w4_quantize)
+from .serve import MOVE_MAX_MOVES
 
 
 class BlockWeights:
@@ -121,13 +122,15 @@ def mamba_block_packed(u, w: BlockWeights, windows, states, starts=None, src=Non
 def beam_advance(logits, scores, slots, pools):
     """A beam search's step: from logits (batch, beams, vocab) and scores (batch,
     beams) fp32 the `beams` best continuations of every batch element, and the
-    pools' slots moved so that beam n's slot slots[b, n] (int32) holds the state of
-    the beam it continues.  pools: the windows and states of every layer.  Returns
-    (scores, tokens, parents), each (batch, beams)."""
+    pools' slots moved so that beam n's slot slots[b, n] (int32, each slot once) holds
+    the state of the beam it continues.  pools: the windows and states of every
+    layer.  Returns (scores, tokens, parents), each (batch, beams)."""
     scores, tokens, parents = beam_select(logits, scores, slots.shape[1])
     src, dst = slots.gather(1, parents.long()).view(-1), slots.reshape(-1)
+    step = MOVE_MAX_MOVES // slots.shape[1] * slots.shape[1]  # whole batch elements: theirs are the only slots they read
     for pool in pools:
-        state_move(pool, src, dst)
+        for i in range(0, src.shape[0], step):
+            state_move(pool, src[i:i + step], dst[i:i + step])
     return scores, tokens, parents
 
 

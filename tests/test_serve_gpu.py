@@ -256,3 +256,17 @@ def test_streams():
     for g in got:
         for a, b in zip(g, want):
             assert torch.equal(a, b)
+
+
+def test_beam_advance_of_many():
+    """More beams than one call of the moves takes: every batch element's slots are its own."""
+    g = torch.Generator().manual_seed(13)
+    batch, beams, V = 700, 3, 40
+    pool = torch.randn(2200, 5, 4, generator=g).cuda()
+    before = pool.clone()
+    slots = torch.randperm(2200, generator=g)[:batch * beams].view(batch, beams).to(torch.int32).cuda()
+    logits, scores = torch.randn(batch, beams, V, generator=g).cuda(), torch.zeros(batch, beams).cuda()
+    _, _, p = block.beam_advance(logits, scores, slots, [pool])
+    ref = before.clone()
+    ref[slots.long().view(-1)] = before[slots.gather(1, p.long()).long().view(-1)]
+    assert torch.equal(pool, ref)
