@@ -362,3 +362,24 @@ def test_neighbours_do_not_meet(dtype, single):
             if s % 2 != bad:
                 assert torch.equal(out[at[s]:at[s + 1]], clean[at[s]:at[s + 1]]), s
                 assert torch.equal(pool[S + s], clean_pool[S + s]), s
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [3, 8, 16, 32, 64])
+@pytest.mark.parametrize("euler", [False, True])
+def test_chained_states_of_every_width(dtype, N, euler):
+    """Sequences over many grid lines that are walked again from their true states, with B and C by rows and by columns,
+    where states hardly decay."""
+    T, D = 1400, 18
+    banner("chained N %d euler %s %s" % (N, euler, dtype))
+    starts = [0, 5, 905, 940, 1400]
+    v = make(87 + N, T, D, N, 6, TYPES[dtype], shift=-6.0, A=-(0.1 + torch.arange(N) / 8).repeat(D, 1))
+    src, dst = [5, 0, -1, 1], [0, 2, 3, 4]
+    src[1] = 1
+    out, pool = run(v, starts, src, dst, euler=euler)
+    compare(out, pool, v, starts, src, dst, euler=euler, dt_min=1e-4, a_min=0.1)
+    by_column = dict(v)
+    for k in ("B", "C"):
+        by_column[k] = v[k].t().contiguous().cuda().t()
+    out2, pool2 = run(by_column, starts, src, dst, euler=euler)
+    assert torch.equal(out2, out) and torch.equal(pool2, pool)
