@@ -357,6 +357,14 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// The state behind a piece: 2^t h + e.  Where A > 0 the product of a piece's decays
+// can pass the largest fp32 next to a state that is zero or small: 2^t in halves, and
+// a zero state stays one (4000 x 128 fp32, 62 lines: 33.8 -> 35.2 us).
+__device__ __forceinline__ float passed(float h, float t, float e) {
+  const float half = __builtin_amdgcn_exp2f(0.5f * t);
+  return h != 0.f ? __builtin_fmaf(half, half * h, e) : e;
+}
+
 // The state at grid line `line` of a sequence that crosses line `first` first:
 // from that line's state on, each piece's end state and the decay over the piece
 // applied to the state before it.  Latency is all there is: several lines are
@@ -380,7 +388,7 @@ __device__ __forceinline__ void enter(const ScanPackedParams& p, const Lane<NS>&
     for (int i = 0; i < kLines; ++i)
       if (l0 + i <= line)
 #pragma unroll
-        for (int k = 0; k < NS; ++k) h[k] = __builtin_fmaf(__builtin_amdgcn_exp2f(ln.A[k] * sum[i]), h[k], e[i][k]);
+        for (int k = 0; k < NS; ++k) h[k] = passed(h[k], ln.A[k] * sum[i], e[i][k]);
   }
 }
 
@@ -564,7 +572,7 @@ __global__ __launch_bounds__(64 * kWaves, NS <= 4 ? 4 : NS == 8 ? 2 : 1) void sc
     const float sum = q.esum[(int64_t)(line - 1) * q.D + dd];
     enter<NS>(q, ln, seq.begin / q.step + 1, line, own, dd, nk, vec, h);
 #pragma unroll
-    for (int k = 0; k < NS; ++k) h[k] = __builtin_fmaf(__builtin_amdgcn_exp2f(ln.A[k] * sum), h[k], e[k]);
+    for (int k = 0; k < NS; ++k) h[k] = passed(h[k], ln.A[k] * sum, e[k]);
   }
   store_block<NS>(q.states + to * q.sts_s + own, nk, vec, h);
 }
@@ -774,9 +782,10 @@ ScanPackedPlan plan_scan_packed(int64_t tokens, int64_t seqs, int64_t dim, int64
   int64_t step = (tokens * waves / (3 * kSimds) + kTile - 1) / kTile * kTile;
   // Where that many waves are not to be had, the rows that a wave walks in either pass
   // (16 in 2.2 us) stand against the lines that it chains a state over: about
-  // sqrt(0.8 tokens) rows a piece.  4000 x 128 fp32: 33.8 us at its 64 rows, 32.8 at 48;
-  // 2000 x 768 bf16: 35.3 at its 48, 38.0 at 32; 500 x 64 bf16: 16.3 at its 16, and 26.7
-  // at 64 (chained four lines at a time).
+  // sqrt(0.8 tokens) rows a piece.  Measured before states were passed on in halves:
+  // 4000 x 128 fp32 33.8 us at its 64 rows, 32.8 at 48; 2000 x 768 bf16 35.3 at its 48,
+  // 38.0 at 32; 500 x 64 bf16 16.3 at its 16, and 26.7 at 64 (chained four lines at a
+  // time).
   step = std::max(step, ((int64_t)std::sqrt(0.8 * (double)tokens) + kTile / 2) / kTile * kTile);
   step = std::max<int64_t>(step, kTile);
   step = std::max<int64_t>(step, ((tokens + 254) / 255 + kTile - 1) / kTile * kTile);  // at most 255 lines

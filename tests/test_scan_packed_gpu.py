@@ -383,3 +383,27 @@ def test_chained_states_of_every_width(dtype, N, euler):
         by_column[k] = v[k].t().contiguous().cuda().t()
     out2, pool2 = run(by_column, starts, src, dst, euler=euler)
     assert torch.equal(out2, out) and torch.equal(pool2, pool)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_growth_from_nothing(dtype):
+    """States that grow (A > 0) and are zero for many pieces, over which the product of the growths passes the largest
+    fp32; then a few steps with inputs.  And a small state that grows by more than that over one piece."""
+    T, D, N = 400, 16, 8
+    v = make(88, T, D, N, 2, TYPES[dtype], z=False, A=torch.full((D, N), 8.0))
+    v["x"][:395] = 0
+    v["delta"] = torch.ones(T, D).to(TYPES[dtype])
+    v["D"] = torch.zeros(D)
+    out, pool = run(v, [0, T], [-1], [1], softplus=False)
+    compare(out, pool, v, [0, T], [-1], [1], softplus=False, dt_min=1.0, a_min=8.0)
+    A = torch.zeros(D, N)
+    v = make(89, 64, D, N, 2, torch.float32, z=False, A=A)
+    v["A"][:] = 6.0
+    v["x"][:] = 0
+    v["delta"] = torch.ones(64, D)
+    v["delta"][16:] = 0
+    v["D"], v["states"] = torch.zeros(D), torch.full((2, D, N), 1e-30)
+    out, pool = run(v, [0, 64], [0], [1], softplus=False)
+    # 16 steps, each factor within (6 + 2) ulp, their exponents' sums exact
+    want = 1e-30 * torch.exp(torch.tensor(96.0, dtype=torch.float64))
+    assert float((pool[1].double().cpu() / want - 1).abs().max()) <= 16 * 8 * ref.U
