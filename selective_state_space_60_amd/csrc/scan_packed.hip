@@ -542,7 +542,8 @@ __global__ __launch_bounds__(64 * kWaves, NS <= 4 ? 4 : NS == 8 ? 2 : 1) void sc
     if constexpr (AGAIN) {
       bool same = true;
 #pragma unroll
-      for (int k = 0; k < NS; ++k) same = same && fabsf(old[k]) <= close * fabsf(h[k]);
+      for (int k = 0; k < NS; ++k)  // (an infinite state, whose old part is infinite too, is never met)
+        same = same && fabsf(old[k]) <= close * fabsf(h[k]) && fabsf(h[k]) < __builtin_inff();
       if (__ballot(!same) == 0) {
         met = left > kTile;
         break;
