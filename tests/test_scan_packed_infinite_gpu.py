@@ -61,3 +61,18 @@ def test_overflow_in_an_earlier_piece(dtype):
     assert not bool(out[over:, 3].isfinite().any()) and not bool(pool[0, 3, 1].isfinite())
     rest = torch.tensor([d for d in range(D) if d != 3])
     assert bool(out[:, rest].isfinite().all()) and bool(pool[0, rest].isfinite().all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("euler", [False, True])
+@pytest.mark.parametrize("N", [4, 16, 40])
+def test_infinite_state_in_a_slot_keeps_its_sign(dtype, euler, N):
+    """No step's decay is zero (exp(-72) at least), so the slot ends as infinite as it began, also where the product of
+    a piece's decays is below the smallest fp32."""
+    banner("infinite slot's end %s euler %s N %d" % (dtype, euler, N))
+    T, D = 1717, 20
+    v = make(202, T, D, N, 4, TYPES[dtype], shift=2.0, A=-(1 + torch.arange(N) * 15 / N).repeat(D, 1))
+    sign = torch.randint(0, 2, (D, N), generator=torch.Generator().manual_seed(1)) * 2 - 1.0
+    v["states"][1] = sign * math.inf
+    _, pool = run(v, [0, 5, T], [0, 1], [2, 3], euler=euler)
+    assert torch.equal(pool[3].cpu(), v["states"][1])
