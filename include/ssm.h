@@ -747,10 +747,9 @@ typedef struct {
  * io is SSM_F32 or SSM_BF16.  Flags: SSM_HAS_Z, SSM_HAS_D, SSM_DISC_EULER,
  * SSM_DELTA_SOFTPLUS, SSM_HAS_DELTA_BIAS, SSM_HAS_STARTS, SSM_HAS_STATES and,
  * with it, SSM_HAS_SRC, SSM_HAS_DST.  dstate <= SSM_SCAN_MAX_DSTATE.
- * (exp(delta A) - 1) / A is good to a few fp32 roundings for single tokens; for
- * sequences, with the largest delta of 16 steps, to 2^-14 of itself where io is F32
- * and 2^-11 where it is BF16 (smaller deltas among larger ones: to that of the
- * largest).  y of a sequence that is walked in pieces is off by up to 2^-16 (BF16 y)
+ * (exp(delta A) - 1) / A is good to a few fp32 roundings, for sequences of BF16 to
+ * 2^-11 of itself (x and B are rounded to 2^-9); a step of delta 0 leaves the state to
+ * the bit.  y of a sequence that is walked in pieces is off by up to 2^-16 (BF16 y)
  * or 2^-20 (F32) of sum |C h| besides; the states are not.
  * Workspace: ssm_selective_scan_packed_workspace_size bytes (may be 0), 256-byte
  * aligned, contents undefined; calls that may overlap in time need workspaces

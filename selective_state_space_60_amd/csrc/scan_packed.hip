@@ -41,13 +41,19 @@
 //
 // Forms, chosen for each tile of a wave (delta A of its steps and channels):
 //   small   all |delta A| < 1/8: expm1(u)/u by its Taylor polynomial; right for A = 0
-//   fast    h <- Abar (h + q) - q, q = B x / A (the update multiplied out), 8 issue
-//           slots a state and step with the readout.  A term u q is off by the
-//           roundings of q, 2^-22 |q|, so it takes that every channel's largest
-//           delta and smallest |A| give |u| >= 2^-11 (bf16: terms are good to
-//           2^-11) or 2^-8 (fp32: to 2^-14)
+//   fast    bf16 only: h <- Abar (h + q) - q, q = B x / A (the update multiplied out), 8
+//           issue slots a state and step with the readout.  A step is off by the
+//           roundings of q, 2^-22 |q|, whatever it adds, so it takes that every step of
+//           every channel has |u| >= 2^-11 (its smallest delta and smallest |A|): then
+//           that is 2^-11 of what the step adds, as its x and B are rounded to 2^-9.  One
+//           step next to zero sends its tile to the last form, and a step of zero
+//           leaves the state to the bit.
 //   any     otherwise, A = 0 among it: (Abar - 1) / A, or the polynomial where
 //           |delta A| < 1/4; 17 issue slots
+// fp32 has no fast form: it would keep its terms to 2^-14 where |u| >= 2^-8, and hardly
+// any tile of common step sizes holds no smaller one (1111 x 1536 in 37 sequences: 51-53
+// us with it, 52-55 without; 38 where the largest step chose the form, and small ones
+// lost up to a percent of the state).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -399,6 +405,7 @@ __device__ __forceinline__ void enter(const ScanPackedParams& p, const Lane<NS>&
 template <bool BF16, int NS, bool EULER, bool AGAIN, bool VEC>
 __global__ __launch_bounds__(64 * kWaves, NS <= 4 ? 4 : NS == 8 ? 2 : 1) void scan_packed_kernel(ScanPackedParams p, unsigned nblk, int vec_state) {
   constexpr int NP = 4 * NS;
+  constexpr bool kMultiplied = BF16 && !EULER;  // kFast is one of the forms
   __shared__ __align__(16) float lds[kWaves][2][kTile][2][NP];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
   const int64_t d0 = ((int64_t)(blockIdx.x % nblk) * kWaves + wave) * kCh;
@@ -476,7 +483,7 @@ __global__ __launch_bounds__(64 * kWaves, NS <= 4 ? 4 : NS == 8 ? 2 : 1) void sc
   int buf = 0;
   for (; left > 0; left -= kTile, buf ^= 1) {
     float x[4], dt[4], xs[4], gate[4];
-    float tmax = 0.f;
+    float tmax = 0.f, tmin = __builtin_inff();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       x[i] = raw2f<BF16>(tile.x[i]);
@@ -502,7 +509,15 @@ __global__ __launch_bounds__(64 * kWaves, NS <= 4 ? 4 : NS == 8 ? 2 : 1) void sc
       xs[i] = EULER ? dt[i] * x[i] : x[i];
       dt[i] *= kLog2e;
       tmax = fmaxf(tmax, fabsf(dt[i]));
+      if constexpr (kMultiplied) tmin = fminf(tmin, fabsf(dt[i]));
       if constexpr (!AGAIN) sum_dt += dt[i];
+    }
+    if constexpr (kMultiplied) {
+      if (left < kTile) {  // uniform; what is past the piece is no step, and changes nothing in any form
+        tmin = __builtin_inff();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmin = 4 * i + j < left ? fminf(tmin, fabsf(dt[i])) : tmin;
+      }
     }
     st.load(left - kTile, tile);
     wave_sync();
@@ -511,11 +526,12 @@ __global__ __launch_bounds__(64 * kWaves, NS <= 4 ? 4 : NS == 8 ? 2 : 1) void sc
     // the four lanes hold different steps
     tmax = fmaxf(tmax, other<1>(tmax));
     tmax = fmaxf(tmax, other<2>(tmax));
-    constexpr float kNear = (BF16 ? 0x1p-11f : 0x1p-8f) * kLog2e;
-    const int form = EULER                                                     ? kEuler
-                     : __ballot(!(tmax * amax < 0.125f * kLog2e)) == 0         ? kSmall
-                     : (__ballot(!(tmax * amin >= kNear)) & alive) == 0        ? kFast
-                                                                               : kAny;
+    int form = EULER ? kEuler : __ballot(!(tmax * amax < 0.125f * kLog2e)) == 0 ? kSmall : kAny;
+    if constexpr (kMultiplied) {
+      tmin = fminf(tmin, other<1>(tmin));
+      tmin = fminf(tmin, other<2>(tmin));
+      if (form == kAny && (__ballot(!(tmin * amin >= 0x1p-11f * kLog2e)) & alive) == 0) form = kFast;
+    }
     if constexpr (EULER) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -526,9 +542,10 @@ __global__ __launch_bounds__(64 * kWaves, NS <= 4 ? 4 : NS == 8 ? 2 : 1) void sc
     } else if (form == kSmall) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) y[i] = four_steps<NS, kSmall, AGAIN>(h, old, ln, dt[i], xs[i], bc + i * 8 * NP);
-    } else if (form == kFast) {
+    } else if (kMultiplied && form == kFast) {
+      constexpr int kForm = kMultiplied ? kFast : kAny;  // (no other variant holds that code)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = four_steps<NS, kFast, AGAIN>(h, old, ln, dt[i], xs[i], bc + i * 8 * NP);
+      for (int i = 0; i < 4; ++i) y[i] = four_steps<NS, kForm, AGAIN>(h, old, ln, dt[i], xs[i], bc + i * 8 * NP);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) y[i] = four_steps<NS, kAny, AGAIN>(h, old, ln, dt[i], xs[i], bc + i * 8 * NP);
