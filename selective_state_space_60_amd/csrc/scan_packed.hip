@@ -46,10 +46,13 @@
 //           roundings of q, 2^-22 |q|, whatever it adds, so it takes that every step of
 //           every channel has |u| >= 2^-11 (its smallest delta and smallest |A|): then
 //           that is 2^-11 of what the step adds, as its x and B are rounded to 2^-9.  One
-//           step next to zero sends its tile to the last form, and a step of zero
+//           step next to zero sends its tile to the next form, and a step of zero
 //           leaves the state to the bit.
-//   any     otherwise, A = 0 among it: (Abar - 1) / A, or the polynomial where
-//           |delta A| < 1/4; 17 issue slots
+//   mixed   bf16 otherwise, A = 0 among it: (Abar - 1) / A, or delta where |delta A| <
+//           2^-11, both to 2^-12; 11 issue slots (16384 x 5120 in 24 sequences with delta
+//           around 10^-3: 1028 us, 1345 in the next form)
+//   any     fp32 otherwise: (Abar - 1) / A, or the polynomial where |delta A| < 1/4; 17
+//           issue slots
 // fp32 has no fast form: it would keep its terms to 2^-14 where |u| >= 2^-8, and hardly
 // any tile of common step sizes holds no smaller one (1111 x 1536 in 37 sequences: 51-53
 // us with it, 52-55 without; 38 where the largest step chose the form, and small ones
@@ -95,7 +98,7 @@ __device__ __forceinline__ float ratio(float t) {
   return __builtin_fmaf(q, t, l1);
 }
 
-enum Form : int { kSmall = 0, kFast = 1, kAny = 2, kEuler = 3 };
+enum Form : int { kSmall = 0, kFast = 1, kAny = 2, kEuler = 3, kMixed = 4 };
 
 // A lane's constants of its states.
 template <int NS>
@@ -120,6 +123,7 @@ __device__ __forceinline__ float step(float (&h)[NS], float (&old)[NS], const La
   for (int k = 0; k < NS; ++k) B[k] = bc[2 * J * NP + k];
 #pragma unroll
   for (int k = 0; k < NS; ++k) q[k] = quad<J>(x) * (FORM == kFast ? ln.iA[k] : B[k]);
+  const float d = quad<J>(dt) * kLn2;  // delta
 #pragma unroll
   for (int k = 0; k < NS; ++k) {
     if constexpr (FORM == kFast) {
@@ -132,6 +136,10 @@ __device__ __forceinline__ float step(float (&h)[NS], float (&old)[NS], const La
       float Ab;
       if constexpr (FORM == kEuler) {
         Ab = __builtin_amdgcn_exp2f(t[k]);
+      } else if constexpr (FORM == kMixed) {
+        Ab = __builtin_amdgcn_exp2f(t[k]);
+        const float far = (Ab - 1.f) * ln.iA[k];  // off by 2^-24 / |u| of itself (A > 0: twice that), delta by |u| / 2
+        q[k] *= fabsf(t[k]) < 0x1p-11f * kLog2e ? d : far;
       } else {
         const float r = ratio(t[k]);
         float c = quad<J>(dt) * r;  // expm1(delta A) / A
@@ -406,6 +414,7 @@ template <bool BF16, int NS, bool EULER, bool AGAIN, bool VEC>
 __global__ __launch_bounds__(64 * kWaves, NS <= 4 ? 4 : NS == 8 ? 2 : 1) void scan_packed_kernel(ScanPackedParams p, unsigned nblk, int vec_state) {
   constexpr int NP = 4 * NS;
   constexpr bool kMultiplied = BF16 && !EULER;  // kFast is one of the forms
+  constexpr int kRest = BF16 ? kMixed : kAny;   // what is left
   __shared__ __align__(16) float lds[kWaves][2][kTile][2][NP];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
   const int64_t d0 = ((int64_t)(blockIdx.x % nblk) * kWaves + wave) * kCh;
@@ -526,11 +535,11 @@ __global__ __launch_bounds__(64 * kWaves, NS <= 4 ? 4 : NS == 8 ? 2 : 1) void sc
     // the four lanes hold different steps
     tmax = fmaxf(tmax, other<1>(tmax));
     tmax = fmaxf(tmax, other<2>(tmax));
-    int form = EULER ? kEuler : __ballot(!(tmax * amax < 0.125f * kLog2e)) == 0 ? kSmall : kAny;
+    int form = EULER ? kEuler : __ballot(!(tmax * amax < 0.125f * kLog2e)) == 0 ? kSmall : kRest;
     if constexpr (kMultiplied) {
       tmin = fminf(tmin, other<1>(tmin));
       tmin = fminf(tmin, other<2>(tmin));
-      if (form == kAny && (__ballot(!(tmin * amin >= 0x1p-11f * kLog2e)) & alive) == 0) form = kFast;
+      if (form == kRest && (__ballot(!(tmin * amin >= 0x1p-11f * kLog2e)) & alive) == 0) form = kFast;
     }
     if constexpr (EULER) {
 #pragma unroll
@@ -548,7 +557,7 @@ __global__ __launch_bounds__(64 * kWaves, NS <= 4 ? 4 : NS == 8 ? 2 : 1) void sc
       for (int i = 0; i < 4; ++i) y[i] = four_steps<NS, kForm, AGAIN>(h, old, ln, dt[i], xs[i], bc + i * 8 * NP);
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = four_steps<NS, kAny, AGAIN>(h, old, ln, dt[i], xs[i], bc + i * 8 * NP);
+      for (int i = 0; i < 4; ++i) y[i] = four_steps<NS, kRest, AGAIN>(h, old, ln, dt[i], xs[i], bc + i * 8 * NP);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[i] = __builtin_fmaf(Dk, x[i], y[i]);
