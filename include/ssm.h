@@ -750,7 +750,8 @@ typedef struct {
  * (exp(delta A) - 1) / A is good to a few fp32 roundings, for sequences of BF16 to
  * 2^-11 of itself (x and B are rounded to 2^-9); a step of delta 0 leaves the state to
  * the bit.  y of a sequence that is walked in pieces is off by up to 2^-16 (BF16 y)
- * or 2^-20 (F32) of sum |C h| besides; the states are not.
+ * or 2^-24 (F32) of sum_n |C m| besides, m the sum of the absolute terms of h (m =
+ * Abar m + |Bbar x|: the same as |h| unless inputs cancel); the states are not.
  * Workspace: ssm_selective_scan_packed_workspace_size bytes (may be 0), 256-byte
  * aligned, contents undefined; calls that may overlap in time need workspaces
  * of their own.

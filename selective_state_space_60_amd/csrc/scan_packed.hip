@@ -26,10 +26,13 @@
 // walks a later piece again from its true state -- chained from the kept ones by
 // each wave for itself -- and carries along what is left of that state, its product
 // with the decays so far, which is what the first pass's states lack.  It stops at
-// the end of the tile where that has come down to 2^-16 of every state where y is
-// bf16 (half a step is 2^-9), 2^-20 where it is fp32 (about what the arithmetic of
-// the walk is good for); it decays on from there.  States that decay are walked
-// again over a short stretch only.  (16384 x 5120 in 24 sequences, all cut at grid
+// the end of the tile where that has come down to 2^-24 of every state where y is
+// fp32 (half a step of the state: the walk itself holds no more of it), 2^-16 where y
+// is bf16 (half a step is 2^-9); it decays on from there, but the state may shrink
+// faster where later inputs cancel it: what y lacks is that part of the sum of its
+// absolute terms, and a caller who needs more of it asks for an fp32 y.  States that
+// decay are walked again over a short stretch only.  (16384 x 5120 bf16 in 24
+// sequences, y bf16: 493 us, 521 with 2^-24; y fp32: 512, 498 with 2^-20.)  (16384 x 5120 in 24 sequences, all cut at grid
 // lines: 126 us walked on until the states equal the first pass's bit for bit, the
 // slowest of a wave's 256 states counts; so 85.)
 //
@@ -485,7 +488,7 @@ __global__ __launch_bounds__(64 * kWaves, NS <= 4 ? 4 : NS == 8 ? 2 : 1) void sc
   };
   float sum_dt = 0.f;
   bool met = false;
-  const float close = p.y_f32 ? 0x1p-20f : 0x1p-16f;
+  const float close = p.y_f32 ? 0x1p-24f : 0x1p-16f;
   int left = run.end - run.begin;
   st.load(left, tile);
   stage(0);
