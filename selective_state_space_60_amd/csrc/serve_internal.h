@@ -9,6 +9,9 @@
 
 namespace ssm {
 
+// Workgroups of 1024 threads that one launch is given at most (it holds fewer than 2^32 threads).
+constexpr int64_t kLaunchBlocks1024 = (int64_t)1 << 21;
+
 // Where packed sequences lie, start and end.
 struct PackedSeqs {
   const int32_t* starts;  // (seqs + 1), or null: one row each

@@ -10,6 +10,8 @@
 // permutation, fork or chain comes out right.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "serve_device.h"
 
 namespace ssm {
@@ -43,11 +45,16 @@ __global__ __launch_bounds__(NT) void move_kernel(MoveParams p) {
     if (to[r] >= 0) *(T*)((char*)p.pool + (int64_t)to[r] * p.slot_bytes + at) = v[r];
 }
 
+// Rows of more slices than one launch may have workgroups take several: no slice meets another.
 template <class T, int L, int R>
-void launch_r(const MoveParams& p, hipStream_t stream) {
-  const int64_t slice = L * (int64_t)sizeof(T);
-  hipLaunchKernelGGL((move_kernel<T, L, R>), dim3((unsigned)((p.row_bytes + slice - 1) / slice)), dim3(NT), 0, stream,
-                     p);
+void launch_r(MoveParams p, hipStream_t stream) {
+  constexpr int64_t slice = L * (int64_t)sizeof(T);
+  while (p.row_bytes > 0) {
+    const int64_t n = std::min((p.row_bytes + slice - 1) / slice, kLaunchBlocks1024);
+    hipLaunchKernelGGL((move_kernel<T, L, R>), dim3((unsigned)n), dim3(NT), 0, stream, p);
+    p.pool = (char*)p.pool + n * slice;
+    p.row_bytes -= n * slice;
+  }
 }
 
 template <class T>
