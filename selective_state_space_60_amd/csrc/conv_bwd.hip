@@ -15,6 +15,8 @@
 // fixed order.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "column_sums.h"
 #include "serve_device.h"
 
@@ -249,12 +251,13 @@ __global__ __launch_bounds__(64 * NW) void conv_bwd_kernel(ConvBwdParams p, unsi
 }
 
 // dweight[d][k], dbias[d] = the parts' sums, in a fixed order.  A workgroup
-// takes 32 of the (W + 1) D columns; 32 threads share a column's parts.
+// takes 32 of the (W + 1) D columns, from column c0 on; 32 threads share a column's
+// parts.
 __global__ __launch_bounds__(1024) void conv_bwd_sum_kernel(const float* part, int64_t parts, int64_t D, int64_t W,
-                                                            float* dweight, float* dbias) {
+                                                            float* dweight, float* dbias, int64_t c0) {
   __shared__ float lds[32][33];
   const int lane = threadIdx.x % 32, run = threadIdx.x / 32;
-  const int64_t c = (int64_t)blockIdx.x * 32 + lane, cols = (W + 1) * D;
+  const int64_t c = c0 + (int64_t)blockIdx.x * 32 + lane, cols = (W + 1) * D;
   float sum = 0.f;
   if (c < cols) {
     if (parts <= 32 * 4) sum = column_run<4>(part + c, run, parts, cols, sum);
@@ -279,8 +282,10 @@ void launch_w(const ConvBwdParams& p, hipStream_t stream) {
   const unsigned nparts = (unsigned)(parts / p.batch);
   hipLaunchKernelGGL((conv_bwd_kernel<BF16, DYF, V, W>), dim3((unsigned)(nchb * parts)), dim3(64 * NW), 0, stream, p,
                      nchb, nparts);
-  hipLaunchKernelGGL(conv_bwd_sum_kernel, dim3((unsigned)(((W + 1) * p.D + 31) / 32)), dim3(1024), 0, stream, p.part,
-                     parts, p.D, p.W, p.dweight, p.dbias);
+  const int64_t groups = ((W + 1) * p.D + 31) / 32;
+  for (int64_t g = 0; g < groups; g += kLaunchBlocks1024)  // one launch up to 64 M columns
+    hipLaunchKernelGGL(conv_bwd_sum_kernel, dim3((unsigned)std::min(groups - g, kLaunchBlocks1024)), dim3(1024), 0,
+                       stream, p.part, parts, p.D, p.W, p.dweight, p.dbias, g * 32);
 }
 
 template <bool BF16, bool DYF, int V>
