@@ -124,7 +124,11 @@ def beam_advance(logits, scores, slots, pools):
     beams) fp32 the `beams` best continuations of every batch element, and the
     pools' slots moved so that beam n's slot slots[b, n] (int32, each slot once) holds
     the state of the beam it continues.  pools: the windows and states of every
-    layer.  Returns (scores, tokens, parents), each (batch, beams)."""
+    layer.  The logits may have fewer beams (one, at the first step), not more.
+    Returns (scores, tokens, parents), each (batch, beams)."""
+    if slots.dim() != 2 or logits.dim() != 3 or logits.shape[0] != slots.shape[0] or logits.shape[1] > slots.shape[1]:
+        raise ValueError("beam_advance: slots are (batch, beams), a slot for every beam of the logits (%s for %s)" %
+                         (tuple(slots.shape), tuple(logits.shape)))
     scores, tokens, parents = beam_select(logits, scores, slots.shape[1])
     src, dst = slots.gather(1, parents.long()).view(-1), slots.reshape(-1)
     step = MOVE_MAX_MOVES // slots.shape[1] * slots.shape[1]  # whole batch elements: theirs are the only slots they read
