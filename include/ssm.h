@@ -821,8 +821,11 @@ typedef struct {
  * continuations the k of the highest score,
  *      s[n,v] = scores[n] + logits[n,v] - log(sum_w exp(logits[n,w])),
  * in falling order, the lower index n vocab + v first where scores are equal.
- * The normaliser is an fp32 sum of up to 4096 tokens at a time, added up in fp64;
- * scores are formed and compared in fp64 and rounded to fp32 once.
+ * The normaliser is an fp32 sum of up to 16384 tokens at a time, added up in fp64, and
+ * good to 2^-17 of itself; scores are formed from it and compared in fp64 and rounded to
+ * fp32 once.  So continuations of different beams whose scores lie within 2^-16 of each
+ * other may change places; those of one beam are in the order of their logits (logits so
+ * close that their scores are equal in fp64: in either order).
  * Banned tokens have the logit -inf.  A beam whose score or normaliser is not a
  * finite number (all tokens banned, a NaN or +inf among the logits, a score of
  * -inf for a beam that is not in use) scores -inf throughout; continuations of

@@ -17,6 +17,11 @@
 // each.  Not kept: candidates taken from the registers by an unrolled loop instead of
 // read again (22 us: a branch for each of the 64 values).
 //
+// The normaliser: a lane adds at most 64 exponentials in fp32, six levels join a wave's
+// lanes, four additions the workgroup's waves: up to 16384 tokens.  The pieces are added
+// up in fp64.  With 17 ulp of the exponentials (arguments down to -32 count) and three of
+// the weights that waves and pieces are joined with, that is within 57 2^-23 of itself.
+//
 // Order: logits are compared as integers that rise with the value (-0 as +0),
 // with the index behind, lower first; scores in fp64, then the index.
 #include <hip/hip_runtime.h>
