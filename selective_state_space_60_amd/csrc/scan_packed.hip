@@ -32,15 +32,16 @@
 // faster where later inputs cancel it: what y lacks is that part of the sum of its
 // absolute terms, and a caller who needs more of it asks for an fp32 y.  States that
 // decay are walked again over a short stretch only.  (16384 x 5120 bf16 in 24
-// sequences, y bf16: 493 us, 521 with 2^-24; y fp32: 512, 498 with 2^-20.)  (16384 x 5120 in 24 sequences, all cut at grid
-// lines: 126 us walked on until the states equal the first pass's bit for bit, the
-// slowest of a wave's 256 states counts; so 85.)
+// sequences, y bf16: 493 us, 521 with 2^-24; y fp32: 512, 498 with 2^-20.)
 //
-// Measured: 16384 x 5120 bf16 in 24 sequences, z, N 16: 486 us (traced from a cold
-// cache: order 5, first pass 460, second 66).  The first pass's VALU issue is 92 %
-// busy at 2.16 GHz: a tile's walk is 484 VALU operations, of which the formula's seven
-// a state and step are 448, and step sizes, gate, loads and stores are 150.  1111 x
-// 1536 fp32 in 37 sequences: 34 us, passes of few tiles each (23 and 15).
+// Measured in a captured graph: 16384 x 5120 bf16 in 24 sequences, z, N 16: 491 us
+// (traced from a cold cache: order 5, first pass 466, second 69).  The first pass's
+// VALU issue is 95 % busy at 2.15 GHz: a tile's walk is 484 VALU operations in the fast
+// form, of which the formula's seven a state and step are 448, and step sizes, forms,
+// gate, loads and stores are 160; 713 in the mixed form, 1090 in the general one.  Where
+// states are forgotten slowly every later piece is walked twice: delta around 7 10^-3
+// 916 us, around 10^-3 1026.  1111 x 1536 fp32 in 37 sequences: 49 us, passes of few
+// tiles each (33 and 21); 16384 x 5120 fp32: 916 us.
 //
 // Forms, chosen for each tile of a wave (delta A of its steps and channels):
 //   small   all |delta A| < 1/8: expm1(u)/u by its Taylor polynomial; right for A = 0
@@ -57,8 +58,8 @@
 //   any     fp32 otherwise: (Abar - 1) / A, or the polynomial where |delta A| < 1/4; 17
 //           issue slots
 // fp32 has no fast form: it would keep its terms to 2^-14 where |u| >= 2^-8, and hardly
-// any tile of common step sizes holds no smaller one (1111 x 1536 in 37 sequences: 51-53
-// us with it, 52-55 without; 38 where the largest step chose the form, and small ones
+// any tile of common step sizes holds no smaller one (1111 x 1536 in 37 sequences, called:
+// 51-53 us with it, 52-55 without; 38 where the largest step chose the form, and small ones
 // lost up to a percent of the state).
 #include <hip/hip_runtime.h>
 
@@ -816,10 +817,10 @@ ScanPackedPlan plan_scan_packed(int64_t tokens, int64_t seqs, int64_t dim, int64
   int64_t step = (tokens * waves / (3 * kSimds) + kTile - 1) / kTile * kTile;
   // Where that many waves are not to be had, the rows that a wave walks in either pass
   // (16 in 2.2 us) stand against the lines that it chains a state over: about
-  // sqrt(0.8 tokens) rows a piece.  Measured before states were passed on in halves:
-  // 4000 x 128 fp32 33.8 us at its 64 rows, 32.8 at 48; 2000 x 768 bf16 35.3 at its 48,
-  // 38.0 at 32; 500 x 64 bf16 16.3 at its 16, and 26.7 at 64 (chained four lines at a
-  // time).
+  // sqrt(0.8 tokens) rows a piece.  Measured before states were passed on in halves and
+  // fp32 lost its fast form: 4000 x 128 fp32 33.8 us at its 64 rows, 32.8 at 48; 2000 x
+  // 768 bf16 35.3 at its 48, 38.0 at 32; 500 x 64 bf16 16.3 at its 16, and 26.7 at 64
+  // (chained four lines at a time).  Now, at the rule's rows: 43.1, 37.8 and 17.6.
   step = std::max(step, ((int64_t)std::sqrt(0.8 * (double)tokens) + kTile / 2) / kTile * kTile);
   step = std::max<int64_t>(step, kTile);
   step = std::max<int64_t>(step, ((tokens + 254) / 255 + kTile - 1) / kTile * kTile);  // at most 255 lines

@@ -6,7 +6,9 @@
 //
 // A workgroup owns a slice of every slot's row and all moves of it: it loads
 // every source's part into registers, waits for all of its threads, and then
-// stores.  Slices do not meet, so no order between workgroups is needed, and any
+// stores.  A thread loads its moves one behind the other, each as its source's number
+// is there (up to 16 of them; many workgroups hide that where rows are wide).  Slices do
+// not meet, so no order between workgroups is needed, and any
 // permutation, fork or chain comes out right.
 #include <hip/hip_runtime.h>
 
